@@ -222,6 +222,107 @@ kvq_status kvq_append_decode(kvq_cache* c, int layer, const void* k, const void*
 kvq_status kvq_decode_attn_noalloc(kvq_cache* c, int layer, const void* q, int q_heads, float sm_scale,
                                    float* out, kvq_stream_t stream);
 
+/* A tensor [batch][n][heads][128] in device memory: element (b, t, h, c) at
+ * data + b stride_b + t stride_t + h stride_h + c, strides in elements, so a
+ * slice of a fused projection or a [batch][heads][n][128] layout is passed
+ * as it is. */
+typedef struct {
+  void* data;
+  long long stride_b, stride_t, stride_h;
+} kvq_rows;
+
+/* ---- rotary positions --------------------------------------------------- */
+
+enum { KVQ_ROPE_HALF = 0, KVQ_ROPE_INTERLEAVED = 1 };
+enum { KVQ_ROPE_NONE = 0, KVQ_ROPE_LINEAR = 1, KVQ_ROPE_NTK = 2, KVQ_ROPE_YARN = 3 };
+enum { KVQ_POS_I32 = 0, KVQ_POS_I64 = 1 };
+
+/* Angles per position of the rot_dim / 2 pairs and the factor on cos and sin,
+ * with d = rot_dim, p = 0 .. d/2 - 1, s = factor:
+ *   KVQ_ROPE_NONE    w_p = theta^(-2p/d), magnitude 1
+ *   KVQ_ROPE_LINEAR  w_p / s (positional interpolation, key design 3)
+ *   KVQ_ROPE_NTK     theta replaced by theta s^(d/(d-2))
+ *   KVQ_ROPE_YARN    w_p ((1 - r_p) + r_p / s): pairs that turn more than 32
+ *     times over original_tokens keep their speed (r = 0), those that turn
+ *     less than once are interpolated (r = 1), r linear in p between (from
+ *     floor to ceil of p(n) = d ln(original_tokens / (2 pi n)) / (2 ln theta)
+ *     at n = 32 and 1); magnitude 0.1 ln s + 1
+ * rot_dim: even, 2 .. 128 (NTK: at least 4).  inv_freq: host double
+ * [rot_dim / 2].  Any other schedule may be filled in by the caller.  Pure
+ * host computation.  Errors: INVALID. */
+kvq_status kvq_rope_freqs(int rot_dim, double theta, int scaling, double factor, int original_tokens,
+                          double* inv_freq, float* magnitude);
+
+/* Turn every pair (x0, x1) of the first rot_dim channels of each head by the
+ * angle positions[b][t] * inv_freq[p] and multiply it by magnitude:
+ *   y0 = (x0 cos - x1 sin) magnitude,  y1 = (x1 cos + x0 sin) magnitude;
+ * the other channels pass unchanged.  Pair p is channels (p, p + rot_dim / 2)
+ * (KVQ_ROPE_HALF) or (2p, 2p + 1) (KVQ_ROPE_INTERLEAVED).  The angle is
+ * reduced exactly, so positions may be any integers; arithmetic is fp32,
+ * rounded once to dtype (KVQ_DTYPE_*).  Keys are turned before kvq_append,
+ * queries before the attention calls, both here in one launch.
+ *
+ * positions: device int32 or int64 (pos_type KVQ_POS_*), at
+ * [b pos_stride_b + t pos_stride_t] (pos_stride_b = 0: the same for every
+ * sequence).  inv_freq: host double [rot_dim / 2], each finite and at most
+ * 2^20 in size, read before the call returns.
+ * q, k: inputs and q_out, k_out: outputs with q_heads and kv_heads heads;
+ * either pair may be NULL with 0 heads.  An output may be its own input (the
+ * same data and strides); other overlaps give unspecified values.  data must
+ * be aligned to an element (interleaved: to a pair, with even strides); 16-byte
+ * aligned rows are the fast case.  batch = 0 or n_tokens = 0 does nothing.
+ * Errors: INVALID, CUDA. */
+kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magnitude, const void* positions,
+                    int pos_type, long long pos_stride_b, long long pos_stride_t, int batch, int n_tokens, int dtype,
+                    const kvq_rows* q, const kvq_rows* q_out, int q_heads, const kvq_rows* k, const kvq_rows* k_out,
+                    int kv_heads, kvq_stream_t stream);
+
+/* ---- attention of a tree of drafted tokens ------------------------------- */
+
+/* Bytes of device workspace kvq_tree_attn needs for this block, number of
+ * query heads and of drafted tokens (any token count).  0 on invalid
+ * arguments. */
+size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_nodes);
+
+/* Attention of n_nodes drafted tokens per sequence over the block's cache and
+ * over one another, in one pass over the packed cache:
+ *   out[b][i][h] = sum_x w_x v_x,  w = softmax over
+ *     every cached token t:              sm_scale (q[b][i][h] * lambda) . k^_t
+ *     every drafted token j seen by i:   sm_scale q[b][i][h] . k[b][j][h']
+ * query head h reading KV head h' = h / (q_heads / kv_heads).  The drafted
+ * Keys and Values are used as given (not quantized) and do not enter the
+ * cache: append the accepted ones with kvq_append afterwards.
+ * mask: device bytes, mask[b mask_stride_b + i n_nodes + j] != 0: node i sees
+ * node j (the diagonal is not implied; mask_stride_b = 0: one mask for every
+ * sequence), or NULL: a chain, i sees j <= i (n_nodes = 1: one decode step
+ * whose token is not yet appended).  A node that sees nothing in an empty
+ * block gets zeros.  What a node does not see never reaches its output,
+ * whatever it holds; drafted values beyond binary16's range and infinities
+ * are read as +-65504, and q lambda sm_scale log2(e) likewise.
+ * q: bf16 [batch][n_nodes][q_heads][128], k, v: dtype KVQ_DTYPE_*
+ * [batch][n_nodes][kv_heads][128], all as kvq_rows with 16-byte aligned rows;
+ * out: device bf16 [batch][n_nodes][q_heads][128], contiguous, 16-byte
+ * aligned.  Scores and sums are fp32; products take operands rounded to
+ * binary16 (the codes are exact at 8 bits and fewer).
+ * 1 <= n_nodes <= 1024; q_heads as in kvq_decode_attn.  workspace: as there,
+ * kvq_tree_workspace(c, layer, q_heads, n_nodes) bytes, 16-byte aligned.
+ * Errors: WORKSPACE, INVALID, CUDA. */
+kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads, int n_nodes, const kvq_rows* k,
+                         const kvq_rows* v, int dtype, const unsigned char* mask, long long mask_stride_b,
+                         float sm_scale, void* out, void* workspace, size_t ws_bytes, kvq_stream_t stream);
+
+/* ---- reading the cache back ---------------------------------------------- */
+
+/* Tokens start .. start + n_tokens - 1 of every sequence (in the order they
+ * were appended) as values: v = Z + q (R / (2^b - 1)) per group, Keys times
+ * lambda (undoing the migration), each step rounded to fp32 and the result
+ * to dtype (KVQ_DTYPE_*).  Sink, window and staged tokens are read at their
+ * 16 bits.  k_out, v_out: [batch][n_tokens][kv_heads][128] with 16-byte aligned
+ * rows; either may be NULL.  n_tokens = 0 does nothing.  Errors: INVALID
+ * (also a range that the block does not hold), CUDA. */
+kvq_status kvq_read(kvq_cache* c, int layer, int start, int n_tokens, int dtype, const kvq_rows* k_out,
+                    const kvq_rows* v_out, kvq_stream_t stream);
+
 /* Host-side state of one block.  Any output pointer may be NULL.
  * capacity: tokens that fit at the current width. */
 kvq_status kvq_query(const kvq_cache* c, int layer, int* tokens, int* bits, int* capacity,

@@ -15,15 +15,17 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from ._lib import (KVQ_DTYPE_BF16, KVQ_DTYPE_F32, KVQ_OPT_KEY_CHANNEL, KVQ_OPT_SINK_WINDOW, KVQ_SHIFT_DIRECT,  # noqa: F401
-                   KVQ_SHIFT_EQUIVALENT, KEY_BLOCK, WINDOW_TOKENS, KVQError, check, load)
+from ._lib import (KVQ_DTYPE_BF16, KVQ_DTYPE_F32, KVQ_POS_I32, KVQ_POS_I64, KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED,  # noqa: F401
+                   KVQ_ROPE_LINEAR, KVQ_ROPE_NONE, KVQ_ROPE_NTK, KVQ_ROPE_YARN, TREE_MAX_NODES, KVQ_OPT_KEY_CHANNEL, KVQ_OPT_SINK_WINDOW, KVQ_SHIFT_DIRECT,  # noqa: F401
+                   KVQ_SHIFT_EQUIVALENT, KEY_BLOCK, Rows, WINDOW_TOKENS, KVQError, check, load)
 
 HEAD_DIM = 128
 
 __all__ = [
-    "KVQCache", "KVQError", "load",
+    "KVQCache", "KVQError", "Rope", "load",
     "kvq_pool_bytes", "kvq_pool_bytes_ex", "kvq_alloc", "kvq_alloc_ex", "kvq_export_window", "kvq_set_lambda", "kvq_append", "kvq_shrink", "kvq_set_shift_mode",
     "kvq_decode_workspace", "kvq_decode_attn", "kvq_decode_attn_noalloc", "kvq_append_decode", "kvq_query", "kvq_max_tokens", "kvq_export",
+    "kvq_rope_freqs", "kvq_rope", "kvq_tree_workspace", "kvq_tree_attn", "kvq_read",
     "kvq_device_status", "kvq_selftest_timeout", "kvq_last_error", "kvq_free", "kvq_allocate_bits",
 ]
 
@@ -155,6 +157,182 @@ def kvq_decode_attn_noalloc(cache, layer: int, q: torch.Tensor, sm_scale: float,
         raise ValueError("q and out must be CUDA tensors")
     check(load().kvq_decode_attn_noalloc(cache, layer, _dptr(q), q.shape[1], float(sm_scale), _dptr(out),
                                          _stream_ptr(stream)))
+
+
+def _rows(t: Optional[torch.Tensor]):
+    """kvq_rows of a [batch][n][heads][128] tensor or view (None: NULL)."""
+    if t is None:
+        return None
+    s = t.stride()
+    return C.byref(Rows(t.data_ptr(), s[0], s[1], s[2]))
+
+
+def _check_rows(name: str, t: torch.Tensor, dtype, shape=None) -> None:
+    if not t.is_cuda or t.dim() != 4 or t.shape[-1] != HEAD_DIM or (t.stride(-1) != 1 and t.numel()):
+        raise ValueError(f"{name} must be a CUDA tensor [batch][n][heads][128] with neighbouring channels")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class _On:
+    """Device guard and launch stream of one call on `device`: the given
+    stream, or the device's current one."""
+
+    def __init__(self, device, stream):
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        self.torch_stream = stream if isinstance(stream, torch.cuda.Stream) else None
+        self.ptr = C.c_void_p(stream.cuda_stream if self.torch_stream is not None else int(stream))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+_SCALINGS = {"none": KVQ_ROPE_NONE, "linear": KVQ_ROPE_LINEAR, "ntk": KVQ_ROPE_NTK, "yarn": KVQ_ROPE_YARN}
+_LAYOUTS = {"half": KVQ_ROPE_HALF, "interleaved": KVQ_ROPE_INTERLEAVED}
+
+
+def kvq_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = KVQ_ROPE_NONE, factor: float = 1.0,
+                   original_tokens: int = 0):
+    """-> (inv_freq [rot_dim / 2] float64 numpy, magnitude)."""
+    inv = np.zeros(max(rot_dim, 2) // 2, np.float64)
+    mag = C.c_float()
+    check(load().kvq_rope_freqs(rot_dim, theta, scaling, factor, original_tokens, inv.ctypes.data_as(C.c_void_p), C.byref(mag)))
+    return inv, mag.value
+
+
+class Rope:
+    """A rotary schedule: which channels form pairs and how fast each turns.
+
+    scaling: "none", "linear" (positional interpolation), "ntk" or "yarn" with
+    `factor` (and `original_tokens` for "yarn"); or inv_freq (and magnitude)
+    of any other schedule."""
+
+    def __init__(self, rot_dim: int = HEAD_DIM, theta: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_tokens: int = 0, inv_freq=None, magnitude: float = 1.0):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+        self.rot_dim, self.layout = int(rot_dim), layout
+        if inv_freq is None:
+            inv_freq, magnitude = kvq_rope_freqs(self.rot_dim, theta, _SCALINGS[scaling], factor, original_tokens)
+        self.inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if self.inv_freq.shape != (self.rot_dim // 2,):
+            raise ValueError(f"inv_freq must hold rot_dim / 2 = {self.rot_dim // 2} values")
+        self.magnitude = float(magnitude)
+        self._code = _LAYOUTS[layout]
+        self._ptr = self.inv_freq.ctypes.data_as(C.c_void_p)
+
+
+def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
+             q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions of q and k (either may be None), in one launch.
+
+    q, k: device [batch][n][heads][128], bf16 or fp32, any strides with
+    neighbouring channels (slices of a fused projection are read in place).
+    positions: device int32 or int64, [batch][n], or [n] for every sequence.
+    q_out, k_out: outputs shaped like q and k (an input itself: in place);
+    allocated contiguous by default.  -> (q_out, k_out)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are both None")
+    if first.dim() != 4:
+        raise ValueError("q and k must be [batch][n][heads][128]")
+    dtype, lead = _dtype_code(first), first.shape[:2]
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out without {name}")
+            continue
+        _check_rows(name, x, first.dtype)
+        if x.shape[:2] != lead or x.device != first.device:
+            raise ValueError("q and k must agree in batch, tokens and device")
+        if y is not None:
+            _check_rows(name + "_out", y, first.dtype, x.shape)
+            if y.device != first.device:
+                raise ValueError("inputs and outputs must be on one device")
+    if positions.dtype not in (torch.int32, torch.int64) or positions.device != first.device:
+        raise ValueError("positions must be an int32 or int64 tensor on the device of q and k")
+    if tuple(positions.shape) == tuple(lead):
+        pb, pt = positions.stride()
+    elif positions.dim() == 1 and positions.shape[0] == lead[1]:
+        pb, pt = 0, positions.stride(0)
+    else:
+        raise ValueError(f"positions must be {list(lead)} or [{lead[1]}], got {list(positions.shape)}")
+    with _On(first.device, stream) as on:
+        if q is not None and q_out is None:
+            q_out = _fresh(q.shape, q.dtype, first.device, on)
+        if k is not None and k_out is None:
+            k_out = _fresh(k.shape, k.dtype, first.device, on)
+        check(load().kvq_rope(rope.rot_dim, rope._code, rope._ptr, rope.magnitude, _dptr(positions),
+                              KVQ_POS_I64 if positions.dtype == torch.int64 else KVQ_POS_I32, pb, pt, lead[0], lead[1], dtype,
+                              _rows(q), _rows(q_out), q.shape[2] if q is not None else 0,
+                              _rows(k), _rows(k_out), k.shape[2] if k is not None else 0, on.ptr))
+    return q_out, k_out
+
+
+def _fresh(shape, dtype, device, on: "_On") -> torch.Tensor:
+    """A new tensor that belongs to the call's stream."""
+    if on.torch_stream is None:  # a raw stream handle: torch knows nothing of it
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(on.torch_stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def kvq_tree_workspace(cache, layer: int, q_heads: int, n_nodes: int) -> int:
+    return load().kvq_tree_workspace(cache, layer, q_heads, n_nodes)
+
+
+def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: Optional[torch.Tensor],
+                  sm_scale: float, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """q: device bf16 [batch][n][q_heads][128]; k, v: device [batch][n][kv_heads][128], bf16 or fp32 (strided views
+    allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
+    shaped like q."""
+    _check_rows("q", q, torch.bfloat16)
+    dtype = _dtype_code(k)
+    b, n = q.shape[:2]
+    _check_rows("k", k, k.dtype, (b, n, k.shape[2], HEAD_DIM))
+    _check_rows("v", v, k.dtype, k.shape)
+    _check_rows("out", out, torch.bfloat16, q.shape)
+    if not out.is_contiguous() or not workspace.is_cuda:
+        raise ValueError("out must be contiguous and workspace a CUDA tensor")
+    mask_b = 0
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8) or not mask.is_cuda or not mask.is_contiguous():
+            raise ValueError("mask must be a contiguous bool or uint8 CUDA tensor")
+        if tuple(mask.shape) == (b, n, n):
+            mask_b = n * n
+        elif tuple(mask.shape) != (n, n):
+            raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(mask.shape)}")
+    ws_bytes = workspace.numel() * workspace.element_size()
+    check(load().kvq_tree_attn(cache, layer, _rows(q), q.shape[2], n, _rows(k), _rows(v), dtype,
+                               _dptr(mask) if mask is not None else None, mask_b, float(sm_scale), _dptr(out),
+                               _dptr(workspace), ws_bytes, _stream_ptr(stream)))
+
+
+def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor],
+             stream=None) -> None:
+    """k_out, v_out: device [batch][count][kv_heads][128], both bf16 or both fp32, any strides with neighbouring
+    channels; either may be None."""
+    first = k_out if k_out is not None else v_out
+    if first is None:
+        raise ValueError("k_out and v_out are both None")
+    for name, x in (("k_out", k_out), ("v_out", v_out)):
+        if x is not None:
+            _check_rows(name, x, first.dtype, first.shape)
+    if first.shape[1] != count:
+        raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
+    check(load().kvq_read(cache, layer, start, count, _dtype_code(first), _rows(k_out), _rows(v_out), _stream_ptr(stream)))
 
 
 def kvq_query(cache, layer: int) -> dict:
@@ -313,6 +491,57 @@ class KVQCache:
             out = torch.empty(q.shape, dtype=torch.float32, device=self.device)
         kvq_append_decode(self.handle, layer, k, v, q, sm_scale, out, self.workspace(layer, q.shape[1]), stream)
         return out
+
+    def tree_attn(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                  sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of n drafted tokens per sequence over the block's cache and over one another.
+
+        q: bf16 [batch][n][q_heads][128]; k, v: the drafted tokens' Keys and Values [batch][n][kv_heads][128], bf16 or
+        fp32; mask: bool or uint8 [batch][n][n] or [n][n], mask[i][j]: node i sees node j (None: a chain, j <= i).
+        -> bf16, shaped like q.  The drafted tokens do not enter the cache."""
+        self._check_batch("q", q, None)
+        self._check_batch("k", k, self.kv_heads)
+        self._check_batch("v", v, self.kv_heads)
+        if mask is not None and mask.device != q.device:
+            raise ValueError("mask must be on the cache's device")
+        if out is not None and out.device != q.device:
+            raise ValueError("out must be on the cache's device")
+        if sm_scale is None:
+            sm_scale = HEAD_DIM ** -0.5
+        with _On(q.device, stream) as on:
+            # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
+            nbytes = kvq_tree_workspace(self.handle, layer, q.shape[2], q.shape[1])
+            if out is None:
+                out = _fresh(q.shape, torch.bfloat16, q.device, on)
+            ws = _fresh(((nbytes + 15) // 16 * 4,), torch.float32, q.device, on)
+            kvq_tree_attn(self.handle, layer, q, k, v, mask, sm_scale, out, ws, on.ptr.value or 0)
+        return out
+
+    def read(self, layer: int, start: int = 0, count: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
+             k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, stream=None):
+        """Tokens start .. start + count - 1 as values in the order they were appended -> (k, v), each
+        [batch][count][kv_heads][128]: what append was given, up to the quantization.  With k_out or v_out only the
+        given ones are written (and returned)."""
+        if count is None:
+            count = self.query(layer)["tokens"] - start
+        if count < 0:
+            raise ValueError(f"count {count} < 0")
+        device = self.pool.device
+        with _On(device, stream) as on:
+            if k_out is None and v_out is None:
+                shape = (self.batch, count, self.kv_heads, HEAD_DIM)
+                k_out, v_out = _fresh(shape, dtype, device, on), _fresh(shape, dtype, device, on)
+            for name, x in (("k_out", k_out), ("v_out", v_out)):
+                if x is not None:
+                    self._check_batch(name, x, self.kv_heads)
+            kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr.value or 0)
+        return k_out, v_out
+
+    def _check_batch(self, name: str, t: torch.Tensor, heads: Optional[int]) -> None:
+        if t.device != self.pool.device:
+            raise ValueError(f"{name} must be on the cache's device {self.pool.device}, got {t.device}")
+        if t.dim() != 4 or t.shape[0] != self.batch or (heads is not None and t.shape[2] != heads):
+            raise ValueError(f"{name} must be [{self.batch}][n][{heads or 'heads'}][128], got {list(t.shape)}")
 
     def query(self, layer: int) -> dict:
         return kvq_query(self.handle, layer)

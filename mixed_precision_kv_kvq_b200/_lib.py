@@ -28,6 +28,15 @@ KVQ_SHIFT_EQUIVALENT = 0
 KVQ_SHIFT_DIRECT = 1
 KVQ_OPT_SINK_WINDOW = 1
 KVQ_OPT_KEY_CHANNEL = 2
+KVQ_ROPE_HALF = 0
+KVQ_ROPE_INTERLEAVED = 1
+KVQ_ROPE_NONE = 0
+KVQ_ROPE_LINEAR = 1
+KVQ_ROPE_NTK = 2
+KVQ_ROPE_YARN = 3
+KVQ_POS_I32 = 0
+KVQ_POS_I64 = 1
+TREE_MAX_NODES = 1024
 KEY_BLOCK = 128
 WINDOW_TOKENS = 128
 
@@ -35,6 +44,9 @@ WINDOW_TOKENS = 128
 P = C.c_void_p
 I = C.c_int
 SZ = C.c_size_t
+LL = C.c_longlong
+F = C.c_float
+D = C.c_double
 SIGNATURES = {
     "kvq_pool_bytes": (SZ, [I, I, I, I, SZ, P]),
     "kvq_pool_bytes_ex": (SZ, [I, I, I, I, SZ, P, I]),
@@ -48,6 +60,11 @@ SIGNATURES = {
     "kvq_decode_attn": (I, [P, I, P, I, C.c_float, P, P, SZ, P]),
     "kvq_decode_attn_noalloc": (I, [P, I, P, I, C.c_float, P, P]),
     "kvq_append_decode": (I, [P, I, P, P, I, P, I, C.c_float, P, P, SZ, P]),
+    "kvq_rope_freqs": (I, [I, D, I, D, I, P, P]),
+    "kvq_rope": (I, [I, I, P, F, P, I, LL, LL, I, I, I, P, P, I, P, P, I, P]),
+    "kvq_tree_workspace": (SZ, [P, I, I, I]),
+    "kvq_tree_attn": (I, [P, I, P, I, I, P, P, I, P, LL, F, P, P, SZ, P]),
+    "kvq_read": (I, [P, I, I, I, I, P, P, P]),
     "kvq_query": (I, [P, I, P, P, P, P]),
     "kvq_max_tokens": (I, [P]),
     "kvq_export": (I, [P, I, I, I, P, P, P, P, P]),
@@ -58,6 +75,12 @@ SIGNATURES = {
     "kvq_last_error": (C.c_char_p, []),
     "kvq_free": (None, [P]),
 }
+
+class Rows(C.Structure):
+    """kvq_rows of include/kvq.h."""
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_longlong), ("stride_t", C.c_longlong),
+                ("stride_h", C.c_longlong)]
+
 
 _lib = None
 

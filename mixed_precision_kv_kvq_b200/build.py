@@ -10,7 +10,8 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libkvq.so"
-SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_shrink.cu", "kvq_decode.cu", "kvq_bitalloc.cu"]
+SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_shrink.cu", "kvq_decode.cu", "kvq_bitalloc.cu", "kvq_rope.cu", "kvq_read.cu",
+           "kvq_tree.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -28,7 +29,7 @@ def _nvcc() -> str:
 
 def build(force: bool = False, verbose: bool = False) -> Path:
     srcs = [CSRC / s for s in SOURCES]
-    deps = srcs + [CSRC / "kvq_internal.cuh", CSRC / "kvq_quant.cuh", CSRC / "kvq_decode_common.cuh", ROOT / "include" / "kvq.h"]
+    deps = srcs + sorted(CSRC.glob("*.cuh")) + [ROOT / "include" / "kvq.h"]
     if not force and LIB.exists() and all(LIB.stat().st_mtime >= d.stat().st_mtime for d in deps):
         return LIB
     tmp = LIB.with_suffix(f".so.{os.getpid()}")

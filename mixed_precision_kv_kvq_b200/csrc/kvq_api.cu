@@ -21,6 +21,8 @@
 
 #include "../../include/kvq.h"
 #include "kvq_internal.cuh"
+#include "kvq_rope.cuh"
+#include "kvq_view.cuh"
 
 using namespace kvq;
 
@@ -864,6 +866,224 @@ kvq_status kvq_decode_attn_noalloc(kvq_cache* c, int layer, const void* q, int q
   // the scratch is fully written before it is read: it needs no clearing
   cudaError_t e = enqueue_decode(c, layer, d, q, q_heads, sm_scale, out, static_cast<float*>(scratch), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
+  return KVQ_OK;
+}
+
+// ---- rotary positions, tree attention, reading back ---------------------------
+
+namespace {
+
+// What the token-wise kernels need to know about one block.
+CacheView view_of(kvq_cache* c, int layer) {
+  const LayerState& L = c->L[layer];
+  CacheView v{};
+  v.codes = c->codes(layer);
+  v.meta = c->meta(layer);
+  v.kmc = L.chan ? c->kmc(layer) : nullptr;
+  v.lam = L.lambda_set ? c->lam(layer) : nullptr;
+  v.lam_inv = L.lambda_set ? c->lam_inv(layer) : nullptr;
+  v.nt = L.nt;
+  v.pf = L.pf;
+  v.bits = L.bits;
+  v.blocks_max = c->blocks_max();
+  v.batch = c->batch;
+  v.kv_heads = c->kv_heads;
+  v.n_prog = L.n;
+  v.n_all = L.window || L.chan ? L.n_all : L.n;
+  v.n_win = (int)(L.chan ? L.n_all - L.n : L.window ? std::min<long long>(L.n_all, kWindowTokens + 1) : 0);
+  if (L.window || L.chan) {
+    v.wcodes = c->wcodes(layer);
+    v.wmeta = c->wmeta(layer);
+  }
+  v.window = L.window;
+  v.ep = make_epochs(L.nt, L.n_shrinks);
+  return v;
+}
+
+// Whether every row of x starts on a multiple of `bytes`.
+bool rows_aligned(const kvq_rows& x, size_t esize, size_t bytes) {
+  return (reinterpret_cast<uintptr_t>(x.data) | (uintptr_t)(x.stride_b * (long long)esize) |
+          (uintptr_t)(x.stride_t * (long long)esize) | (uintptr_t)(x.stride_h * (long long)esize)) %
+             bytes ==
+         0;
+}
+
+}  // namespace
+
+kvq_status kvq_rope_freqs(int rot_dim, double theta, int scaling, double factor, int original_tokens, double* inv_freq,
+                          float* magnitude) {
+  if (rot_dim < 2 || rot_dim > kHeadDim || rot_dim % 2)
+    return fail(KVQ_ERR_INVALID, "rot_dim %d is not an even number in [2, %d]", rot_dim, kHeadDim);
+  if (!inv_freq || !magnitude) return fail(KVQ_ERR_INVALID, "inv_freq or magnitude is NULL");
+  if (!(theta > 1.0) || !std::isfinite(theta)) return fail(KVQ_ERR_INVALID, "theta %g is not finite and > 1", theta);
+  if (scaling < KVQ_ROPE_NONE || scaling > KVQ_ROPE_YARN) return fail(KVQ_ERR_INVALID, "scaling %d unknown", scaling);
+  if (scaling != KVQ_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(KVQ_ERR_INVALID, "factor %g is not finite and >= 1", factor);
+  if (scaling == KVQ_ROPE_NTK && rot_dim < 4) return fail(KVQ_ERR_INVALID, "KVQ_ROPE_NTK needs rot_dim >= 4");
+  if (scaling == KVQ_ROPE_YARN && original_tokens < 1)
+    return fail(KVQ_ERR_INVALID, "original_tokens %d < 1", original_tokens);
+  const double d = rot_dim, pi = 3.14159265358979323846;
+  if (scaling == KVQ_ROPE_NTK) theta *= std::pow(factor, d / (d - 2.0));
+  double low = 0.0, high = 0.0;
+  if (scaling == KVQ_ROPE_YARN) {
+    auto place = [&](double turns) { return d * std::log(original_tokens / (turns * 2.0 * pi)) / (2.0 * std::log(theta)); };
+    low = std::max(std::floor(place(32.0)), 0.0);
+    high = std::min(std::ceil(place(1.0)), d - 1.0);
+  }
+  for (int p = 0; p < rot_dim / 2; p++) {
+    double w = std::pow(theta, -2.0 * p / d);
+    if (scaling == KVQ_ROPE_LINEAR) w /= factor;
+    if (scaling == KVQ_ROPE_YARN) {
+      const double r = std::min(std::max((p - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      w = w / factor * r + w * (1.0 - r);
+    }
+    inv_freq[p] = w;
+  }
+  *magnitude = scaling == KVQ_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return KVQ_OK;
+}
+
+kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magnitude, const void* positions, int pos_type,
+                    long long pos_stride_b, long long pos_stride_t, int batch, int n_tokens, int dtype, const kvq_rows* q,
+                    const kvq_rows* q_out, int q_heads, const kvq_rows* k, const kvq_rows* k_out, int kv_heads,
+                    kvq_stream_t stream) {
+  const Range range("kvq_rope");
+  if (rot_dim < 2 || rot_dim > kHeadDim || rot_dim % 2)
+    return fail(KVQ_ERR_INVALID, "rot_dim %d is not an even number in [2, %d]", rot_dim, kHeadDim);
+  if (layout != KVQ_ROPE_HALF && layout != KVQ_ROPE_INTERLEAVED) return fail(KVQ_ERR_INVALID, "layout %d unknown", layout);
+  if (pos_type != KVQ_POS_I32 && pos_type != KVQ_POS_I64) return fail(KVQ_ERR_INVALID, "pos_type %d unknown", pos_type);
+  if (dtype != KVQ_DTYPE_BF16 && dtype != KVQ_DTYPE_F32) return fail(KVQ_ERR_INVALID, "dtype %d unknown", dtype);
+  if (batch < 0 || n_tokens < 0 || q_heads < 0 || kv_heads < 0 || q_heads > 65535 || kv_heads > 65535)
+    return fail(KVQ_ERR_INVALID, "batch %d, n_tokens %d, q_heads %d or kv_heads %d out of range", batch, n_tokens, q_heads,
+                kv_heads);
+  if (!inv_freq || !std::isfinite(magnitude)) return fail(KVQ_ERR_INVALID, "inv_freq is NULL or magnitude is not finite");
+  RopeArgs a{};
+  for (int p = 0; p < rot_dim / 2; p++) {
+    const double w = inv_freq[p];
+    if (!(std::fabs(w) <= 1048576.0)) return fail(KVQ_ERR_INVALID, "inv_freq[%d] = %g is not within 2^20", p, w);
+    // 2^64 w / (2 pi) modulo 2^64, in 64-bit significands (the whole turns of
+    // a frequency above 2 pi drop out)
+    const long double turns = (long double)w * 0.159154943091895335768883763372514362L;
+    const long double part = turns - floorl(turns);  // [0, 1]
+    const long double scaled = roundl(ldexpl(part, 64));
+    a.turn[p] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
+  }
+  const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
+  const size_t unit = layout == KVQ_ROPE_INTERLEAVED ? 2 * esize : esize;
+  const bool none = batch == 0 || n_tokens == 0 || q_heads + kv_heads == 0;
+  if (none) return KVQ_OK;
+  if (!positions || reinterpret_cast<uintptr_t>(positions) % (pos_type == KVQ_POS_I64 ? 8 : 4))
+    return fail(KVQ_ERR_INVALID, "positions is NULL or not aligned to its type");
+  a.align = 16;
+  auto take = [&](const kvq_rows* in, const kvq_rows* out, int heads, RopeRows& r) {
+    r.heads = heads;
+    if (heads == 0) return true;
+    if (!in || !out || !in->data || !out->data) return false;
+    r = RopeRows{in->data, out->data, heads, in->stride_b, in->stride_t, in->stride_h, out->stride_b, out->stride_t, out->stride_h};
+    while (a.align > 1 && !(rows_aligned(*in, esize, a.align) && rows_aligned(*out, esize, a.align))) a.align /= 2;
+    return true;
+  };
+  if (!take(q, q_out, q_heads, a.q) || !take(k, k_out, kv_heads, a.k)) return fail(KVQ_ERR_INVALID, "q, k or an output is NULL");
+  if ((size_t)a.align < unit)
+    return fail(KVQ_ERR_INVALID, "every row must be aligned to %zu bytes (%s)", unit,
+                layout == KVQ_ROPE_INTERLEAVED ? "a pair" : "an element");
+  a.pos = positions;
+  a.pos64 = pos_type == KVQ_POS_I64;
+  a.pos_b = pos_stride_b;
+  a.pos_t = pos_stride_t;
+  a.n = n_tokens;
+  a.tokens = (long long)batch * n_tokens;
+  a.rot_dim = rot_dim;
+  a.mag = magnitude;
+  a.tokens_per_cta = a.tokens >= 4096 ? 4 : 1;
+  if (cudaError_t e = launch_rope(a, layout == KVQ_ROPE_INTERLEAVED, dtype == KVQ_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)))
+    return cuda_fail(e, "rope launch");
+  return KVQ_OK;
+}
+
+size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_nodes) {
+  if (!c || layer < 0 || layer >= c->layers || q_heads <= 0 || q_heads % c->kv_heads || q_heads / c->kv_heads > 8) return 0;
+  if (n_nodes < 1 || n_nodes > kTreeMaxNodes) return 0;
+  return tree_workspace(const_cast<kvq_cache*>(c)->sms());
+}
+
+kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads, int n_nodes, const kvq_rows* k,
+                         const kvq_rows* v, int dtype, const unsigned char* mask, long long mask_stride_b, float sm_scale,
+                         void* out, void* workspace, size_t ws_bytes, kvq_stream_t stream) {
+  const Range range("kvq_tree_attn");
+  if (kvq_status s = check_layer(c, layer)) return s;
+  if (!q || !k || !v || !q->data || !k->data || !v->data || !out) return fail(KVQ_ERR_INVALID, "q, k, v or out is NULL");
+  if (dtype != KVQ_DTYPE_BF16 && dtype != KVQ_DTYPE_F32) return fail(KVQ_ERR_INVALID, "dtype %d unknown", dtype);
+  if (q_heads <= 0 || q_heads % c->kv_heads)
+    return fail(KVQ_ERR_INVALID, "q_heads %d is not a positive multiple of kv_heads %d", q_heads, c->kv_heads);
+  const int G = q_heads / c->kv_heads;
+  if (G > 8) return fail(KVQ_ERR_INVALID, "%d query heads per KV head; at most 8 are supported", G);
+  if (n_nodes < 1 || n_nodes > kTreeMaxNodes)
+    return fail(KVQ_ERR_INVALID, "n_nodes %d out of range [1, %d]", n_nodes, kTreeMaxNodes);
+  if (!std::isfinite(sm_scale)) return fail(KVQ_ERR_INVALID, "sm_scale is not finite");
+  if (mask_stride_b < 0) return fail(KVQ_ERR_INVALID, "mask_stride_b < 0");
+  const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
+  if (!rows_aligned(*q, 2, 16) || !rows_aligned(*k, esize, 16) || !rows_aligned(*v, esize, 16) ||
+      reinterpret_cast<uintptr_t>(out) % 16)
+    return fail(KVQ_ERR_INVALID, "the rows of q, k and v, and out, must be 16-byte aligned");
+  const size_t need = kvq_tree_workspace(c, layer, q_heads, n_nodes);
+  if (!workspace || ws_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)
+    return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed, 16-byte aligned", workspace ? ws_bytes : (size_t)0, need);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
+  TreeArgs a{};
+  a.c = view_of(c, layer);
+  a.q = q->data;
+  a.k = k->data;
+  a.v = v->data;
+  a.q_b = q->stride_b; a.q_t = q->stride_t; a.q_h = q->stride_h;
+  a.k_b = k->stride_b; a.k_t = k->stride_t; a.k_h = k->stride_h;
+  a.v_b = v->stride_b; a.v_t = v->stride_t; a.v_h = v->stride_h;
+  a.f32 = dtype == KVQ_DTYPE_F32;
+  a.mask = mask;
+  a.mask_b = mask_stride_b;
+  a.n = n_nodes;
+  a.q_heads = q_heads;
+  a.group = G;
+  a.qscale = sm_scale * 1.4426950408889634f;
+  a.out = out;
+  a.err = c->err();
+  a.ws = workspace;
+  a.num_sms = c->sms();
+  if (cudaError_t e = launch_tree(a, s)) return cuda_fail(e, "tree attention launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_read(kvq_cache* c, int layer, int start, int n_tokens, int dtype, const kvq_rows* k_out,
+                    const kvq_rows* v_out, kvq_stream_t stream) {
+  const Range range("kvq_read");
+  if (kvq_status s = check_layer(c, layer)) return s;
+  if (dtype != KVQ_DTYPE_BF16 && dtype != KVQ_DTYPE_F32) return fail(KVQ_ERR_INVALID, "dtype %d unknown", dtype);
+  const LayerState& L = c->L[layer];
+  const long long held = L.window || L.chan ? L.n_all : L.n;
+  if (start < 0 || n_tokens < 0 || (long long)start + n_tokens > held)
+    return fail(KVQ_ERR_INVALID, "tokens [%d, %d + %d) are not within the %lld that layer %d holds", start, start, n_tokens,
+                held, layer);
+  if (n_tokens > 0 && ((k_out && !k_out->data) || (v_out && !v_out->data)))
+    return fail(KVQ_ERR_INVALID, "an output has no data");
+  const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
+  if ((k_out && !rows_aligned(*k_out, esize, 16)) || (v_out && !rows_aligned(*v_out, esize, 16)))
+    return fail(KVQ_ERR_INVALID, "the rows of k_out and v_out must be 16-byte aligned");
+  if (n_tokens == 0 || (!k_out && !v_out)) return KVQ_OK;
+  ReadArgs a{};
+  a.c = view_of(c, layer);
+  a.start = start;
+  a.n = n_tokens;
+  a.f32 = dtype == KVQ_DTYPE_F32;
+  if (k_out) {
+    a.k = k_out->data;
+    a.k_b = k_out->stride_b; a.k_t = k_out->stride_t; a.k_h = k_out->stride_h;
+  }
+  if (v_out) {
+    a.v = v_out->data;
+    a.v_b = v_out->stride_b; a.v_t = v_out->stride_t; a.v_h = v_out->stride_h;
+  }
+  if (cudaError_t e = launch_read(a, reinterpret_cast<cudaStream_t>(stream))) return cuda_fail(e, "read launch");
   return KVQ_OK;
 }
 

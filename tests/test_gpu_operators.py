@@ -1,0 +1,568 @@
+"""Rotary positions, tree attention and reading back on the GPU, against plain
+64-bit forms.
+
+Tolerances.  A rounding to type t is off by at most half a step, u_t =
+finfo(t).eps / 2 relative to the value (bf16 2^-8, fp16 2^-11, fp32 2^-24).
+ * rotary: y = (x0 c - x1 s) mag in fp32: the angle is off by 2 pi 2^-26 rad
+   (and the 64-bit form's own product by angle 2^-53 <= 2.4e-7 at 2^31), c and
+   s by 2 steps (2^-22), three fp32 roundings: below 1e-6 (|x0| + |x1|) mag in
+   all, plus u_t |y|.
+ * read: every step is one IEEE fp32 operation, so fp32 outputs are equal and
+   bf16 outputs are those values rounded.
+ * tree: a score is sum_c q'_c k_c with both factors rounded to fp16, so it is
+   off by at most delta = 2.1 u_fp16 sum_c |q'_c k_c| (plus 0.2e-3 for the fp32
+   sums and the exponential); weights then change by at most e^(2 delta) - 1
+   relative, each p and v is rounded to fp16 once or twice (4 u_fp16), and the
+   output once to bf16: |o - o*| <= u_bf16 |o*| (1 + small) + (e^(2 delta) - 1 +
+   4 u_fp16) sum_t w_t |v_t| + 1e-6."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kvq_synth as S
+
+pytestmark = pytest.mark.gpu
+
+U16, UBF = 2.0 ** -11, 2.0 ** -8
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mixed_precision_kv_kvq_b200 import build
+
+    build.build()
+    import mixed_precision_kv_kvq_b200 as m
+
+    m.load()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(seed, *shape, dtype=BF):
+    return torch.randn(*shape, generator=gen(seed), device="cuda").to(dtype)
+
+
+# ------------------------------------------------------------------ rotary
+
+def rope_exact(rope, pos, x):
+    half = rope.rot_dim // 2
+    inv = torch.tensor(rope.inv_freq, device="cuda")
+    ang = (pos if pos.dim() == 2 else pos.expand(x.shape[0], -1)).double()[:, :, None, None] * inv
+    c, s = ang.cos() * rope.magnitude, ang.sin() * rope.magnitude
+    y = x.double().clone()
+    if rope.layout == "half":
+        i, j = slice(0, half), slice(half, 2 * half)
+    else:
+        i, j = slice(0, 2 * half, 2), slice(1, 2 * half, 2)
+    a, b = x[..., i].double(), x[..., j].double()
+    y[..., i], y[..., j] = a * c - b * s, b * c + a * s
+    size = torch.zeros_like(y)
+    size[..., i] = size[..., j] = (a.abs() + b.abs()) * abs(rope.magnitude)
+    return y, size
+
+
+def rope_check(rope, pos, x, got):
+    y, size = rope_exact(rope, pos, x)
+    tol = torch.finfo(x.dtype).eps / 2 * y.abs() + 1.01e-6 * size
+    assert got.dtype == x.dtype and got.shape == x.shape
+    assert ((got.double() - y).abs() <= tol).all()
+    assert torch.equal(got[..., rope.rot_dim:], x[..., rope.rot_dim:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot", [2, 6, 24, 40, 64, 96, 128])
+def test_rope_layouts_and_parts(kvq, dtype, layout, rot):
+    rope = kvq.Rope(rot, layout=layout)
+    q, k = randn(1, 2, 5, 6, 128, dtype=dtype), randn(2, 2, 5, 2, 128, dtype=dtype)
+    pos = torch.randint(0, 4000, (2, 5), generator=gen(3), device="cuda")
+    qo, ko = kvq.kvq_rope(rope, pos, q, k)
+    rope_check(rope, pos, q, qo)
+    rope_check(rope, pos, k, ko)
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn"])
+@pytest.mark.parametrize("first", [0, 131072, 2 ** 31 - 4100])
+def test_rope_far_positions(kvq, scaling, first):
+    rope = kvq.Rope(128, scaling=scaling, factor=8.0 if scaling != "none" else 1.0, original_tokens=4096)
+    q = randn(4, 1, 4099, 3, 128, dtype=F32)
+    pos = torch.arange(first, first + 4099, device="cuda")[None]
+    qo, ko = kvq.kvq_rope(rope, pos, q)
+    assert ko is None
+    rope_check(rope, pos, q, qo)
+    p32 = pos.to(torch.int32)
+    assert torch.equal(kvq.kvq_rope(rope, p32, q)[0], qo)
+    assert torch.equal(kvq.kvq_rope(rope, p32[0], q)[0], qo)
+
+
+def test_rope_negative_positions_turn_back(kvq):
+    rope = kvq.Rope(128, layout="interleaved")
+    q = randn(5, 2, 7, 4, 128, dtype=F32)
+    pos = torch.randint(0, 100000, (2, 7), generator=gen(6), device="cuda")
+    back = kvq.kvq_rope(rope, -pos, kvq.kvq_rope(rope, pos, q)[0])[0]
+    size = q[..., 0::2].abs() + q[..., 1::2].abs()
+    assert ((back - q).abs() <= 4.1e-6 * size.repeat_interleave(2, -1)).all()  # two turns, each 1e-6 of up to twice the size
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 4, 8])
+def test_rope_strided_views_and_alignment(kvq, offset):
+    """q and k as slices of a fused projection, [b][h][t][d] outputs, rows off 16 bytes."""
+    rope = kvq.Rope(128)
+    flat = randn(7, 3 * 9 * 8 * 128 + offset)
+    qkv = flat[offset:].view(3, 9, 8, 128)
+    q, k = qkv[:, :, :4], qkv[:, :, 4:6]
+    pos = torch.randint(0, 4000, (9, 3), generator=gen(8), device="cuda").t()
+    qo = torch.zeros(3, 4, 9, 128, dtype=BF, device="cuda").transpose(1, 2)
+    ko = torch.zeros(3, 9, 2, 128, dtype=BF, device="cuda")
+    keep = flat.clone()
+    a, b = kvq.kvq_rope(rope, pos, q, k, qo, ko)
+    assert a is qo and b is ko and torch.equal(flat, keep)
+    rope_check(rope, pos, q, qo)
+    rope_check(rope, pos, k, ko)
+    # in place
+    kvq.kvq_rope(rope, pos, q, k, q, k)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    assert torch.equal(qkv[:, :, 6:], keep[offset:].view(3, 9, 8, 128)[:, :, 6:])
+
+
+def test_rope_interleaved_refuses_half_pairs(kvq):
+    x = randn(9, 1 * 2 * 1 * 128 + 1)[1:].view(1, 2, 1, 128)
+    with pytest.raises(kvq.KVQError):
+        kvq.kvq_rope(kvq.Rope(128, layout="interleaved"), torch.zeros(1, 2, dtype=torch.int64, device="cuda"), x)
+
+
+def test_rope_streams_graphs_and_nothing(kvq):
+    rope = kvq.Rope(64)
+    q = randn(10, 2, 3, 4, 128)
+    pos = torch.arange(3, device="cuda")
+    want = kvq.kvq_rope(rope, pos, q)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = kvq.kvq_rope(rope, pos, q, stream=side)[0]
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_rope(rope, pos, q, q_out=out)
+    q.copy_(randn(11, 2, 3, 4, 128))
+    graph.replay()
+    torch.cuda.synchronize()
+    rope_check(rope, pos[None].expand(2, 3), q, out)
+    empty = torch.empty(2, 0, 4, 128, dtype=BF, device="cuda")
+    assert kvq.kvq_rope(rope, torch.empty(0, dtype=torch.int64, device="cuda"), empty)[0].shape == empty.shape
+    none = torch.empty(2, 3, 0, 128, dtype=BF, device="cuda")
+    assert kvq.kvq_rope(rope, pos, none, q)[1].shape == q.shape
+
+
+def test_rope_refusals(kvq):
+    rope = kvq.Rope(128)
+    q = randn(12, 2, 3, 4, 128)
+    pos = torch.arange(3, device="cuda")
+    for bad in (lambda: kvq.kvq_rope(rope, pos.float(), q), lambda: kvq.kvq_rope(rope, pos[:2], q),
+                lambda: kvq.kvq_rope(rope, pos, q, q[:, :2]), lambda: kvq.kvq_rope(rope, pos, q[..., :64]),
+                lambda: kvq.kvq_rope(rope, pos, q, q_out=q[:, :, :2]), lambda: kvq.kvq_rope(rope, pos.cpu(), q),
+                lambda: kvq.kvq_rope(rope, pos, q.transpose(2, 3).contiguous().transpose(2, 3)),
+                lambda: kvq.kvq_rope(rope, pos, q, k_out=q)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: kvq.kvq_rope(rope, pos, q.half()), lambda: kvq.kvq_rope(rope, pos, q, q.float())):
+        with pytest.raises(TypeError):
+            bad()
+
+
+# ------------------------------------------------------ caches of the tests
+
+MODES = ["plain", "window", "channel"]
+
+
+def make_cache(kvq, mode, B, H, T, fbit, n_f, seed=0, lam=True, direct=False, chunk=0):
+    """A cache of T random tokens (Keys with loud channels) and the values it holds, fp32 [B][H][T][128] each, by the
+    codes and meta that export gives (lambda undone)."""
+    per = B * H * 2 * (16 * fbit + 4)
+    cache = kvq.KVQCache(1, B, H, n_f * per, [fbit], sink_window=mode == "window", key_channel=mode == "channel")
+    k, v = S.keys_values(seed, 0, B, max(T, 1), H, 0, 4, dtype=torch.float32)
+    k, v = k[:, :T], v[:, :T]
+    scale = None
+    if lam:
+        scale = (k.abs().amax((0, 1)).sqrt().clamp_min(0.05) if T else torch.ones(H, 128)).float().contiguous()
+        cache.set_lambda(0, scale)
+    if direct:
+        cache.set_shift_mode(0, kvq.KVQ_SHIFT_DIRECT)
+    at = 0
+    while at < T:
+        n = min(chunk or T, T - at)
+        cache.append(0, k[:, at:at + n].contiguous().cuda(), v[:, at:at + n].contiguous().cuda())
+        at += n
+    return (cache, scale) + held(kvq, cache, mode, B, H, T, scale)
+
+
+def half(bits):
+    return bits.view(np.float16).astype(np.float32)
+
+
+def held(kvq, cache, mode, B, H, T, scale):
+    bits = cache.query(0)["bits"]
+    ks, vs = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 128), np.float32)
+
+    def values(codes, r, z, b):
+        return (codes.astype(np.float32) * (r / np.float32(2 ** b - 1)) + z).astype(np.float32)
+
+    for b in range(B):
+        for j in range(H):
+            kc, vc, km, vm = cache.export(0, b, j)
+            n = len(kc)
+            off = 1 if mode == "window" else 0
+            if n:
+                if mode == "channel":
+                    kr = np.repeat(half(km[:, 0]).reshape(-1, 128), 128, 0)
+                    kz = np.repeat(half(km[:, 1]).reshape(-1, 128), 128, 0)
+                else:
+                    kr, kz = half(km[:, 0])[:, None], half(km[:, 1])[:, None]
+                ks[b, j, off:off + n] = values(kc, kr, kz, bits)
+                vs[b, j, off:off + n] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
+            if mode != "plain":
+                kc, vc, km, vm = cache.export_window(0, b, j)
+                m = len(kc)
+                at = list(range(T - m, T)) if mode == "channel" else ([0] + list(range(T - m + 1, T)) if m else [])
+                ks[b, j, at] = values(kc, half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
+                vs[b, j, at] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
+    if scale is not None:
+        ks = ks * scale.numpy()[None, :, None, :]
+    return torch.from_numpy(ks), torch.from_numpy(vs)
+
+
+# ------------------------------------------------------------- reading back
+
+CASES = [("plain", 700, 2, 1024), ("plain", 333, 16, 512), ("plain", 1024, 2, 1024), ("plain", 1500, 4, 1536),
+         ("plain", 1000, 8, 1024), ("plain", 1, 4, 512), ("plain", 17, 2, 512),
+         ("window", 1, 2, 512), ("window", 100, 4, 512), ("window", 129, 2, 512), ("window", 130, 2, 512),
+         ("window", 700, 2, 1024), ("window", 600, 8, 512),
+         ("channel", 100, 2, 1024), ("channel", 128, 4, 1024), ("channel", 1100, 2, 1024), ("channel", 700, 8, 1024)]
+
+
+@pytest.mark.parametrize("mode,T,fbit,n_f", CASES)
+@pytest.mark.parametrize("lam", [True, False])
+def test_read_equals_the_codes(kvq, mode, T, fbit, n_f, lam):
+    cache, _, ks, vs = make_cache(kvq, mode, 2, 3, T, fbit, n_f, lam=lam, direct=T == 700)
+    k, v = cache.read(0, dtype=F32)
+    assert k.shape == (2, T, 3, 128)
+    assert torch.equal(k.cpu().transpose(1, 2), ks) and torch.equal(v.cpu().transpose(1, 2), vs)
+    g = torch.Generator().manual_seed(T)
+    for _ in range(4):
+        a = int(torch.randint(0, T, (1,), generator=g))
+        n = int(torch.randint(1, T - a + 1, (1,), generator=g))
+        k, v = cache.read(0, a, n)
+        assert torch.equal(k.cpu().transpose(1, 2), ks[:, :, a:a + n].bfloat16())
+        assert torch.equal(v.cpu().transpose(1, 2), vs[:, :, a:a + n].bfloat16())
+    assert cache.read(0, T, 0)[0].shape == (2, 0, 3, 128)
+
+
+def test_read_into_views(kvq):
+    """One output only, [b][h][t][d] layout, rows around the range left as they were, another stream, a replayed graph."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, 700, 4, 1024)
+    room = torch.full((2, 2, 40, 128), 7.0, device="cuda")
+    view = room[:, :, 5:30].transpose(1, 2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    k, v = cache.read(0, 300, 25, k_out=view, stream=side)
+    side.synchronize()
+    assert v is None and k is view
+    assert torch.equal(room[:, :, 5:30].cpu(), ks[:, :, 300:325])
+    assert (room[:, :, :5] == 7).all() and (room[:, :, 30:] == 7).all()
+    out = torch.zeros(2, 25, 2, 128, device="cuda", dtype=BF)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.read(0, 300, 25, v_out=out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().transpose(1, 2), vs[:, :, 300:325].bfloat16())
+    for bad in (lambda: cache.read(0, 0, 701), lambda: cache.read(0, -1, 2), lambda: cache.read(1, 0, 1)):
+        with pytest.raises(kvq.KVQError):
+            bad()
+    for bad in (lambda: cache.read(0, 0, 24, v_out=out), lambda: cache.read(0, 0, -1), lambda: cache.read(0, 701),
+                lambda: cache.read(0, 0, 25, v_out=out[:, :, :1])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        cache.read(0, 0, 25, v_out=out.half())
+
+
+def test_read_appended_again_is_stable(kvq):
+    """Reading a 16-bit block and appending it to another gives back the same values up to two 16-bit quantizations."""
+    cache, scale, ks, vs = make_cache(kvq, "plain", 1, 2, 300, 16, 512)
+    k, v = cache.read(0, dtype=F32)
+    other = kvq.KVQCache(1, 1, 2, 512 * 2 * 2 * (16 * 16 + 4), [16])
+    other.set_lambda(0, scale)
+    other.append(0, k, v)
+    k2, v2 = other.read(0, dtype=F32)
+    span = (v.amax(-1) - v.amin(-1))[..., None]
+    # half a 16-bit step, and the binary16 range rounded up by at most 2^-10 of itself
+    assert ((v2 - v).abs() <= 0.6 * span * 1.01 / 65535 + 2.0 ** -22 * v.abs()).all()
+
+
+# --------------------------------------------------------- tree attention
+
+def tree_mask(seed, *lead, n):
+    g = torch.Generator().manual_seed(seed)
+    m = torch.zeros(*lead, n, n, dtype=torch.bool)
+    for i in range(n):
+        for at in np.ndindex(*lead) if lead else [()]:
+            p = int(torch.randint(-1, i, (1,), generator=g)) if i else -1
+            if p >= 0:
+                m[at + (i,)] = m[at + (p,)]
+            m[at + (i, i)] = True
+    return m
+
+
+def tree_check(q, dk, dv, mask, ks, vs, got, sm_scale=128 ** -0.5):
+    """q [B][n][Hq][128], dk, dv [B][n][H][128], ks, vs [B][H][T][128]; mask bool [n][n], [B][n][n] or None."""
+    B, n, Hq, _ = q.shape
+    H = dk.shape[2]
+    G = Hq // H
+    dev = "cuda"
+    seen = torch.ones(n, n, dtype=torch.bool).tril() if mask is None else mask.bool().cpu()
+    seen = seen.expand(B, n, n).to(dev)
+    ks, vs = ks.to(dev).double(), vs.to(dev).double()
+    T = ks.shape[2]
+    bad = torch.full((), -math.inf, dtype=torch.float64, device=dev)
+    for b in range(B):
+        for j in range(H):
+            kk = torch.cat([ks[b, j], dk[b, :, j].double()])
+            vv = torch.cat([vs[b, j], dv[b, :, j].double()])
+            vis = torch.cat([torch.ones(n, T, dtype=torch.bool, device=dev), seen[b]], 1)
+            kk, vv = torch.nan_to_num(kk, 0, 0, 0), torch.nan_to_num(vv, 0, 0, 0)
+            for g in range(G):
+                qq = q[b, :, j * G + g].double()
+                s = torch.where(vis, sm_scale * (qq @ kk.T), bad)
+                size = torch.where(vis, abs(sm_scale) * (qq.abs() @ kk.abs().T), 0.0).amax(1, keepdim=True)
+                w = torch.softmax(s, -1)
+                empty = ~vis.any(1)
+                w[empty] = 0.0
+                o = w @ vv
+                delta = 2.1 * U16 * size + 2e-4
+                tol = UBF * 1.02 * o.abs() + (torch.exp(2 * delta) - 1 + 4 * U16) * (w @ vv.abs()) * 1.02 + 1e-6
+                y = got[b, :, j * G + g].double()
+                assert torch.isfinite(y).all(), (b, j, g)
+                off = (y - o).abs() - tol
+                assert (off <= 0).all(), (b, j, g, float(off.max()), torch.nonzero(off > 0)[:3].tolist())
+                assert (y[empty] == 0).all()
+
+
+def tree_inputs(seed, B, n, H, G, dtype=BF):
+    q = randn(seed, B, n, H * G, 128)
+    dk, dv = randn(seed + 1, B, n, H, 128, dtype=dtype), randn(seed + 2, B, n, H, 128, dtype=dtype)
+    return q, dk, dv
+
+
+@pytest.mark.parametrize("mode,T,fbit,n_f", CASES + [("plain", 0, 4, 512), ("window", 0, 4, 512), ("channel", 0, 4, 1024)])
+@pytest.mark.parametrize("n,G,masked", [(1, 1, False), (3, 7, True), (16, 8, True), (37, 5, False)])
+def test_tree_caches(kvq, mode, T, fbit, n_f, n, G, masked):
+    B, H = 2, 3
+    cache, _, ks, vs = make_cache(kvq, mode, B, H, T, fbit, n_f, lam=n != 3, direct=T == 700)
+    q, dk, dv = tree_inputs(T + n, B, n, H, G, BF if n % 2 else F32)
+    mask = tree_mask(n, B, n=n) if masked else None
+    out = cache.tree_attn(0, q, dk, dv, mask.cuda() if masked else None)
+    assert out.dtype == BF and out.shape == q.shape
+    tree_check(q, dk, dv, mask, ks, vs, out)
+    cache.device_status()
+
+
+@pytest.mark.parametrize("n,G", [(1, 2), (1, 8), (2, 8), (4, 8), (6, 8), (8, 8), (9, 7), (12, 8), (16, 8), (17, 8), (64, 1),
+                                 (65, 1), (128, 1), (129, 2), (257, 1), (300, 5)])
+def test_tree_rows(kvq, n, G):
+    """Every number of query rows around the row blocks' borders, over several splits."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 1, 2, 2900, 4, 4096, lam=True)
+    q, dk, dv = tree_inputs(n, 1, n, 2, G)
+    mask = tree_mask(n, n=n).to(torch.uint8) * 3
+    out = cache.tree_attn(0, q, dk, dv, mask.cuda())
+    tree_check(q, dk, dv, mask, ks, vs, out)
+
+
+@pytest.mark.parametrize("T", [1, 15, 16, 127, 128, 129, 255, 1023, 2047, 2048, 2049, 4095, 4096])
+@pytest.mark.parametrize("fbit", [2, 4])
+def test_tree_lengths(kvq, T, fbit):
+    """Partial groups, tiles that are half full after a shrink, blocks that end inside a tile."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 1, 1, T, fbit, 4096, chunk=999)
+    q, dk, dv = tree_inputs(T, 1, 5, 1, 6)
+    out = cache.tree_attn(0, q, dk, dv)
+    tree_check(q, dk, dv, None, ks, vs, out)
+
+
+def test_tree_long(kvq):
+    """A long context and more streams than one wave; the largest tree."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 3, 5, 20000, 2, 20480)
+    for n in (1, 13):
+        q, dk, dv = tree_inputs(n, 3, n, 5, 7)
+        tree_check(q, dk, dv, None, ks, vs, cache.tree_attn(0, q, dk, dv))
+    cache, _, ks, vs = make_cache(kvq, "plain", 1, 1, 600, 8, 1024)
+    q, dk, dv = tree_inputs(5, 1, 1024, 1, 3)
+    mask = torch.rand(1024, 1024, generator=torch.Generator().manual_seed(1)) < 0.3
+    tree_check(q, dk, dv, mask, ks, vs, cache.tree_attn(0, q, dk, dv, mask.cuda()))
+
+
+def test_tree_growing_scores(kvq):
+    """Scores that rise and fall by hundreds along the context: the running maximum moves many times."""
+    B, H, T = 1, 2, 1500
+    cache = kvq.KVQCache(1, B, H, 2048 * B * H * 2 * (16 * 8 + 4), [8])
+    k = torch.zeros(B, T, H, 128)
+    k[..., 0] = torch.linspace(-30, 40, T)[None, :, None]
+    k[..., 1] = torch.linspace(50, -50, T)[None, :, None]
+    k += 0.1 * torch.randn(B, T, H, 128, generator=torch.Generator().manual_seed(0))
+    v = torch.randn(B, T, H, 128, generator=torch.Generator().manual_seed(1))
+    cache.append(0, k.cuda(), v.cuda())
+    ks, vs = held(kvq, cache, "plain", B, H, T, None)
+    q, dk, dv = tree_inputs(3, B, 6, H, 4)
+    q *= 0.3
+    q[:, 0::3, :, 0] = 60.0
+    q[:, 1::3, :, 1] = -60.0
+    tree_check(q, dk, dv, None, ks, vs, cache.tree_attn(0, q, dk, dv))
+
+
+@pytest.mark.parametrize("T", [0, 300])
+def test_tree_rows_that_see_nothing(kvq, T):
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, T, 4, 512)
+    n = 20
+    q, dk, dv = tree_inputs(9, 2, n, 2, 3)
+    mask = tree_mask(2, 2, n=n)
+    mask[:, 4:9] = False
+    mask[1] = False
+    tree_check(q, dk, dv, mask, ks, vs, cache.tree_attn(0, q, dk, dv, mask.cuda()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0, 200])
+def test_tree_padding_never_leaks(kvq, dtype, T):
+    """Padded nodes hold NaN, infinities and the type's extremes; no other node's output notices."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 1, 2, T, 4, 512)
+    n, real = 14, 9
+    q, dk, dv = tree_inputs(11, 1, n, 2, 5, dtype)
+    mask = torch.zeros(n, n, dtype=torch.bool)
+    mask[:real, :real] = tree_mask(3, n=real)
+    want = cache.tree_attn(0, q, dk, dv, mask.cuda())
+    big = torch.finfo(dtype).max
+    for x in (dk, dv):
+        for i, bad in enumerate((math.nan, math.inf, -math.inf, big, -big)):
+            x[:, real + i] = bad
+    q[:, real:] = math.nan
+    q[:, real + 1] = math.inf
+    got = cache.tree_attn(0, q, dk, dv, mask.cuda())
+    assert torch.equal(got[:, :real], want[:, :real])
+
+
+def test_tree_strided_inputs(kvq):
+    """q, k, v as slices of one projection; an output and a scale of the caller's."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, 500, 2, 512)
+    qkv = randn(13, 2, 6, 3 * 2 + 2 + 2, 128)
+    q, dk, dv = qkv[:, :, :6], qkv[:, :, 6:8], qkv[:, :, 8:]
+    out = torch.zeros(2, 6, 6, 128, dtype=BF, device="cuda")
+    assert cache.tree_attn(0, q, dk, dv, sm_scale=0.2, out=out) is out
+    tree_check(q, dk, dv, None, ks, vs, out, 0.2)
+    tree_check(q, dk, dv, None, ks, vs, cache.tree_attn(0, q, dk, dv, sm_scale=-0.05), -0.05)
+
+
+def test_tree_equals_decode_of_one_token(kvq):
+    """A tree of one node equals appending its token at 16 bits and decoding."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, 300, 16, 512)
+    q, dk, dv = tree_inputs(17, 2, 1, 2, 4)
+    tree = cache.tree_attn(0, q, dk, dv)
+    dec = cache.append_decode(0, dk, dv, q[:, 0].contiguous())
+    assert ((tree[:, 0].float() - dec).abs() <= 2 * UBF * dec.abs() + 0.01 * dec.abs().amax(-1, keepdim=True)).all()
+
+
+def test_tree_streams_and_graphs(kvq):
+    """Two calls at once on two streams, and two captured graphs replayed in turn and together."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, 3000, 2, 4096)
+    a, b = tree_inputs(19, 2, 9, 2, 7), tree_inputs(23, 2, 9, 2, 7)
+    wa, wb = cache.tree_attn(0, *a), cache.tree_attn(0, *b)
+    tree_check(*a, None, ks, vs, wa)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(cache.tree_attn(0, *a, stream=s1), cache.tree_attn(0, *b, stream=s2)) for _ in range(20)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, wa) and torch.equal(y, wb)
+    oa, ob = torch.zeros_like(wa), torch.zeros_like(wb)
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(ga):
+        cache.tree_attn(0, *a, out=oa)
+    with torch.cuda.graph(gb):
+        cache.tree_attn(0, *b, out=ob)
+    for _ in range(5):
+        oa.zero_()
+        ob.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            ga.replay()
+        with torch.cuda.stream(s2):
+            gb.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oa, wa) and torch.equal(ob, wb)
+    cache.device_status()
+
+
+def test_tree_python_refusals(kvq):
+    cache, _, _, _ = make_cache(kvq, "plain", 2, 2, 100, 4, 512)
+    q, dk, dv = tree_inputs(29, 2, 4, 2, 3)
+    m = torch.ones(4, 4, dtype=torch.bool, device="cuda")
+    for bad in (lambda: cache.tree_attn(0, q[:1], dk, dv), lambda: cache.tree_attn(0, q, dk[:, :3], dv),
+                lambda: cache.tree_attn(0, q, dk, dv[:, :, :1]), lambda: cache.tree_attn(0, q, dk, dv, m[:3]),
+                lambda: cache.tree_attn(0, q, dk, dv, m.float()), lambda: cache.tree_attn(0, q, dk, dv, m.cpu()),
+                lambda: cache.tree_attn(0, q, dk, dv, out=q[:, :2]), lambda: cache.tree_attn(0, q.cpu(), dk, dv),
+                lambda: cache.tree_attn(0, q, dk, dv, torch.ones(4, 8, dtype=torch.bool, device="cuda")[:, ::2])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: cache.tree_attn(0, q.float(), dk, dv), lambda: cache.tree_attn(0, q, dk, dv.float()),
+                lambda: cache.tree_attn(0, q, dk.half(), dv.half())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: cache.tree_attn(1, q, dk, dv), lambda: cache.tree_attn(0, q[:, :, :5], dk, dv),
+                lambda: cache.tree_attn(0, q, dk, dv, sm_scale=math.inf)):
+        with pytest.raises((kvq.KVQError, ValueError)):
+            bad()
+
+
+# ---------------------------------------------------------- used together
+
+@pytest.mark.parametrize("mode", MODES)
+def test_draft_verify_commit_read(kvq, mode):
+    """One round of drafting: rotate the projection's q and k, attend the tree over the cache, append the accepted
+    path's Keys and Values, read the cache back; then the same for the next round on the grown cache."""
+    B, H, G, n = 2, 2, 4, 6
+    T = 400
+    cache, scale, ks, vs = make_cache(kvq, mode, B, H, T, 4, 1024)
+    rope = kvq.Rope(128, scaling="linear", factor=2.0)
+    for r in range(3):
+        qkv = randn(31 + r, B, n, H * G + 2 * H, 128)
+        depth = torch.tensor([0, 1, 1, 2, 2, 3], device="cuda")
+        seen = torch.zeros(n, n, dtype=torch.bool)
+        for i, p in enumerate([-1, 0, 0, 1, 2, 3]):
+            if p >= 0:
+                seen[i] = seen[p]
+            seen[i, i] = True
+        q, k = kvq.kvq_rope(rope, T + depth, qkv[:, :, :H * G], qkv[:, :, H * G:H * G + H])
+        rope_check(rope, (T + depth).expand(B, n), qkv[:, :, :H * G], q)
+        v = qkv[:, :, H * G + H:]
+        out = cache.tree_attn(0, q, k, v, seen.cuda())
+        tree_check(q, k, v, seen, ks, vs, out)
+        path = torch.tensor([0, 1, 3, 5], device="cuda")
+        cache.append(0, k[:, path].contiguous(), v[:, path].contiguous())
+        T += 4
+        ks, vs = held(kvq, cache, mode, B, H, T, scale)
+        rk, rv = cache.read(0, T - 4, 4, dtype=F32)
+        assert torch.equal(rk.cpu().transpose(1, 2), ks[:, :, -4:]) and torch.equal(rv.cpu().transpose(1, 2), vs[:, :, -4:])
+        # what was appended comes back within half a step of its width (16 bits in the window and the staged block)
+        x = k[:, path].float() / scale.cuda()
+        bits = cache.query(0)["bits"] if mode == "plain" else 16
+        step = (x.amax(-1) - x.amin(-1)) * 1.002 / (2 ** bits - 1)  # the range is rounded up to binary16
+        worst = ((rk - k[:, path].float()).abs() / scale.cuda()).amax(-1)
+        assert (worst <= 0.5 * step + 2.0 ** -20 * x.abs().amax(-1)).all()

@@ -1004,7 +1004,7 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
 size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_nodes) {
   if (!c || layer < 0 || layer >= c->layers || q_heads <= 0 || q_heads % c->kv_heads || q_heads / c->kv_heads > 8) return 0;
   if (n_nodes < 1 || n_nodes > kTreeMaxNodes) return 0;
-  return tree_workspace(const_cast<kvq_cache*>(c)->sms());
+  return tree_workspace(const_cast<kvq_cache*>(c)->sms(), n_nodes * (q_heads / c->kv_heads));
 }
 
 kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads, int n_nodes, const kvq_rows* k,
@@ -1050,7 +1050,8 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   a.err = c->err();
   a.ws = workspace;
   a.num_sms = c->sms();
-  if (cudaError_t e = launch_tree(a, s)) return cuda_fail(e, "tree attention launch");
+  const LayerState& L = c->L[layer];
+  if (cudaError_t e = launch_tree(a, make_fill(L.bits, L.nt, L.pf, L.n_shrinks, L.n), s)) return cuda_fail(e, "tree attention launch");
   return KVQ_OK;
 }
 

@@ -1,9 +1,52 @@
 // kvq_tree.cu -- attention of a tree of drafted tokens over the packed cache
 // and over one another (kvq_tree_attn).
 //
-// One CTA per (query row, stream): its warps take the cached and the drafted
-// tokens in turn, each lane four channels, with an online softmax per warp;
-// the warps' states are joined at the end.
+// For one (sequence, KV head) stream the n nodes' G query heads are R = n G
+// rows r, and with s the scores in log2 units
+//   s[t][r] = (q_r lambda sm_scale log2 e) . k^_t          (cached token t)
+//   out_r   = sum_t 2^(s[t][r] - m_r) v^_t / sum_t 2^(s[t][r] - m_r),
+// the drafted tokens being further tokens t that a mask hides from some rows.
+//
+// Products on tcgen05, tokens as rows.  A tile is 128 tokens.  Both products
+// take their left operand from tensor memory and a narrow right operand from
+// shared memory, so their cost follows the number of query rows (16, 32 or 64
+// columns a half, below) and not a fixed 128:
+//   S[token][row]   = K[token][channel]   Q[row][channel]^T
+//   O[channel][row] += V[token][channel]^T P[token][row]
+// The cache's lane units are what tcgen05.st takes: lane 4g + t of a warp
+// holds tokens g, g + 8 and four neighbouring channels of each Key quad
+// (16x256b: rows lane / 4 and + 8, two columns a lane), and one channel of two
+// neighbouring tokens in each Value pair (16x128b, one column a lane), so
+// codes are widened in registers and stored once, with no transposition.
+//   Keys go in as val = (c - 2^(b-1)) 2^(1-b), exact in fp16 (rounded to 11
+//   bits at 16-bit codes); with Rk = R 2^(b-1) / (2^b - 1), Zk = Z + Rk the
+//   score is Rk (q' . val) + Zk sum(q'), applied in fp32 by the thread that
+//   owns the token.  Per-channel Key groups and drafted Keys go in as fp16
+//   values (Rk, Zk constant).
+//   Values go in as fp16(v g), g = (1 - 2^-b) / 2: v g = val R/4 + (Z g + R/4),
+//   so R/4 is exact, and nothing in binary16's range overflows.
+// S has a token per tensor-memory lane: a thread owns one token and walks the
+// rows, so a token's range, zero and validity are registers, P is written row
+// by row as the K-slices that an MN-major operand wants (16-byte stores,
+// 128-byte swizzle), and row sums are per-thread partial sums until the end.
+// A running maximum m_r is shared by the 128 threads; it moves only when some
+// score exceeds it by more than 2^8 (one vote per 32 rows), and only then are
+// column maxima formed and O rescaled in tensor memory.
+//
+// Roles (20 warps, one CTA per SM, which holds all 512 tensor-memory columns):
+// two softmax warpgroups, four warps widening Keys, four widening Values, one
+// warp streaming packed tiles with bulk copies, two issuing MMAs.  Each softmax
+// warpgroup with its issuer, its S, P, Q and O forms a half.  With up to 64
+// rows the halves take alternate tiles of the same rows (two independent
+// softmax states, joined at the end); above, each takes 64 of 128 rows of every
+// tile.  K and V tiles are double-buffered in tensor memory.
+//
+// Work split: the (stream, block of rows, tile) units form one line that is cut
+// evenly over the grid; a CTA writes the rows it covers whole, and leaves a
+// partial (max, sum, O) of at most two others in the workspace, which
+// tree_merge_kernel joins.  Every wait is bounded: a wait that gives up raises
+// the cache's error flag and the CTA's abort flag, after which all waits return
+// at once and the loops run out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -13,99 +56,1154 @@
 namespace kvq {
 namespace {
 
-constexpr int kTreeWarps = 8;
+constexpr int kTile = 128;           // tokens per tile
+constexpr int kTileGroups = kTile / kGroupTokens;
+constexpr int kTreeThreads = 640;
+constexpr int kMaxStages = 8;
+constexpr int kHalfRows = 64;        // rows of a half's operands in shared memory
+constexpr int kQBytes = kHalfRows * kHeadDim * 2;  // one half's Q: two 64-channel slabs of [64][128 B]
+constexpr int kPBytes = kTile * 128;               // one half's P: [128 tokens][64 rows] fp16
+constexpr float kUnset = 1e30f;      // -m of a row with no token yet
 
-__device__ __forceinline__ float lo16(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+// Tensor-memory columns.
+constexpr uint32_t kColS = 0, kColO = 128, kColK = 256, kColV = 384;  // + 64 per half or buffer
 
-struct State {
-  float m, l, o[4];
+struct Small {
+  float2 kz[4][kTile];               // (Rk, Zk) of the tokens of tile t, ring of 4
+  float4 col[2][kHalfRows / 2];      // per half, rows 2i and 2i + 1: sum(q') twice, -m twice
+  float alpha[2][kHalfRows];         // factor of the last rescaling
+  float red[2][4][kHalfRows];        // per warp: column maxima, then row sums
+  float2 ml[2][kHalfRows];           // final (m, l)
+  uint32_t seen[4][kTile][4];        // drafted tile t: bit i of word w: the row sees token 32 w + i
+  uint64_t ring_full[kMaxStages], ring_free[kMaxStages];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
+  uint32_t tmem;
+  volatile int abort;
 };
-__device__ __forceinline__ void step(State& st, const float (&q)[4], const float (&k)[4], const float (&v)[4]) {
-  float d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  const float m = fmaxf(st.m, d), f = exp2f(st.m - m), p = exp2f(d - m);
-  st.m = m;
-  st.l = st.l * f + p;
-#pragma unroll
-  for (int i = 0; i < 4; i++) st.o[i] = st.o[i] * f + p * v[i];
+constexpr int kSmallBytes = (sizeof(Small) + 1023) / 1024 * 1024;
+constexpr int kFixedBytes = 2 * kQBytes + 2 * kPBytes + kSmallBytes;
+constexpr int kSmemMax = 227 * 1024 - 1024;  // the base is aligned by hand
+
+struct TreePlan {
+  TreeArgs a;
+  Fill f;               // progressive cache (group order)
+  int part_group, part_valid;  // the one group that may be partial, and its tokens
+  int rows, block_rows, blocks;  // query rows of a stream, rows per block, blocks
+  int tp, tw, td, tiles;         // progressive, window and drafted tiles of a stream
+  int units, grid;
+  int stages, stage_bytes;
+  int rec;              // floats of one partial record
+  float* parts;         // [grid][2][rec]: m[block_rows], l[block_rows], O[block_rows][128]
+};
+
+__host__ __device__ __forceinline__ int cta_begin(int units, int grid, int i) { return (int)((long long)units * i / grid); }
+__host__ __device__ __forceinline__ int cta_of(int units, int grid, int u) {
+  return (int)((((long long)u + 1) * grid - 1) / units);
 }
 
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const TreeArgs a) {
-  const CacheView& c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int s = blockIdx.y, b = s / c.kv_heads, j = s - b * c.kv_heads;
-  const int node = blockIdx.x / a.group, h = j * a.group + blockIdx.x % a.group;
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t + h * a.q_h + 4 * lane;
-  float qd[4], qc[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    qd[i] = __bfloat162float(qp[i]) * a.qscale;
-    qc[i] = qd[i] * (c.lam ? c.lam[j * kHeadDim + 4 * lane + i] : 1.f);
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ bool tree_wait_slow(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+  const unsigned long long t0 = global_ns();
+  for (unsigned it = 0;; it++) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if ((it & 15) == 15 && global_ns() - t0 > kWaitNs) {
+      *abort = 1;
+      atomicExch(err, 1);
+      return false;
+    }
   }
-  State st{-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
-  for (int seg = 0; seg < 2; seg++) {
-    const int n = seg == 0 ? (int)c.n_prog : c.n_win;
-    const int bits = seg == 0 ? c.bits : 16;
-    const float inv = 1.0f / (float)((1u << bits) - 1u);
-    for (int i = warp; i < n; i += kTreeWarps) {
-      const Place pl = seg == 0 ? place_of(c.ep, i) : Place{i / slots_per_tile(16), i % slots_per_tile(16)};
-      const size_t tile = (size_t)s * (seg == 0 ? c.nt : kWindowTiles) + pl.tile;
-      const uint8_t* gb = (seg == 0 ? c.codes : c.wcodes) + tile * kTileBytes + (size_t)(pl.slot >> 4) * group_bytes(bits);
-      const uint32_t* mt = (seg == 0 ? c.meta : c.wmeta) + (tile * (seg == 0 ? c.pf : slots_per_tile(16)) + pl.slot) * 2;
-      float k[4], v[4];
+}
+__device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
+  const uint32_t b = smem_u32(bar);
+  if (!mbar_try(b, parity)) (void)tree_wait_slow(b, parity, err, abort);
+}
+// Also after an abort: what is in flight lands before the CTA ends.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try(smem_u32(bar), parity))
+    if (global_ns() - t0 > kWaitNs) break;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool bar_or(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+// One 128 x N x 16 step: A [128][16] fp16 in tensor memory, B in shared memory.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// Instruction descriptor: fp16 A and B, fp32 D, M = 128; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+// Shared-memory descriptor: 128-byte swizzle, 1024 bytes between the 8-row
+// groups (rows of Q along N, tokens of P along K); one 64-element atom wide.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+
+#define KVQ_R4(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3])
+#define KVQ_R16(r, i) KVQ_R4(r, i), KVQ_R4(r, (i) + 4), KVQ_R4(r, (i) + 8), KVQ_R4(r, (i) + 12)
+#define KVQ_W4(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3])
+#define KVQ_W16(r, i) KVQ_W4(r, i), KVQ_W4(r, (i) + 4), KVQ_W4(r, (i) + 8), KVQ_W4(r, (i) + 12)
+
+// 16 rows x 64 columns (Keys of a group).
+__device__ __forceinline__ void tc_st_16x256_x8(uint32_t t, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_R16(r, 0),
+      KVQ_R16(r, 16), "r"(t)
+      : "memory");
+}
+// 16 rows x 16 columns (16 channels of the Values of two groups).
+__device__ __forceinline__ void tc_st_16x128_x4(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KVQ_R4(r, 0), KVQ_R4(r, 4),
+               "r"(t)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_ld(uint32_t (&r)[N], uint32_t t) {
+  static_assert(N == 16 || N == 32);
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : KVQ_W16(r, 0), KVQ_W16(r, 16)
+        : "r"(t)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : KVQ_W16(r, 0)
+        : "r"(t)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_st(uint32_t t, const uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32);
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_R16(r, 0),
+        KVQ_R16(r, 16), "r"(t)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16(r, 0),
+        "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ float warp_max_f32(float x) {  // one redux
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// --------------------------------------------------------------- widening
+
+__host__ __device__ constexpr uint32_t splat_h(uint32_t h) { return h | (h << 16); }
+// fp16 bits of 2^e (normal)
+__host__ __device__ constexpr uint32_t pow2_h(int e) { return (uint32_t)(15 + e) << 10; }
+__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Codes at bits [E, E + BITS) of both half-words -> (c - 2^(BITS-1)) 2^(1-BITS),
+// exact: the code lands in the mantissa of 2^X (1 + c 2^(E-10)) with
+// X = 11 - E - BITS, i.e. 2^X + c 2^(1-BITS); 2^X + 1 comes off.
+template <int BITS, int E>
+__device__ __forceinline__ uint32_t code_val(uint32_t w) {
+  constexpr int X = 11 - E - BITS;
+  static_assert(X >= 0 && X <= 9, "the code lies in the mantissa");
+  constexpr uint32_t m = ((1u << BITS) - 1u) << E;
+  // -(2^X + 1) in fp16: mantissa bit 10 - X (X = 0: -2)
+  constexpr uint32_t off = X == 0 ? 0xc000u : (0x8000u | pow2_h(X) | (1u << (10 - X)));
+  return hadd2_u(lop_and_or(w, splat_h(m), splat_h(pow2_h(X))), splat_h(off));
+}
+// Two 16-bit codes -> fp16((c - 2^15) 2^-15), rounded once.
+__device__ __forceinline__ uint32_t code_val16(uint32_t w) {
+  const uint32_t hi = lop_and_or(w >> 8, 0x00ff00ffu, splat_h(pow2_h(3)));  // 8 + hi / 128
+  const uint32_t lo = lop_and_or(w, 0x00ff00ffu, splat_h(pow2_h(3)));       // 8 + lo / 128
+  // hi / 128 - 1 - 2^-5 is exact; (8 + lo / 128) 2^-8 adds 2^-5 + lo 2^-15
+  return hfma2_u(lo, splat_h(pow2_h(-8)), hadd2_u(hi, splat_h(0xc884u)));  // - 9.03125
+}
+__device__ __forceinline__ uint32_t sat_h2(float lo, float hi) {
+  return pack_h2(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
+}
+
+// One Key quad position p (channels 16 p + 4 t .. + 3) of token half x: the
+// pairs (members 0, 2) and (members 1, 3).
+template <int BITS>
+__device__ __forceinline__ void key_pairs(const uint32_t (&u)[2 * BITS], int x, int p, uint32_t& a, uint32_t& b) {
+  if constexpr (BITS == 16) {
+    const uint32_t w0 = u[x * 16 + 2 * p], w1 = u[x * 16 + 2 * p + 1];
+    a = code_val16(__byte_perm(w0, w1, 0x5410));
+    b = code_val16(__byte_perm(w0, w1, 0x7632));
+  } else {
+    constexpr int qpw = 8 / BITS;
+    const uint32_t w = u[x * BITS + p / qpw], w8 = w >> 8;
+    switch (p % qpw) {  // a constant after unrolling
+      case 0: a = code_val<BITS, 0>(w); b = code_val<BITS, 0>(w8); break;
+      case 1: if constexpr (qpw > 1) { a = code_val<BITS, BITS>(w); b = code_val<BITS, BITS>(w8); } break;
+      case 2: if constexpr (qpw > 2) { a = code_val<BITS, 2 * BITS>(w); b = code_val<BITS, 2 * BITS>(w8); } break;
+      default: if constexpr (qpw > 2) { a = code_val<BITS, 3 * BITS>(w); b = code_val<BITS, 3 * BITS>(w8); } break;
+    }
+  }
+}
+
+// Keys of one group into 16 tensor-memory rows.  part: the group's Key part;
+// kmc: the block's per-channel (R, Z) words in shared memory, or null.
+template <int BITS>
+__device__ __forceinline__ void widen_keys(const uint8_t* part, const uint32_t* kmc, uint32_t taddr, int lane) {
+  uint32_t u[2 * BITS], r[32];
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int ch = 4 * lane + e;
-        uint32_t km = mt[0];
-        if (seg == 0 && c.kmc) km = c.kmc[((size_t)s * c.blocks_max + i / kKeyBlock) * kHeadDim + ch];
-        k[e] = hi16(km) + (float)key_code(gb, bits, pl.slot & 15, ch) * (lo16(km) * inv);
-        v[e] = hi16(mt[1]) + (float)value_code(gb, bits, pl.slot & 15, ch) * (lo16(mt[1]) * inv);
+  for (int i = 0; i < 2 * BITS; i += 4) {
+    const uint4 w = *(reinterpret_cast<const uint4*>(part + lane * unit_bytes(BITS)) + i / 4);
+    u[i] = w.x; u[i + 1] = w.y; u[i + 2] = w.z; u[i + 3] = w.w;
+  }
+#pragma unroll
+  for (int p = 0; p < 8; p++) {
+#pragma unroll
+    for (int x = 0; x < 2; x++) key_pairs<BITS>(u, x, p, r[4 * p + 2 * x], r[4 * p + 2 * x + 1]);
+    if (kmc) {  // k (1 - 2^-b) / 2 = val R/4 + (Z (1 - 2^-b) / 2 + R/4)
+      constexpr uint32_t g = BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
+      const uint4 w = *reinterpret_cast<const uint4*>(kmc + 16 * p + 4 * (lane & 3));
+      const uint32_t ra = hmul2_u(__byte_perm(w.x, w.z, 0x5410), splat_h(pow2_h(-2)));
+      const uint32_t rb = hmul2_u(__byte_perm(w.y, w.w, 0x5410), splat_h(pow2_h(-2)));
+      const uint32_t za = hfma2_u(__byte_perm(w.x, w.z, 0x7632), splat_h(g), ra);
+      const uint32_t zb = hfma2_u(__byte_perm(w.y, w.w, 0x7632), splat_h(g), rb);
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        r[4 * p + 2 * x] = hfma2_u(r[4 * p + 2 * x], ra, za);
+        r[4 * p + 2 * x + 1] = hfma2_u(r[4 * p + 2 * x + 1], rb, zb);
       }
-      step(st, qc, k, v);
     }
   }
-  for (int i = warp; i < a.n; i += kTreeWarps) {
-    const bool seen = a.mask ? a.mask[b * a.mask_b + (long long)node * a.n + i] != 0 : i <= node;
-    if (!seen) continue;
-    float k[4], v[4];
-    const long long ko = b * a.k_b + i * a.k_t + j * a.k_h + 4 * lane, vo = b * a.v_b + i * a.v_t + j * a.v_h + 4 * lane;
+  tc_st_16x256_x8(taddr, r);
+}
+
+// Values of one group and this warp's 32 channels.  The warp takes the channels
+// of lane units g = 2 w and 2 w + 1 (h = 0, 1): tensor-memory row 16 h + 8 r +
+// g' holds channel 16 g' + 8 r + 2 w + h, so every unit is read by one warp only;
+// lane (g', t) turns pairs 2 g', 2 g' + 1 (r = 0, 1) of unit (2 w + h, t).
+// out[h][2 u + r]: rows g' + 8 r, column 4 u + t of the group's eight.
+// rc, zc: half2 of (R, Z) factors of tokens 2t, 2t + 1 (+ 8 u).
+template <int BITS>
+__device__ __forceinline__ void widen_values(const uint8_t* part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], int w,
+                                             int lane, uint32_t (&out)[2][4]) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-      k[e] = a.f32 ? static_cast<const float*>(a.k)[ko + e] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.k)[ko + e]);
-      v[e] = a.f32 ? static_cast<const float*>(a.v)[vo + e] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[vo + e]);
+  for (int h = 0; h < 2; h++) {
+    const uint32_t* unit = reinterpret_cast<const uint32_t*>(part + (4 * (2 * w + h) + t) * unit_bytes(BITS));
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      uint32_t v0, v1;
+      if constexpr (BITS == 16) {
+        const uint2 x = *reinterpret_cast<const uint2*>(unit + u * 16 + 2 * g);
+        v0 = code_val16(x.x);
+        v1 = code_val16(x.y);
+      } else {
+        constexpr int ppw = 16 / BITS;  // pairs per word
+        const uint32_t x = unit[u * BITS + 2 * g / ppw] >> (2 * BITS * (g % (ppw / 2)));
+        v0 = code_val<BITS, 0>(x);
+        if constexpr (BITS == 8)
+          v1 = code_val<8, 0>(x >> 8);
+        else
+          v1 = code_val<BITS, BITS>(x);
+      }
+      out[h][2 * u] = hfma2_u(v0, rc[u], zc[u]);
+      out[h][2 * u + 1] = hfma2_u(v1, rc[u], zc[u]);
     }
-    step(st, qd, k, v);
   }
-  __shared__ float sm[kTreeWarps], sl[kTreeWarps], so[kTreeWarps][kHeadDim];
-  if (lane == 0) {
-    sm[warp] = st.m;
-    sl[warp] = st.l;
+}
+// Channel of tensor-memory row rho of V and O.
+__device__ __forceinline__ int channel_of(int rho) {
+  return 16 * (rho & 7) + 8 * ((rho >> 3) & 1) + 2 * (rho >> 5) + ((rho >> 4) & 1);
+}
+// (1 - 2^-b) / 2 as fp16 (16 bits: 1/2, off by 2^-16)
+__device__ __forceinline__ uint32_t value_scale_h(int bits) {
+  return bits == 2 ? 0x3600u : bits == 4 ? 0x3780u : bits == 8 ? 0x37f8u : 0x3800u;
+}
+__device__ __forceinline__ float value_scale(int bits) {
+  return bits == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << bits);
+}
+
+// ------------------------------------------------------------------ roles
+
+// One CTA's walk over its share: segments (a stream's block of rows), tiles.
+struct Walk {
+  int u, end;               // units left
+  int s, block, t0, t1;     // current segment
+  __device__ __forceinline__ bool next(const TreePlan& p) {
+    if (u >= end) return false;
+    const int x = u / p.tiles;
+    t0 = u - x * p.tiles;
+    t1 = min(p.tiles, t0 + end - u);
+    s = x / p.blocks;
+    block = x - s * p.blocks;
+    u += t1 - t0;
+    return true;
   }
+};
+
+// Whether token tl (0..127) of tile t exists.
+__device__ __forceinline__ bool token_valid(const TreePlan& p, int t, int tl) {
+  if (t < p.tp) {
+    const long long v = (long long)t * kTileGroups + (tl >> 4);
+    return v < p.f.gps && (v != p.part_group || (tl & 15) < p.part_valid);
+  }
+  if (t < p.tp + p.tw) return (t - p.tp) * kTile + tl < p.a.c.n_win;
+  return (t - p.tp - p.tw) * kTile + tl < p.a.n;
+}
+
+// Producer: packed progressive tiles into the ring.
+__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk) {
+  const CacheView& c = p.a.c;
+  const int bits = c.bits, gb = group_bytes(bits);
+  uint32_t rc = 0;
+  while (wk.next(p)) {
+    const uint8_t* sbase = c.codes + (size_t)wk.s * c.nt * kTileBytes;
+    const uint32_t* mbase = c.meta + (size_t)wk.s * c.nt * c.pf * 2;
+    for (int t = wk.t0; t < min(wk.t1, p.tp); t++, rc++) {
+      const int slot = rc % p.stages;
+      tree_wait(&sm.ring_free[slot], ((rc / p.stages) & 1) ^ 1, p.a.err, &sm.abort);
+      if (sm.abort) goto out;
+      uint8_t* st = ring + (size_t)slot * p.stage_bytes;
+      const uint32_t bar = smem_u32(&sm.ring_full[slot]);
+      const int n = (int)min((long long)kTileGroups, p.f.gps - (long long)t * kTileGroups);
+      mbar_expect_tx(bar, (uint32_t)n * (gb + 128u) + (c.kmc ? 4u * kHeadDim : 0u));
+      for (int g = 0; g < n;) {
+        int tile, grp, run;
+        if (c.kmc) {  // a block in the order of arrival: whole runs of its epochs
+          const Place pl = place_of(c.ep, t * kTile + g * kGroupTokens);
+          tile = pl.tile;
+          grp = pl.slot >> 4;
+          int e = 0;
+          while (e + 1 < c.ep.n && t * kTile + g * kGroupTokens >= c.ep.start[e + 1]) e++;
+          run = min(n - g, (c.ep.h[e] + (1 << c.ep.lg_ee[e]) - pl.slot) >> 4);
+        } else {
+          const GroupLoc loc = locate_group(p.f, (long long)t * kTileGroups + g);
+          tile = loc.tile;
+          grp = loc.grp;
+          run = min(n - g, loc.tile_groups - loc.grp);
+        }
+        bulk_g2s(smem_u32(st + g * gb), sbase + (size_t)tile * kTileBytes + (size_t)grp * gb, (uint32_t)(run * gb), bar);
+        bulk_g2s(smem_u32(st + kTileGroups * gb + g * 128), mbase + ((size_t)tile * c.pf + (size_t)grp * 16) * 2,
+                 (uint32_t)run * 128u, bar);
+        g += run;
+      }
+      if (c.kmc)
+        bulk_g2s(smem_u32(st + kTileGroups * (gb + 128)), c.kmc + ((size_t)wk.s * c.blocks_max + t) * kHeadDim, 4u * kHeadDim,
+                 bar);
+    }
+  }
+out:
+  if (sm.abort)  // copies in flight land before the CTA ends
+    for (uint32_t i = rc > (uint32_t)p.stages ? rc - p.stages : 0; i < rc; i++)
+      drain_wait(&sm.ring_full[i % p.stages], (i / p.stages) & 1);
+}
+
+// Group gi (0..7) of tile t as (code part, meta words): in the ring's stage,
+// or the window's tiles in global memory; null if the group does not exist.
+struct GroupAt {
+  const uint8_t* code;
+  const uint32_t* meta;
+};
+__device__ __forceinline__ GroupAt window_group(const TreePlan& p, int s, int t, int gi) {
+  const int wg = (t - p.tp) * kTileGroups + gi;
+  if (wg * kGroupTokens >= p.a.c.n_win) return GroupAt{nullptr, nullptr};
+  constexpr int kPer = slots_per_tile(16) / kGroupTokens;
+  const size_t tile = (size_t)s * kWindowTiles + wg / kPer;
+  return GroupAt{p.a.c.wcodes + tile * kTileBytes + (size_t)(wg % kPer) * group_bytes(16),
+                 p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
+}
+
+// Drafted Keys: rows g and g + 8 of the group, channels 16 p + 4 t .. + 3, as k / (2 lambda).
+__device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, uint32_t taddr, int lane) {
+  const TreeArgs& a = p.a;
+  const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t r[32];
 #pragma unroll
-  for (int e = 0; e < 4; e++) so[warp][4 * lane + e] = st.o[e];
+  for (int x = 0; x < 2; x++) {
+    const int j = j0 + g + 8 * x;
+    const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 4 * t;
+#pragma unroll
+    for (int q = 0; q < 8; q++) {
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < a.n) {
+        if (a.f32) {
+          k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at + 16 * q));
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q));
+          k = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xffff0000u));
+        }
+      }
+      float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (a.c.lam_inv) l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 16 * q + 4 * t));
+      r[4 * q + 2 * x] = sat_h2(0.5f * k.x * l.x, 0.5f * k.z * l.z);
+      r[4 * q + 2 * x + 1] = sat_h2(0.5f * k.y * l.y, 0.5f * k.w * l.w);
+    }
+  }
+  tc_st_16x256_x8(taddr, r);
+}
+// Drafted Values of a group for this warp's channels (widen_values' layout), times g.
+__device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, float scale, int w, int lane,
+                                             uint32_t (&out)[2][4]) {
+  const TreeArgs& a = p.a;
+  const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int u = 0; u < 2; u++) {
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+      float2 v[2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const int j = j0 + 8 * u + 2 * t + e;
+        const long long at = b * a.v_b + j * a.v_t + h * a.v_h + 16 * g + 8 * r + 2 * w;
+        v[e] = make_float2(0.f, 0.f);
+        if (j < a.n) {
+          if (a.f32) {
+            v[e] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.v) + at));
+          } else {
+            const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.v) + at));
+            v[e] = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+          }
+        }
+      }
+      out[0][2 * u + r] = sat_h2(scale * v[0].x, scale * v[1].x);
+      out[1][2 * u + r] = sat_h2(scale * v[0].y, scale * v[1].y);
+    }
+  }
+}
+
+// Four warps: Keys of every tile into tensor memory, the tokens' (Rk, Zk) and,
+// for drafted tiles, which rows see them.  Warp w: tokens 32 w .. 32 w + 31.
+template <int BITS>
+__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk, int w, int lane) {
+  const CacheView& c = p.a.c;
+  constexpr int gb = group_bytes(BITS);
+  uint32_t ct = 0, rc = 0;
+  while (wk.next(p)) {
+    for (int t = wk.t0; t < wk.t1; t++, ct++) {
+      const int buf = ct & 1;
+      const uint32_t ta = sm.tmem + kColK + 64 * buf + ((uint32_t)(32 * w) << 16);
+      tree_wait(&sm.k_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
+      float2 kz = make_float2(0.f, 0.f);
+      const int tl = 32 * w + lane;
+      if (t < p.tp) {
+        const int slot = rc % p.stages;
+        tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
+        tc_after();
+        const uint8_t* st = ring + (size_t)slot * p.stage_bytes;
+        const uint32_t* meta = reinterpret_cast<const uint32_t*>(st + kTileGroups * gb);
+        const uint32_t* kmc = c.kmc ? reinterpret_cast<const uint32_t*>(st + kTileGroups * (gb + 128)) : nullptr;
+        // groups that do not exist leave what the stage held: those rows of S are not used
+#pragma unroll 1
+        for (int i = 0; i < 2; i++)
+          widen_keys<BITS>(st + (2 * w + i) * gb, kmc, ta + ((uint32_t)(16 * i) << 16), lane);
+        if (c.kmc) {
+          kz = make_float2(1.0f / value_scale(BITS), 0.f);
+        } else {
+          const uint32_t m = meta[2 * tl];
+          const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
+                           ((float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u));
+          kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
+        rc++;
+      } else if (t < p.tp + p.tw) {
+        tc_after();
+#pragma unroll 1
+        for (int i = 0; i < 2; i++) {
+          const GroupAt at = window_group(p, wk.s, t, 2 * w + i);
+          if (at.code) widen_keys<16>(at.code, nullptr, ta + ((uint32_t)(16 * i) << 16), lane);
+        }
+        const GroupAt at = window_group(p, wk.s, t, tl >> 4);
+        if (at.meta) {
+          const uint32_t m = at.meta[2 * (tl & 15)];
+          const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * (32768.0f / 65535.0f);
+          kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
+        }
+      } else {
+        tc_after();
+        const int j0 = (t - p.tp - p.tw) * kTile;
+#pragma unroll 1
+        for (int i = 0; i < 2; i++)
+          if (j0 + 32 * w + 16 * i < p.a.n)
+            draft_keys(p, wk.s, j0 + 32 * w + 16 * i, ta + ((uint32_t)(16 * i) << 16), lane);
+        kz = make_float2(2.f, 0.f);
+        // one word per row: which of the warp's 32 tokens its node sees
+        const int b = wk.s / c.kv_heads, j = j0 + tl;
+        const int r0 = wk.block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
+        for (int node = r0 / p.a.group; node * p.a.group < r1; node++) {
+          bool see = j < p.a.n;
+          if (see) see = p.a.mask ? p.a.mask[b * p.a.mask_b + (long long)node * p.a.n + j] != 0 : j <= node;
+          const uint32_t bitsw = __ballot_sync(0xffffffffu, see);
+          const int row = node * p.a.group + lane - r0;
+          if (lane < p.a.group && row >= 0 && row < r1 - r0) sm.seen[ct & 3][row][w] = bitsw;
+        }
+      }
+      sm.kz[ct & 3][tl] = kz;
+      tc_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[buf]);
+    }
+  }
+}
+
+// Four warps: Values of every tile.  Warp w: the channels of lane units 2 w, 2 w + 1.
+template <int BITS>
+__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk, int w, int lane) {
+  const int t4 = lane & 3;
+  constexpr int gb = group_bytes(BITS);
+  const uint32_t gh = splat_h(value_scale_h(BITS));
+  uint32_t ct = 0, rc = 0;
+  while (wk.next(p)) {
+    for (int t = wk.t0; t < wk.t1; t++, ct++) {
+      const int buf = ct & 1;
+      const uint32_t ta = sm.tmem + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
+      tree_wait(&sm.v_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
+      const bool packed = t < p.tp;
+      const int slot = rc % p.stages;
+      if (packed) tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
+      tc_after();
+      const uint8_t* st = ring + (size_t)slot * p.stage_bytes;
+      const long long v0 = (long long)t * kTileGroups;
+#pragma unroll 1
+      for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
+        uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const int gi = g2 + i;
+          uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};  // tokens that do not exist: zeros (P is zero there too)
+          if (t < p.tp + p.tw) {
+            GroupAt at{nullptr, nullptr};
+            if (packed) {
+              if (v0 + gi < p.f.gps)
+                at = GroupAt{st + gi * gb, reinterpret_cast<const uint32_t*>(st + kTileGroups * gb + gi * 128)};
+            } else {
+              at = window_group(p, wk.s, t, gi);
+            }
+            if (at.code) {
+              uint32_t rcv[2], zcv[2];
+#pragma unroll
+              for (int u = 0; u < 2; u++) {
+                const uint4 m = *reinterpret_cast<const uint4*>(at.meta + 2 * (8 * u + 2 * t4));  // K, V of tokens 2t, 2t + 1
+                uint32_t m0 = m.y, m1 = m.w;
+                if (!token_valid(p, t, 16 * gi + 8 * u + 2 * t4)) m0 = 0u;
+                if (!token_valid(p, t, 16 * gi + 8 * u + 2 * t4 + 1)) m1 = 0u;
+                const uint32_t r2 = __byte_perm(m0, m1, 0x5410), z2 = __byte_perm(m0, m1, 0x7632);
+                if (packed) {  // R g 2^(b-1) / (2^b - 1) = R / 4
+                  rcv[u] = hmul2_u(r2, splat_h(pow2_h(-2)));
+                  zcv[u] = hfma2_u(z2, gh, rcv[u]);
+                } else {  // 16-bit codes beside another width: not exact, so the centre is formed in fp32
+                  const float g = value_scale(BITS), f = g * (32768.0f / 65535.0f);
+                  const float2 rf = __half22float2(*reinterpret_cast<const __half2*>(&r2));
+                  const float2 zf = __half22float2(*reinterpret_cast<const __half2*>(&z2));
+                  rcv[u] = pack_h2(rf.x * f, rf.y * f);
+                  zcv[u] = pack_h2(fmaf(rf.x, f, zf.x * g), fmaf(rf.y, f, zf.y * g));
+                }
+              }
+              if (packed)
+                widen_values<BITS>(at.code + part_bytes(BITS), rcv, zcv, w, lane, out);
+              else
+                widen_values<16>(at.code + part_bytes(16), rcv, zcv, w, lane, out);
+            }
+          } else {
+            const int j0 = (t - p.tp - p.tw) * kTile + 16 * gi;
+            if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale(BITS), w, lane, out);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            o0[4 * i + e] = out[0][e];
+            o1[4 * i + e] = out[1][e];
+          }
+        }
+        tc_st_16x128_x4(ta + 8 * g2, o0);
+        tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
+      }
+      tc_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.v_full[buf]);
+        if (packed) mbar_arrive(&sm.ring_free[slot]);
+      }
+      if (packed) rc++;
+    }
+  }
+}
+
+// One thread per half: the MMAs of the half's tiles.
+template <int COLS, bool DUAL>
+__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t q_smem, uint32_t p_smem, Walk wk, int half) {
+  constexpr uint32_t kDescQk = mma_desc(COLS, false), kDescPv = mma_desc(COLS, true);
+  const uint32_t tm = sm.tmem;
+  uint32_t ct = 0, n = 0, seg = 0;  // tiles of the CTA, tiles of this half, segments with tiles of this half
+  auto pv = [&](uint32_t tile, uint32_t i, bool first) {
+    const int buf = tile & 1;
+    tree_wait(&sm.v_full[buf], (tile >> 1) & 1, p.a.err, &sm.abort);
+    tree_wait(&sm.p_full[half], i & 1, p.a.err, &sm.abort);
+    tc_after();
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      tc_mma(tm + kColO + 64 * half, tm + kColV + 64 * buf + 8 * k, smem_desc(p_smem + 2048 * k), kDescPv, !(first && k == 0));
+    tc_commit(&sm.v_free[buf]);
+    tc_commit(&sm.pv_done[half]);
+  };
+  while (wk.next(p)) {
+    bool any = false;
+    uint32_t prev = 0;
+    bool prev_first = false;
+    for (int t = wk.t0; t < wk.t1; t++, ct++) {
+      const int buf = ct & 1;
+      if (!DUAL && buf != half) continue;
+      if (!any) tree_wait(&sm.q_full[half], seg & 1, p.a.err, &sm.abort);
+      tree_wait(&sm.k_full[buf], (ct >> 1) & 1, p.a.err, &sm.abort);
+      tree_wait(&sm.s_free[half], (n & 1) ^ 1, p.a.err, &sm.abort);
+      tc_after();
+#pragma unroll
+      for (int k = 0; k < 8; k++)
+        tc_mma(tm + kColS + 64 * half, tm + kColK + 64 * buf + 8 * k, smem_desc(q_smem + (k >> 2) * (kQBytes / 2) + 32 * (k & 3)),
+               kDescQk, k > 0);
+      tc_commit(&sm.k_free[buf]);
+      tc_commit(&sm.s_full[half]);
+      if (any) pv(prev, n - 1, prev_first);
+      prev = ct;
+      prev_first = !any;
+      any = true;
+      n++;
+    }
+    if (any) {
+      pv(prev, n - 1, prev_first);
+      seg++;
+    }
+  }
+  tc_commit(&sm.drain[half]);
+  drain_wait(&sm.drain[half], 0);
+}
+
+// A warpgroup: softmax of the half's tiles, and the segment's results.
+template <int COLS, bool DUAL>
+__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8_t* q_smem, uint8_t* p_all, Walk wk, int half,
+                                             int tl) {
+  constexpr int CH = COLS < 32 ? COLS : 32;
+  const TreeArgs& a = p.a;
+  const int w = tl >> 5, lane = tl & 31;
+  const uint32_t lanes = (uint32_t)(32 * w) << 16;
+  const uint32_t ts = sm.tmem + kColS + 64 * half + lanes, to = sm.tmem + kColO + 64 * half + lanes;
+  uint8_t* p_smem = p_all + half * kPBytes;
+  float4* col = sm.col[half];
+  const int id = 1 + half;
+  uint32_t ct = 0, n = 0;
+  const float out_scale = 1.0f / value_scale(a.c.bits);
+  while (wk.next(p)) {
+    const int b = wk.s / a.c.kv_heads, j = wk.s - b * a.c.kv_heads;
+    const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0);
+    const int nr = max(0, min(p.rows, wk.block * p.block_rows + p.block_rows) - r0);  // rows of this half (may exceed COLS in no case)
+    const int first_ct = ct;
+    (void)first_ct;
+    int mine = 0;  // tiles of this half in the segment
+    if (DUAL)
+      mine = wk.t1 - wk.t0;
+    else
+      mine = (int)((wk.t1 - wk.t0 + ((ct & 1) == (uint32_t)half ? 1 : 0)) >> 1);
+    float2 l2[COLS / 2];
+#pragma unroll
+    for (int i = 0; i < COLS / 2; i++) l2[i] = make_float2(0.f, 0.f);
+    if (mine > 0) {
+      // ---- q' = q lambda sm_scale log2(e) as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
+      const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
+                                 : make_float4(1.f, 1.f, 1.f, 1.f);
+#pragma unroll 4
+      for (int r = w; r < COLS; r += 4) {
+        uint2 raw = make_uint2(0u, 0u);
+        if (r < nr) {
+          const int row = r0 + r, node = row / a.group, g = row - node * a.group;
+          raw = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t +
+                                                (long long)(j * a.group + g) * a.q_h + 4 * lane);
+        }
+        const float x0 = __uint_as_float(raw.x << 16) * a.qscale * lam.x, x1 = __uint_as_float(raw.x & 0xffff0000u) * a.qscale * lam.y;
+        const float x2 = __uint_as_float(raw.y << 16) * a.qscale * lam.z, x3 = __uint_as_float(raw.y & 0xffff0000u) * a.qscale * lam.w;
+        const uint32_t h02 = sat_h2(x0, x2), h13 = sat_h2(x1, x3);
+        const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02)), f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
+        float sum = (f02.x + f02.y) + (f13.x + f13.y);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int chunk = (lane & 15) >> 1;
+        *reinterpret_cast<uint2*>(q_smem + half * kQBytes + (lane >> 4) * (kQBytes / 2) + r * 128 + ((chunk ^ (r & 7)) << 4) +
+                                  8 * (lane & 1)) = make_uint2(h02, h13);
+        if (lane == 0) {
+          float* cp = reinterpret_cast<float*>(&col[r >> 1]);
+          cp[r & 1] = sum;
+          cp[2 + (r & 1)] = kUnset;
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[half]);
+      bar_sync(id, 128);
+    }
+    int done = 0;
+    for (int t = wk.t0; t < wk.t1; t++, ct++) {
+      if (!DUAL && (ct & 1) != (uint32_t)half) continue;
+      tree_wait(&sm.s_full[half], n & 1, a.err, &sm.abort);
+      tc_after();
+      const float2 kz = sm.kz[ct & 3][tl];
+      const bool valid = token_valid(p, t, tl);
+      const bool draft = t >= p.tp + p.tw;
+      const uint32_t(*seen)[4] = sm.seen[ct & 3] + (DUAL ? half * kHalfRows : 0);
+#pragma unroll
+      for (int c0 = 0; c0 < COLS; c0 += CH) {
+        uint32_t d[CH];
+        tc_ld(d, ts + c0);
+        float2 x[CH / 2];
+        const float2 rk = splat2(kz.x), zk = splat2(kz.y);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < CH / 2; i++) {
+          const float4 cp = col[c0 / 2 + i];
+          x[i] = fma2(rk, make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])),
+                      fma2(make_float2(cp.x, cp.y), zk, make_float2(cp.z, cp.w)));
+        }
+        // rows that do not see the token
+        uint32_t hide = valid ? 0u : 0xffffffffu;  // bit i: row c0 + i does not see this token
+        if (draft && valid) {
+#pragma unroll
+          for (int i = 0; i < CH; i++) hide |= ((seen[c0 + i][w] >> lane) & 1u) ? 0u : 1u << i;
+        }
+        if (hide) {
+#pragma unroll
+          for (int i = 0; i < CH / 2; i++) {
+            if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
+            if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < CH / 2; i++) mx = fmaxf(mx, fmaxf(x[i].x, x[i].y));
+        if (bar_or(id, 128, mx > kRebase)) {
+          // From the scores themselves (a row's first ones were taken against no
+          // maximum); S and O are read again rather than held beside each other.
+          auto score = [&](int i) {
+            const float4 cp = col[c0 / 2 + i / 2];
+            return (hide >> i & 1u) ? -INFINITY : fmaf(kz.x, __uint_as_float(d[i]), (i & 1 ? cp.y : cp.x) * kz.y);
+          };
+          tc_ld(d, ts + c0);
+          float mine_max = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < CH; i++) {
+            const float m = warp_max_f32(score(i));
+            if (lane == i) mine_max = m;
+          }
+          if (lane < CH) sm.red[half][w][c0 + lane] = mine_max;
+          bar_sync(id, 128);
+          if (tl < CH) {
+            const int c = c0 + tl;
+            float* cp = reinterpret_cast<float*>(&col[c >> 1]) + 2 + (c & 1);
+            const float neg = *cp;
+            float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
+            float f = 0.f;
+            if (neg != kUnset) {
+              m = fmaxf(m, -neg);
+              f = ex2(-neg - m);
+            }
+            sm.alpha[half][c] = f;
+            *cp = m == -INFINITY ? kUnset : -m;  // a row that has seen nothing stays unset
+          }
+          bar_sync(id, 128);
+          if (done > 0) {  // O so far, once the last product is in
+            tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
+            tc_after();
+            tc_ld(d, to + c0);
+#pragma unroll
+            for (int i = 0; i < CH; i++) d[i] = __float_as_uint(__uint_as_float(d[i]) * sm.alpha[half][c0 + i]);
+            tc_st(to + c0, d);
+            tc_wait_st();
+          }
+          tc_ld(d, ts + c0);
+#pragma unroll
+          for (int i = 0; i < CH / 2; i++) {
+            const float4 cp = col[c0 / 2 + i];
+            l2[c0 / 2 + i] = mul2(l2[c0 / 2 + i], make_float2(sm.alpha[half][c0 + 2 * i], sm.alpha[half][c0 + 2 * i + 1]));
+            x[i] = add2(make_float2(score(2 * i), score(2 * i + 1)), make_float2(cp.z, cp.w));
+          }
+        }
+        if (c0 + CH == COLS) {  // S is in registers: the next tile's product may start
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free[half]);
+        }
+        if (c0 == 0 && done > 0) tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);  // P is free again
+#pragma unroll
+        for (int q = 0; q < CH / 8; q++) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float2 pr = make_float2(ex2(x[4 * q + e].x), ex2(x[4 * q + e].y));
+            l2[c0 / 2 + 4 * q + e] = add2(l2[c0 / 2 + 4 * q + e], pr);
+            h[e] = pack_h2(pr.x, pr.y);
+          }
+          *reinterpret_cast<uint4*>(p_smem + tl * 128 + (((c0 / 8 + q) ^ (tl & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_async_smem();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[half]);
+      n++;
+      done++;
+    }
+    // ---- the segment's results ----
+    // row sums: halve the rows a lane carries with every exchange
+    {
+      float v[COLS];
+#pragma unroll
+      for (int i = 0; i < COLS / 2; i++) { v[2 * i] = l2[i].x; v[2 * i + 1] = l2[i].y; }
+      int len = COLS;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        if (len > 1) {
+          len /= 2;
+#pragma unroll
+          for (int i = 0; i < COLS / 2; i++) {
+            if (i < len) {
+              const float keep = (lane & o) ? v[i + len] : v[i], send = (lane & o) ? v[i] : v[i + len];
+              v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+          }
+        } else {
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+      }
+      constexpr int kLeft = COLS >= 32 ? COLS / 32 : 1;
+      const int c = COLS >= 32 ? lane * kLeft : lane / (32 / COLS);
+#pragma unroll
+      for (int i = 0; i < kLeft; i++) sm.red[half][w][c + i] = v[i];
+    }
+    bar_sync(id, 128);
+    if (tl < COLS) {
+      const float* r = &sm.red[half][0][tl];
+      const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
+      const float neg = mine > 0 ? reinterpret_cast<const float*>(&col[tl >> 1])[2 + (tl & 1)] : kUnset;
+      sm.ml[half][tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
+    }
+    if (mine > 0) {
+      tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
+      tc_after();
+    }
+    const bool whole = wk.t0 == 0 && wk.t1 == p.tiles;
+    // this CTA's records: 0 for the segment its share begins in, else 1
+    const int x = wk.s * p.blocks + wk.block, begin = cta_begin(p.units, p.grid, blockIdx.x);
+    float* rec = p.parts + ((size_t)blockIdx.x * 2 + (x * p.tiles + wk.t0 == begin ? 0 : 1)) * p.rec;
+    __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(a.out);
+    auto row_at = [&](int r) {  // output row of row r of this half
+      const int row = r0 + r, node = row / a.group, g = row - node * a.group;
+      return outp + (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim;
+    };
+    // rows of bf16 leave from shared memory, 16 bytes a thread
+    auto flush = [&](const uint8_t* sh, int c0, int cnt) {
+      for (int i = tl; i < cnt * 16; i += 128) {
+        const int r = i >> 4, q = i & 15;
+        if (c0 + r < nr) reinterpret_cast<uint4*>(row_at(c0 + r))[q] = *reinterpret_cast<const uint4*>(sh + r * 256 + 16 * q);
+      }
+    };
+    const int ch = channel_of(tl);
+    if constexpr (DUAL) {
+      bar_sync(id, 128);  // ml
+#pragma unroll 1
+      for (int c0 = 0; c0 < COLS; c0 += CH) {
+        uint32_t o[CH];
+        tc_ld(o, to + c0);
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < CH; i++) {
+            const float l = sm.ml[half][c0 + i].y;
+            reinterpret_cast<__nv_bfloat16*>(p_smem)[(c0 + i) * kHeadDim + ch] =
+                __float2bfloat16_rn(l != 0.f ? __uint_as_float(o[i]) * out_scale / l : 0.f);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CH; i++)
+            if (c0 + i < nr) rec[2 * p.block_rows + (half * kHalfRows + c0 + i) * kHeadDim + tl] = __uint_as_float(o[i]);
+        }
+      }
+      tc_before();
+      if (whole) {
+        bar_sync(id, 128);
+        flush(p_smem, 0, COLS);
+        bar_sync(id, 128);  // P is written again
+      } else if (tl < nr) {
+        rec[half * kHalfRows + tl] = sm.ml[half][tl].x;
+        rec[p.block_rows + half * kHalfRows + tl] = sm.ml[half][tl].y;
+      }
+    } else {
+      // join the halves: half 1 hands its O over in shared memory (both P areas: [COLS][128] fp32)
+      bar_sync(3, 256);  // ml of both; every product of both halves is in
+      float* xb = reinterpret_cast<float*>(p_all);
+      auto joint = [&](int c, float& f0, float& f1, float& m, float& l) {
+        const float2 m0 = sm.ml[0][c], m1 = sm.ml[1][c];
+        m = fmaxf(m0.x, m1.x);
+        f0 = m0.y != 0.f ? ex2(m0.x - m) : 0.f;
+        f1 = m1.y != 0.f ? ex2(m1.x - m) : 0.f;
+        l = m0.y * f0 + m1.y * f1;
+      };
+      if (half == 1 && mine > 0) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < COLS; c0 += CH) {
+          uint32_t o[CH];
+          tc_ld(o, to + c0);
+#pragma unroll
+          for (int i = 0; i < CH; i++) xb[(c0 + i) * kTile + tl] = __uint_as_float(o[i]);
+        }
+      }
+      tc_before();
+      bar_sync(3, 256);
+      if (half == 0) {
+        const int other = wk.t1 - wk.t0 - mine;
+#pragma unroll 1
+        for (int c0 = 0; c0 < COLS; c0 += CH) {
+          uint32_t o[CH];
+          if (mine > 0) tc_ld(o, to + c0);
+#pragma unroll
+          for (int i = 0; i < CH; i++) {
+            float f0, f1, m, l;
+            joint(c0 + i, f0, f1, m, l);
+            float v = mine > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
+            if (other > 0) v = fmaf(xb[(c0 + i) * kTile + tl], f1, v);
+            if (whole)
+              o[i] = __float_as_uint(l != 0.f ? v * out_scale / l : 0.f);
+            else if (c0 + i < nr)
+              rec[2 * p.block_rows + (c0 + i) * kHeadDim + tl] = v;
+          }
+          if (whole) {
+            bar_sync(id, 128);  // these rows of xb are read
+#pragma unroll
+            for (int i = 0; i < CH; i++)
+              reinterpret_cast<__nv_bfloat16*>(p_all + c0 * kTile * 4)[i * kHeadDim + ch] = __float2bfloat16_rn(__uint_as_float(o[i]));
+            bar_sync(id, 128);
+            flush(p_all + c0 * kTile * 4, c0, CH);
+          }
+        }
+        if (!whole && tl < nr) {
+          float f0, f1, m, l;
+          joint(tl, f0, f1, m, l);
+          rec[tl] = m;
+          rec[p.block_rows + tl] = l;
+        }
+        tc_before();
+      }
+      bar_sync(3, 256);  // P and ml are written again
+    }
+  }
+}
+
+template <int COLS, bool DUAL>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreePlan p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* q_smem = base;
+  uint8_t* p_smem = base + 2 * kQBytes;
+  Small& sm = *reinterpret_cast<Small*>(base + 2 * kQBytes + 2 * kPBytes);
+  uint8_t* ring = base + kFixedBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 19) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int i = 0; i < kMaxStages; i++) {
+      mbar_init(smem_u32(&sm.ring_full[i]), 1);
+      mbar_init(smem_u32(&sm.ring_free[i]), 8);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(&sm.k_full[i]), 4);
+      mbar_init(smem_u32(&sm.k_free[i]), DUAL ? 2 : 1);
+      mbar_init(smem_u32(&sm.v_full[i]), 4);
+      mbar_init(smem_u32(&sm.v_free[i]), DUAL ? 2 : 1);
+      mbar_init(smem_u32(&sm.q_full[i]), 4);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_free[i]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      mbar_init(smem_u32(&sm.drain[i]), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_before();
   __syncthreads();
-  if (threadIdx.x < kHeadDim) {
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int w = 0; w < kTreeWarps; w++) m = fmaxf(m, sm[w]);
-    for (int w = 0; w < kTreeWarps; w++) {
-      const float f = sl[w] > 0.f ? exp2f(sm[w] - m) : 0.f;
-      l += f * sl[w];
-      o += f * so[w][threadIdx.x];
+  tc_after();
+  pdl_wait();  // the cache, q, k, v and the mask may be written by earlier kernels
+  Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
+  // 640 x 96 registers at launch; 2 x 128 x 144 + 2 x 128 x 80 + 128 x 32 = 61440
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    softmax_role<COLS, DUAL>(p, sm, q_smem, p_smem, wk, warp >> 2, threadIdx.x & 127);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    switch (p.a.c.bits) {
+      case 2: key_role<2>(p, sm, ring, wk, warp & 3, lane); break;
+      case 4: key_role<4>(p, sm, ring, wk, warp & 3, lane); break;
+      case 8: key_role<8>(p, sm, ring, wk, warp & 3, lane); break;
+      default: key_role<16>(p, sm, ring, wk, warp & 3, lane); break;
     }
-    static_cast<__nv_bfloat16*>(a.out)[(((long long)b * a.n + node) * a.q_heads + h) * kHeadDim + threadIdx.x] =
-        __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    switch (p.a.c.bits) {
+      case 2: value_role<2>(p, sm, ring, wk, warp & 3, lane); break;
+      case 4: value_role<4>(p, sm, ring, wk, warp & 3, lane); break;
+      case 8: value_role<8>(p, sm, ring, wk, warp & 3, lane); break;
+      default: value_role<16>(p, sm, ring, wk, warp & 3, lane); break;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    if (warp == 16) {
+      if (lane == 0) produce(p, sm, ring, wk);
+    } else if (warp < 19) {
+      const int half = warp - 17;
+      if (lane == 0)
+        mma_role<COLS, DUAL>(p, sm, smem_u32(q_smem) + half * kQBytes, smem_u32(p_smem) + half * kPBytes, wk, half);
+    }
+    __syncwarp();
   }
+  tc_before();
+  __syncthreads();
+  pdl_launch_dependents();
+  tc_after();
+  if (warp == 19) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
+}
+
+// Joins the partial records of one block of rows: a CTA per (stream, block of
+// rows, 8 rows); a thread per tensor-memory row (channel).
+constexpr int kMergeRows = 4;
+__global__ void __launch_bounds__(kHeadDim) tree_merge_kernel(const __grid_constant__ TreePlan p) {
+  pdl_wait();
+  const TreeArgs& a = p.a;
+  const int x = blockIdx.x, s = x / p.blocks, block = x - s * p.blocks;
+  const int c0 = cta_of(p.units, p.grid, x * p.tiles), c1 = cta_of(p.units, p.grid, x * p.tiles + p.tiles - 1);
+  if (c0 == c1) return;
+  const int b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
+  const int first = cta_begin(p.units, p.grid, c0) == x * p.tiles ? 0 : 1;  // the record of CTA c0
+  const float out_scale = 1.0f / value_scale(a.c.bits);
+  __shared__ __align__(16) __nv_bfloat16 sh[kMergeRows][kHeadDim];
+  const int ch = channel_of(threadIdx.x);
+  const int rb = blockIdx.y * kMergeRows;
+  for (int i = 0; i < kMergeRows; i++) {
+    const int r = rb + i;
+    if (r >= p.block_rows || block * p.block_rows + r >= p.rows) break;
+    const float* rec = p.parts + ((size_t)c0 * 2 + first) * p.rec;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int c = c0; c <= c1; c++) {
+      const float* q = c == c0 ? rec : p.parts + (size_t)c * 2 * p.rec;
+      const float mk = q[r], lk = q[p.block_rows + r], ok = q[2 * p.block_rows + r * kHeadDim + threadIdx.x];
+      if (lk == 0.f) continue;
+      const float mn = fmaxf(m, mk), f = ex2(m - mn), fk = ex2(mk - mn);
+      l = l * f + lk * fk;
+      o = o * f + ok * fk;
+      m = mn;
+    }
+    sh[i][ch] = __float2bfloat16_rn(l != 0.f ? o * out_scale / l : 0.f);
+  }
+  __syncthreads();
+  if (threadIdx.x < kMergeRows * 16) {
+    const int i = threadIdx.x >> 4, q = threadIdx.x & 15, r = rb + i;
+    const int row = block * p.block_rows + r;
+    if (r < p.block_rows && row < p.rows) {
+      const int node = row / a.group, g = row - node * a.group;
+      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                               (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim)[q] =
+          reinterpret_cast<const uint4*>(sh[i])[q];
+    }
+  }
+}
+
+template <int COLS, bool DUAL>
+cudaError_t launch_cols(const TreePlan& p, cudaStream_t s) {
+  const size_t smem = kFixedBytes + (size_t)p.stages * p.stage_bytes + 1024;
+  if (cudaError_t e = cudaFuncSetAttribute(tree_kernel<COLS, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
+    return e;
+  return launch_pdl(tree_kernel<COLS, DUAL>, dim3(p.grid), dim3(kTreeThreads), smem, s, p);
 }
 
 }  // namespace
 
-size_t tree_workspace(int num_sms) { return (size_t)num_sms * 16; }
+size_t tree_workspace(int num_sms, int rows) {
+  const int block = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return (size_t)num_sms * 2 * block * (2 + kHeadDim) * sizeof(float);
+}
 
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
-  tree_kernel<<<dim3(a.n * a.group, a.c.batch * a.c.kv_heads), kTreeWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
+  TreePlan p{};
+  p.a = a;
+  p.f = f;
+  p.rows = a.n * a.group;
+  p.block_rows = p.rows <= 16 ? 16 : p.rows <= 32 ? 32 : p.rows <= 64 ? 64 : 128;
+  p.blocks = (p.rows + p.block_rows - 1) / p.block_rows;
+  p.part_group = -1;
+  if (a.c.n_prog > 0) {
+    if (a.c.kmc) p.f.gps = a.c.n_prog / kGroupTokens;  // whole blocks, all full
+    p.tp = (int)((p.f.gps + kTileGroups - 1) / kTileGroups);
+    if (!a.c.kmc && f.k < f.nt && (f.h + f.r) % kGroupTokens) {  // tile k's last group
+      p.part_group = f.k * f.gpt + f.gk - 1;
+      p.part_valid = (f.h + f.r) % kGroupTokens;
+    }
+  } else {
+    p.f.gps = 0;
+  }
+  p.tw = (a.c.n_win + kTile - 1) / kTile;
+  p.td = (a.n + kTile - 1) / kTile;
+  p.tiles = p.tp + p.tw + p.td;
+  const long long units = (long long)a.c.batch * a.c.kv_heads * p.blocks * p.tiles;
+  if (units > 0x7fffffffLL || a.num_sms < 1) return cudaErrorInvalidValue;
+  p.units = (int)units;
+  p.grid = (int)(units < a.num_sms ? units : a.num_sms);
+  p.stage_bytes = kTileGroups * (group_bytes(a.c.bits) + 128) + 4 * kHeadDim;
+  p.stages = (kSmemMax - kFixedBytes) / p.stage_bytes;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  if (p.stages < 2) return cudaErrorInvalidValue;
+  p.rec = p.block_rows * (2 + kHeadDim);
+  p.parts = static_cast<float*>(a.ws);
+  cudaError_t e;
+  switch (p.block_rows) {
+    case 16: e = launch_cols<16, false>(p, s); break;
+    case 32: e = launch_cols<32, false>(p, s); break;
+    case 64: e = launch_cols<64, false>(p, s); break;
+    default: e = launch_cols<64, true>(p, s); break;
+  }
+  if (e != cudaSuccess || p.units % p.grid == 0 && (p.units / p.grid) % p.tiles == 0) return e;  // every share whole blocks of rows
+  return launch_pdl(tree_merge_kernel, dim3((unsigned)(p.units / p.tiles), (unsigned)((p.block_rows + kMergeRows - 1) / kMergeRows)),
+                    dim3(kHeadDim), 0, s, p);
 }
 
 }  // namespace kvq

@@ -41,29 +41,6 @@ __device__ __forceinline__ long long window_token(long long n, int s) {
   return last - ((last - (s - 1)) & (kWindowTokens - 1)) + 1;
 }
 
-// Group g of 16 slots in a tile: code of Key channel c, token `tok` (0..15).
-__device__ __forceinline__ uint32_t key_code(const uint8_t* gbase, int bits, int tok, int c) {
-  const int g = tok & 7, x = tok >> 3;
-  const int p = 2 * (c >> 5) + ((c >> 4) & 1), t = (c >> 2) & 3, i = c & 3;
-  int word, shift;
-  if (bits == 16) {
-    word = x * 16 + 2 * p + (i >> 1);
-    shift = 16 * (i & 1);
-  } else {
-    const int qpw = 8 / bits;
-    word = x * bits + p / qpw;
-    shift = 8 * i + bits * (p % qpw);
-  }
-  return (reinterpret_cast<const uint32_t*>(gbase + (4 * g + t) * unit_bytes(bits))[word] >> shift) & ((1u << bits) - 1u);
-}
-__device__ __forceinline__ uint32_t value_code(const uint8_t* gbase, int bits, int tok, int c) {
-  const int t = (tok & 7) >> 1, m = tok & 1, u = tok >> 3;
-  const int p = 2 * (c >> 4) + ((c >> 3) & 1), g = c & 7, ppw = 16 / bits;
-  const int word = u * bits + p / ppw;
-  const uint8_t* unit = gbase + part_bytes(bits) + (4 * g + t) * unit_bytes(bits);
-  return (reinterpret_cast<const uint32_t*>(unit)[word] >> (16 * m + bits * (p % ppw))) & ((1u << bits) - 1u);
-}
-
 struct ReadArgs {
   CacheView c;
   long long start;
@@ -92,7 +69,7 @@ struct TreeArgs {
   void* ws;
   int num_sms;
 };
-size_t tree_workspace(int num_sms);
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
+size_t tree_workspace(int num_sms, int rows);
+cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s);
 
 }  // namespace kvq

@@ -9,12 +9,19 @@ finfo(t).eps / 2 relative to the value (bf16 2^-8, fp16 2^-11, fp32 2^-24).
    all, plus u_t |y|.
  * read: every step is one IEEE fp32 operation, so fp32 outputs are equal and
    bf16 outputs are those values rounded.
- * tree: a score is sum_c q'_c k_c with both factors rounded to fp16, so it is
-   off by at most delta = 2.1 u_fp16 sum_c |q'_c k_c| (plus 0.2e-3 for the fp32
-   sums and the exponential); weights then change by at most e^(2 delta) - 1
-   relative, each p and v is rounded to fp16 once or twice (4 u_fp16), and the
-   output once to bf16: |o - o*| <= u_bf16 |o*| (1 + small) + (e^(2 delta) - 1 +
-   4 u_fp16) sum_t w_t |v_t| + 1e-6."""
+ * tree, u = u_fp16 and w the weights.  Cached values go through their group's
+   centre c = Z + R 2^(b-1) / (2^b - 1): centre and value are each rounded
+   once, the 16-bit codes once more and the 16-bit range of a block that has
+   other widths once more, the latter two relative to |v - c| <= |v| + |c|; p is
+   rounded once (2^-25 absolute below 2^-14, against a largest p of about 1).  So
+   the output is off by u sum_t w_t (4 |v_t| + 3 |c_t|) + T 2^-25 max |v|.
+   A score sum_c q'_c k_c has q' rounded, and k like a value but for the range:
+   delta = u sum_c |q'_c| (3 |k_c| + 2 |c|), c the centre of the Key's group (of
+   its channel's block with per-channel groups), plus 2e-4 for the fp32 sums
+   and the exponential; weights then change by at most e^(2 delta) - 1 relative.
+   The output is rounded once to bf16:
+   |o - o*| <= u_bf16 |o*| 1.02 + 1.02 ((e^(2 delta) - 1) sum_t w_t |v_t| + the
+   above) + 1e-6 (1.02: products of these, and second orders)."""
 import math
 
 import numpy as np
@@ -186,7 +193,7 @@ MODES = ["plain", "window", "channel"]
 
 def make_cache(kvq, mode, B, H, T, fbit, n_f, seed=0, lam=True, direct=False, chunk=0):
     """A cache of T random tokens (Keys with loud channels) and the values it holds, fp32 [B][H][T][128] each, by the
-    codes and meta that export gives (lambda undone)."""
+    codes and meta that export gives (lambda undone).  ks.centre, vs.centre: the centres of their groups."""
     per = B * H * 2 * (16 * fbit + 4)
     cache = kvq.KVQCache(1, B, H, n_f * per, [fbit], sink_window=mode == "window", key_channel=mode == "channel")
     k, v = S.keys_values(seed, 0, B, max(T, 1), H, 0, 4, dtype=torch.float32)
@@ -213,6 +220,11 @@ def held(kvq, cache, mode, B, H, T, scale):
     bits = cache.query(0)["bits"]
     ks, vs = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 128), np.float32)
 
+    kcen, vcen = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 1), np.float32)
+
+    def centre(r, z, b):
+        return z + r * (2.0 ** (b - 1) / (2.0 ** b - 1))
+
     def values(codes, r, z, b):
         return (codes.astype(np.float32) * (r / np.float32(2 ** b - 1)) + z).astype(np.float32)
 
@@ -229,15 +241,22 @@ def held(kvq, cache, mode, B, H, T, scale):
                     kr, kz = half(km[:, 0])[:, None], half(km[:, 1])[:, None]
                 ks[b, j, off:off + n] = values(kc, kr, kz, bits)
                 vs[b, j, off:off + n] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
+                kcen[b, j, off:off + n] = centre(kr, kz, bits)
+                vcen[b, j, off:off + n] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
             if mode != "plain":
                 kc, vc, km, vm = cache.export_window(0, b, j)
                 m = len(kc)
                 at = list(range(T - m, T)) if mode == "channel" else ([0] + list(range(T - m + 1, T)) if m else [])
                 ks[b, j, at] = values(kc, half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
                 vs[b, j, at] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
+                kcen[b, j, at] = centre(half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
+                vcen[b, j, at] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
     if scale is not None:
         ks = ks * scale.numpy()[None, :, None, :]
-    return torch.from_numpy(ks), torch.from_numpy(vs)
+        kcen = kcen * scale.numpy()[None, :, None, :]
+    ks, vs = torch.from_numpy(ks), torch.from_numpy(vs)
+    ks.centre, vs.centre = torch.from_numpy(kcen), torch.from_numpy(vcen)
+    return ks, vs
 
 
 # ------------------------------------------------------------- reading back
@@ -332,6 +351,7 @@ def tree_check(q, dk, dv, mask, ks, vs, got, sm_scale=128 ** -0.5):
     dev = "cuda"
     seen = torch.ones(n, n, dtype=torch.bool).tril() if mask is None else mask.bool().cpu()
     seen = seen.expand(B, n, n).to(dev)
+    kc, vc = ks.centre.to(dev).double().abs(), vs.centre.to(dev).double().abs()
     ks, vs = ks.to(dev).double(), vs.to(dev).double()
     T = ks.shape[2]
     bad = torch.full((), -math.inf, dtype=torch.float64, device=dev)
@@ -341,16 +361,21 @@ def tree_check(q, dk, dv, mask, ks, vs, got, sm_scale=128 ** -0.5):
             vv = torch.cat([vs[b, j], dv[b, :, j].double()])
             vis = torch.cat([torch.ones(n, T, dtype=torch.bool, device=dev), seen[b]], 1)
             kk, vv = torch.nan_to_num(kk, 0, 0, 0), torch.nan_to_num(vv, 0, 0, 0)
+            kerr = 3 * kk.abs()
+            kerr[:T] += 2 * kc[b, j]
+            verr = 4 * vv.abs()
+            verr[:T] += 3 * vc[b, j]
             for g in range(G):
                 qq = q[b, :, j * G + g].double()
                 s = torch.where(vis, sm_scale * (qq @ kk.T), bad)
-                size = torch.where(vis, abs(sm_scale) * (qq.abs() @ kk.abs().T), 0.0).amax(1, keepdim=True)
+                size = torch.where(vis, abs(sm_scale) * (qq.abs() @ kerr.T), 0.0).amax(1, keepdim=True)
                 w = torch.softmax(s, -1)
                 empty = ~vis.any(1)
                 w[empty] = 0.0
                 o = w @ vv
-                delta = 2.1 * U16 * size + 2e-4
-                tol = UBF * 1.02 * o.abs() + (torch.exp(2 * delta) - 1 + 4 * U16) * (w @ vv.abs()) * 1.02 + 1e-6
+                delta = U16 * size + 2e-4
+                off = (torch.exp(2 * delta) - 1) * (w @ vv.abs()) + U16 * (w @ verr) + (T + n) * 2.0 ** -25 * vv.abs().max()
+                tol = UBF * 1.02 * o.abs() + 1.02 * off + 1e-6
                 y = got[b, :, j * G + g].double()
                 assert torch.isfinite(y).all(), (b, j, g)
                 off = (y - o).abs() - tol

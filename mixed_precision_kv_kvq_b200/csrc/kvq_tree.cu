@@ -170,12 +170,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
 #define KVQ_W4(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3])
 #define KVQ_W16(r, i) KVQ_W4(r, i), KVQ_W4(r, (i) + 4), KVQ_W4(r, (i) + 8), KVQ_W4(r, (i) + 12)
 
-// 16 rows x 64 columns (Keys of a group).
-__device__ __forceinline__ void tc_st_16x256_x8(uint32_t t, const uint32_t (&r)[32]) {
+// 16 rows x 32 columns (64 channels of the Keys of a group).
+__device__ __forceinline__ void tc_st_16x256_x4(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_R16(r, 0),
-      KVQ_R16(r, 16), "r"(t)
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16(r, 0),
+      "r"(t)
       : "memory");
 }
 // 16 rows x 16 columns (16 channels of the Values of two groups).
@@ -224,6 +223,35 @@ __device__ __forceinline__ float warp_max_f32(float x) {  // one redux
   return y;
 }
 
+// Where a group lies: a stage of the ring (shared memory) or the window's
+// tiles (global memory).
+struct FromRing {
+  uint32_t at;
+  __device__ __forceinline__ FromRing operator+(int o) const { return FromRing{at + (uint32_t)o}; }
+  __device__ __forceinline__ uint32_t u32() const {
+    uint32_t x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at));
+    return x;
+  }
+  __device__ __forceinline__ uint2 u64() const {
+    uint2 x;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at));
+    return x;
+  }
+  __device__ __forceinline__ uint4 u128() const {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+    return x;
+  }
+};
+struct FromGlobal {
+  const uint8_t* at;
+  __device__ __forceinline__ FromGlobal operator+(int o) const { return FromGlobal{at + o}; }
+  __device__ __forceinline__ uint32_t u32() const { return *reinterpret_cast<const uint32_t*>(at); }
+  __device__ __forceinline__ uint2 u64() const { return *reinterpret_cast<const uint2*>(at); }
+  __device__ __forceinline__ uint4 u128() const { return *reinterpret_cast<const uint4*>(at); }
+};
+
 // --------------------------------------------------------------- widening
 
 __host__ __device__ constexpr uint32_t splat_h(uint32_t h) { return h | (h << 16); }
@@ -257,17 +285,17 @@ __device__ __forceinline__ uint32_t sat_h2(float lo, float hi) {
   return pack_h2(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
 }
 
-// One Key quad position p (channels 16 p + 4 t .. + 3) of token half x: the
-// pairs (members 0, 2) and (members 1, 3).
+// Quad position p (channels 16 p + 4 t .. + 3) of one token: the pairs (members
+// 0, 2) and (members 1, 3).  u: the words of the token's half of the lane unit
+// from quad position p0 on.
 template <int BITS>
-__device__ __forceinline__ void key_pairs(const uint32_t (&u)[2 * BITS], int x, int p, uint32_t& a, uint32_t& b) {
+__device__ __forceinline__ void key_pairs(const uint32_t* u, int p, uint32_t& a, uint32_t& b) {
   if constexpr (BITS == 16) {
-    const uint32_t w0 = u[x * 16 + 2 * p], w1 = u[x * 16 + 2 * p + 1];
-    a = code_val16(__byte_perm(w0, w1, 0x5410));
-    b = code_val16(__byte_perm(w0, w1, 0x7632));
+    a = code_val16(__byte_perm(u[2 * p], u[2 * p + 1], 0x5410));
+    b = code_val16(__byte_perm(u[2 * p], u[2 * p + 1], 0x7632));
   } else {
     constexpr int qpw = 8 / BITS;
-    const uint32_t w = u[x * BITS + p / qpw], w8 = w >> 8;
+    const uint32_t w = u[p / qpw], w8 = w >> 8;
     switch (p % qpw) {  // a constant after unrolling
       case 0: a = code_val<BITS, 0>(w); b = code_val<BITS, 0>(w8); break;
       case 1: if constexpr (qpw > 1) { a = code_val<BITS, BITS>(w); b = code_val<BITS, BITS>(w8); } break;
@@ -277,35 +305,51 @@ __device__ __forceinline__ void key_pairs(const uint32_t (&u)[2 * BITS], int x, 
   }
 }
 
-// Keys of one group into 16 tensor-memory rows.  part: the group's Key part;
-// kmc: the block's per-channel (R, Z) words in shared memory, or null.
-template <int BITS>
-__device__ __forceinline__ void widen_keys(const uint8_t* part, const uint32_t* kmc, uint32_t taddr, int lane) {
-  uint32_t u[2 * BITS], r[32];
+// Keys of one group into 16 tensor-memory rows, 64 channels at a time.  part:
+// the group's Key part; CHAN: per-channel groups, their (R, Z) words at kmc.
+template <int BITS, bool CHAN, typename From>
+__device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t taddr, int lane) {
+  constexpr int kHalfWords = BITS / 2;  // words of 4 quad positions of one token
+  const From unit = part + lane * unit_bytes(BITS);
 #pragma unroll
-  for (int i = 0; i < 2 * BITS; i += 4) {
-    const uint4 w = *(reinterpret_cast<const uint4*>(part + lane * unit_bytes(BITS)) + i / 4);
-    u[i] = w.x; u[i + 1] = w.y; u[i + 2] = w.z; u[i + 3] = w.w;
-  }
+  for (int hf = 0; hf < 2; hf++) {
+    uint32_t u[2][kHalfWords], r[16];
 #pragma unroll
-  for (int p = 0; p < 8; p++) {
+    for (int x = 0; x < 2; x++) {
+      const From at = unit + 4 * (x * BITS + hf * kHalfWords);
+      if constexpr (kHalfWords == 1) {
+        u[x][0] = at.u32();
+      } else if constexpr (kHalfWords == 2) {
+        const uint2 w = at.u64();
+        u[x][0] = w.x; u[x][1] = w.y;
+      } else {
 #pragma unroll
-    for (int x = 0; x < 2; x++) key_pairs<BITS>(u, x, p, r[4 * p + 2 * x], r[4 * p + 2 * x + 1]);
-    if (kmc) {  // k (1 - 2^-b) / 2 = val R/4 + (Z (1 - 2^-b) / 2 + R/4)
-      constexpr uint32_t g = BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
-      const uint4 w = *reinterpret_cast<const uint4*>(kmc + 16 * p + 4 * (lane & 3));
-      const uint32_t ra = hmul2_u(__byte_perm(w.x, w.z, 0x5410), splat_h(pow2_h(-2)));
-      const uint32_t rb = hmul2_u(__byte_perm(w.y, w.w, 0x5410), splat_h(pow2_h(-2)));
-      const uint32_t za = hfma2_u(__byte_perm(w.x, w.z, 0x7632), splat_h(g), ra);
-      const uint32_t zb = hfma2_u(__byte_perm(w.y, w.w, 0x7632), splat_h(g), rb);
-#pragma unroll
-      for (int x = 0; x < 2; x++) {
-        r[4 * p + 2 * x] = hfma2_u(r[4 * p + 2 * x], ra, za);
-        r[4 * p + 2 * x + 1] = hfma2_u(r[4 * p + 2 * x + 1], rb, zb);
+        for (int i = 0; i < kHalfWords; i += 4) {
+          const uint4 w = (at + 4 * i).u128();
+          u[x][i] = w.x; u[x][i + 1] = w.y; u[x][i + 2] = w.z; u[x][i + 3] = w.w;
+        }
       }
     }
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+#pragma unroll
+      for (int x = 0; x < 2; x++) key_pairs<BITS>(u[x], p, r[4 * p + 2 * x], r[4 * p + 2 * x + 1]);
+      if constexpr (CHAN) {  // k (1 - 2^-b) / 2 = val R/4 + (Z (1 - 2^-b) / 2 + R/4)
+        constexpr uint32_t g = BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
+        const uint4 w = (kmc + 4 * (16 * (4 * hf + p) + 4 * (lane & 3))).u128();
+        const uint32_t ra = hmul2_u(__byte_perm(w.x, w.z, 0x5410), splat_h(pow2_h(-2)));
+        const uint32_t rb = hmul2_u(__byte_perm(w.y, w.w, 0x5410), splat_h(pow2_h(-2)));
+        const uint32_t za = hfma2_u(__byte_perm(w.x, w.z, 0x7632), splat_h(g), ra);
+        const uint32_t zb = hfma2_u(__byte_perm(w.y, w.w, 0x7632), splat_h(g), rb);
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          r[4 * p + 2 * x] = hfma2_u(r[4 * p + 2 * x], ra, za);
+          r[4 * p + 2 * x + 1] = hfma2_u(r[4 * p + 2 * x + 1], rb, zb);
+        }
+      }
+    }
+    tc_st_16x256_x4(taddr + 32 * hf, r);
   }
-  tc_st_16x256_x8(taddr, r);
 }
 
 // Values of one group and this warp's 32 channels.  The warp takes the channels
@@ -314,23 +358,23 @@ __device__ __forceinline__ void widen_keys(const uint8_t* part, const uint32_t* 
 // lane (g', t) turns pairs 2 g', 2 g' + 1 (r = 0, 1) of unit (2 w + h, t).
 // out[h][2 u + r]: rows g' + 8 r, column 4 u + t of the group's eight.
 // rc, zc: half2 of (R, Z) factors of tokens 2t, 2t + 1 (+ 8 u).
-template <int BITS>
-__device__ __forceinline__ void widen_values(const uint8_t* part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], int w,
-                                             int lane, uint32_t (&out)[2][4]) {
+template <int BITS, typename From>
+__device__ __forceinline__ void widen_values(From part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], int w, int lane,
+                                             uint32_t (&out)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; h++) {
-    const uint32_t* unit = reinterpret_cast<const uint32_t*>(part + (4 * (2 * w + h) + t) * unit_bytes(BITS));
+    const From unit = part + (4 * (2 * w + h) + t) * unit_bytes(BITS);
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       uint32_t v0, v1;
       if constexpr (BITS == 16) {
-        const uint2 x = *reinterpret_cast<const uint2*>(unit + u * 16 + 2 * g);
+        const uint2 x = (unit + 4 * (u * 16 + 2 * g)).u64();
         v0 = code_val16(x.x);
         v1 = code_val16(x.y);
       } else {
         constexpr int ppw = 16 / BITS;  // pairs per word
-        const uint32_t x = unit[u * BITS + 2 * g / ppw] >> (2 * BITS * (g % (ppw / 2)));
+        const uint32_t x = (unit + 4 * (u * BITS + 2 * g / ppw)).u32() >> (2 * BITS * (g % (ppw / 2)));
         v0 = code_val<BITS, 0>(x);
         if constexpr (BITS == 8)
           v1 = code_val<8, 0>(x >> 8);
@@ -429,19 +473,18 @@ out:
       drain_wait(&sm.ring_full[i % p.stages], (i / p.stages) & 1);
 }
 
-// Group gi (0..7) of tile t as (code part, meta words): in the ring's stage,
-// or the window's tiles in global memory; null if the group does not exist.
-struct GroupAt {
+// Group gi (0..7) of window tile t; null if it does not exist.
+struct WindowGroup {
   const uint8_t* code;
   const uint32_t* meta;
 };
-__device__ __forceinline__ GroupAt window_group(const TreePlan& p, int s, int t, int gi) {
+__device__ __forceinline__ WindowGroup window_group(const TreePlan& p, int s, int t, int gi) {
   const int wg = (t - p.tp) * kTileGroups + gi;
-  if (wg * kGroupTokens >= p.a.c.n_win) return GroupAt{nullptr, nullptr};
+  if (wg * kGroupTokens >= p.a.c.n_win) return WindowGroup{nullptr, nullptr};
   constexpr int kPer = slots_per_tile(16) / kGroupTokens;
   const size_t tile = (size_t)s * kWindowTiles + wg / kPer;
-  return GroupAt{p.a.c.wcodes + tile * kTileBytes + (size_t)(wg % kPer) * group_bytes(16),
-                 p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
+  return WindowGroup{p.a.c.wcodes + tile * kTileBytes + (size_t)(wg % kPer) * group_bytes(16),
+                     p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
 }
 
 // Drafted Keys: rows g and g + 8 of the group, channels 16 p + 4 t .. + 3, as k / (2 lambda).
@@ -449,30 +492,34 @@ __device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, uin
   const TreeArgs& a = p.a;
   const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t r[32];
 #pragma unroll
-  for (int x = 0; x < 2; x++) {
-    const int j = j0 + g + 8 * x;
-    const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 4 * t;
+  for (int hf = 0; hf < 2; hf++) {
+    uint32_t r[16];
 #pragma unroll
-    for (int q = 0; q < 8; q++) {
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j < a.n) {
-        if (a.f32) {
-          k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at + 16 * q));
-        } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q));
-          k = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                          __uint_as_float(w.y & 0xffff0000u));
+    for (int x = 0; x < 2; x++) {
+      const int j = j0 + g + 8 * x;
+      const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 64 * hf + 4 * t;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < a.n) {
+          if (a.f32) {
+            k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at + 16 * q));
+          } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q));
+            k = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                            __uint_as_float(w.y & 0xffff0000u));
+          }
         }
+        float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (a.c.lam_inv)
+          l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 64 * hf + 16 * q + 4 * t));
+        r[4 * q + 2 * x] = sat_h2(0.5f * k.x * l.x, 0.5f * k.z * l.z);
+        r[4 * q + 2 * x + 1] = sat_h2(0.5f * k.y * l.y, 0.5f * k.w * l.w);
       }
-      float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (a.c.lam_inv) l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 16 * q + 4 * t));
-      r[4 * q + 2 * x] = sat_h2(0.5f * k.x * l.x, 0.5f * k.z * l.z);
-      r[4 * q + 2 * x + 1] = sat_h2(0.5f * k.y * l.y, 0.5f * k.w * l.w);
     }
+    tc_st_16x256_x4(taddr + 32 * hf, r);
   }
-  tc_st_16x256_x8(taddr, r);
 }
 // Drafted Values of a group for this warp's channels (widen_values' layout), times g.
 __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, float scale, int w, int lane,
@@ -508,7 +555,7 @@ __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, f
 // Four warps: Keys of every tile into tensor memory, the tokens' (Rk, Zk) and,
 // for drafted tiles, which rows see them.  Warp w: tokens 32 w .. 32 w + 31.
 template <int BITS>
-__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk, int w, int lane) {
+__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int w, int lane) {
   const CacheView& c = p.a.c;
   constexpr int gb = group_bytes(BITS);
   uint32_t ct = 0, rc = 0;
@@ -523,17 +570,18 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint8_t* 
         const int slot = rc % p.stages;
         tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
         tc_after();
-        const uint8_t* st = ring + (size_t)slot * p.stage_bytes;
-        const uint32_t* meta = reinterpret_cast<const uint32_t*>(st + kTileGroups * gb);
-        const uint32_t* kmc = c.kmc ? reinterpret_cast<const uint32_t*>(st + kTileGroups * (gb + 128)) : nullptr;
-        // groups that do not exist leave what the stage held: those rows of S are not used
-#pragma unroll 1
-        for (int i = 0; i < 2; i++)
-          widen_keys<BITS>(st + (2 * w + i) * gb, kmc, ta + ((uint32_t)(16 * i) << 16), lane);
+        const FromRing st{ring + (uint32_t)(slot * p.stage_bytes)};
+        const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
+        // groups that do not exist are read as whatever the stage holds: those rows of S are not used
         if (c.kmc) {
+#pragma unroll 1
+          for (int i = 0; i < 2; i++)
+            widen_keys<BITS, true>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), ta + ((uint32_t)(16 * i) << 16), lane);
           kz = make_float2(1.0f / value_scale(BITS), 0.f);
         } else {
-          const uint32_t m = meta[2 * tl];
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+            widen_keys<BITS, false>(st + (2 * w + i) * gb, st, ta + ((uint32_t)(16 * i) << 16), lane);
           const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
                            ((float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u));
           kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
@@ -545,10 +593,10 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint8_t* 
         tc_after();
 #pragma unroll 1
         for (int i = 0; i < 2; i++) {
-          const GroupAt at = window_group(p, wk.s, t, 2 * w + i);
-          if (at.code) widen_keys<16>(at.code, nullptr, ta + ((uint32_t)(16 * i) << 16), lane);
+          const WindowGroup at = window_group(p, wk.s, t, 2 * w + i);
+          if (at.code) widen_keys<16, false>(FromGlobal{at.code}, FromRing{0}, ta + ((uint32_t)(16 * i) << 16), lane);
         }
-        const GroupAt at = window_group(p, wk.s, t, tl >> 4);
+        const WindowGroup at = window_group(p, wk.s, t, tl >> 4);
         if (at.meta) {
           const uint32_t m = at.meta[2 * (tl & 15)];
           const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * (32768.0f / 65535.0f);
@@ -582,85 +630,115 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint8_t* 
   }
 }
 
+// Values of a packed tile in the ring.  CHECK: some of its tokens do not exist
+// (n groups do; group part only its first valid tokens): they become zeros, as
+// P is zero there and stale codes with a stale range may be anything.
+template <int BITS, bool CHECK>
+__device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int n, int part, int valid, int w, int lane) {
+  constexpr int gb = group_bytes(BITS);
+  const int t = lane & 3;
+  const uint32_t gh = splat_h(value_scale_h(BITS));
+#pragma unroll 2
+  for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
+    uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int gi = g2 + i;
+      uint32_t rc[2], zc[2], out[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        uint4 m = (st + (kTileGroups * gb + gi * 128 + 8 * (8 * u + 2 * t))).u128();  // K, V of tokens 2t, 2t + 1 (+ 8u)
+        if constexpr (CHECK) {
+          const int first = 8 * u + 2 * t, have = gi >= n ? 0 : gi == part ? valid : kGroupTokens;
+          if (first >= have) m.y = 0u;
+          if (first + 1 >= have) m.w = 0u;
+        }
+        const uint32_t r2 = __byte_perm(m.y, m.w, 0x5410), z2 = __byte_perm(m.y, m.w, 0x7632);
+        rc[u] = hmul2_u(r2, splat_h(pow2_h(-2)));  // R g 2^(b-1) / (2^b - 1) = R / 4
+        zc[u] = hfma2_u(z2, gh, rc[u]);
+      }
+      widen_values<BITS>(st + (gi * gb + part_bytes(BITS)), rc, zc, w, lane, out);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        o0[4 * i + e] = out[0][e];
+        o1[4 * i + e] = out[1][e];
+      }
+    }
+    tc_st_16x128_x4(ta + 8 * g2, o0);
+    tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
+  }
+}
+
 // Four warps: Values of every tile.  Warp w: the channels of lane units 2 w, 2 w + 1.
 template <int BITS>
-__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk, int w, int lane) {
+__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int w, int lane) {
   const int t4 = lane & 3;
-  constexpr int gb = group_bytes(BITS);
-  const uint32_t gh = splat_h(value_scale_h(BITS));
   uint32_t ct = 0, rc = 0;
   while (wk.next(p)) {
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
       const uint32_t ta = sm.tmem + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
       tree_wait(&sm.v_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
-      const bool packed = t < p.tp;
-      const int slot = rc % p.stages;
-      if (packed) tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
-      tc_after();
-      const uint8_t* st = ring + (size_t)slot * p.stage_bytes;
-      const long long v0 = (long long)t * kTileGroups;
+      if (t < p.tp) {
+        const int slot = rc % p.stages;
+        tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
+        tc_after();
+        const FromRing st{ring + (uint32_t)(slot * p.stage_bytes)};
+        const int n = (int)min((long long)kTileGroups, p.f.gps - (long long)t * kTileGroups);
+        const int part = p.part_group - t * kTileGroups;
+        if (n == kTileGroups && (unsigned)part >= (unsigned)kTileGroups)
+          value_tile<BITS, false>(st, ta, n, part, p.part_valid, w, lane);
+        else
+          value_tile<BITS, true>(st, ta, n, part, p.part_valid, w, lane);
+        rc++;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
+      } else {
+        tc_after();
 #pragma unroll 1
-      for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
-        uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
+        for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
+          uint32_t o0[8], o1[8];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const int gi = g2 + i;
-          uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};  // tokens that do not exist: zeros (P is zero there too)
-          if (t < p.tp + p.tw) {
-            GroupAt at{nullptr, nullptr};
-            if (packed) {
-              if (v0 + gi < p.f.gps)
-                at = GroupAt{st + gi * gb, reinterpret_cast<const uint32_t*>(st + kTileGroups * gb + gi * 128)};
-            } else {
-              at = window_group(p, wk.s, t, gi);
-            }
-            if (at.code) {
-              uint32_t rcv[2], zcv[2];
+          for (int i = 0; i < 2; i++) {
+            uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+            if (t < p.tp + p.tw) {
+              const WindowGroup at = window_group(p, wk.s, t, g2 + i);
+              if (at.code) {
+                // 16-bit codes beside another width: R g / 2 is not exact, so the centre is formed in fp32
+                const float g = value_scale(BITS), f = g * (32768.0f / 65535.0f);
+                uint32_t rcv[2], zcv[2];
 #pragma unroll
-              for (int u = 0; u < 2; u++) {
-                const uint4 m = *reinterpret_cast<const uint4*>(at.meta + 2 * (8 * u + 2 * t4));  // K, V of tokens 2t, 2t + 1
-                uint32_t m0 = m.y, m1 = m.w;
-                if (!token_valid(p, t, 16 * gi + 8 * u + 2 * t4)) m0 = 0u;
-                if (!token_valid(p, t, 16 * gi + 8 * u + 2 * t4 + 1)) m1 = 0u;
-                const uint32_t r2 = __byte_perm(m0, m1, 0x5410), z2 = __byte_perm(m0, m1, 0x7632);
-                if (packed) {  // R g 2^(b-1) / (2^b - 1) = R / 4
-                  rcv[u] = hmul2_u(r2, splat_h(pow2_h(-2)));
-                  zcv[u] = hfma2_u(z2, gh, rcv[u]);
-                } else {  // 16-bit codes beside another width: not exact, so the centre is formed in fp32
-                  const float g = value_scale(BITS), f = g * (32768.0f / 65535.0f);
+                for (int u = 0; u < 2; u++) {
+                  const uint4 m = *reinterpret_cast<const uint4*>(at.meta + 2 * (8 * u + 2 * t4));
+                  const bool v0 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4);
+                  const bool v1 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4 + 1);
+                  const uint32_t r2 = __byte_perm(v0 ? m.y : 0u, v1 ? m.w : 0u, 0x5410);
+                  const uint32_t z2 = __byte_perm(v0 ? m.y : 0u, v1 ? m.w : 0u, 0x7632);
                   const float2 rf = __half22float2(*reinterpret_cast<const __half2*>(&r2));
                   const float2 zf = __half22float2(*reinterpret_cast<const __half2*>(&z2));
                   rcv[u] = pack_h2(rf.x * f, rf.y * f);
                   zcv[u] = pack_h2(fmaf(rf.x, f, zf.x * g), fmaf(rf.y, f, zf.y * g));
                 }
+                widen_values<16>(FromGlobal{at.code + part_bytes(16)}, rcv, zcv, w, lane, out);
               }
-              if (packed)
-                widen_values<BITS>(at.code + part_bytes(BITS), rcv, zcv, w, lane, out);
-              else
-                widen_values<16>(at.code + part_bytes(16), rcv, zcv, w, lane, out);
+            } else {
+              const int j0 = (t - p.tp - p.tw) * kTile + 16 * (g2 + i);
+              if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale(BITS), w, lane, out);
             }
-          } else {
-            const int j0 = (t - p.tp - p.tw) * kTile + 16 * gi;
-            if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale(BITS), w, lane, out);
-          }
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            o0[4 * i + e] = out[0][e];
-            o1[4 * i + e] = out[1][e];
+            for (int e = 0; e < 4; e++) {
+              o0[4 * i + e] = out[0][e];
+              o1[4 * i + e] = out[1][e];
+            }
           }
+          tc_st_16x128_x4(ta + 8 * g2, o0);
+          tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
         }
-        tc_st_16x128_x4(ta + 8 * g2, o0);
-        tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
       }
       tc_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.v_full[buf]);
-        if (packed) mbar_arrive(&sm.ring_free[slot]);
-      }
-      if (packed) rc++;
+      if (lane == 0) mbar_arrive(&sm.v_full[buf]);
     }
   }
 }
@@ -1073,18 +1151,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     switch (p.a.c.bits) {
-      case 2: key_role<2>(p, sm, ring, wk, warp & 3, lane); break;
-      case 4: key_role<4>(p, sm, ring, wk, warp & 3, lane); break;
-      case 8: key_role<8>(p, sm, ring, wk, warp & 3, lane); break;
-      default: key_role<16>(p, sm, ring, wk, warp & 3, lane); break;
+      case 2: key_role<2>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      case 4: key_role<4>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      case 8: key_role<8>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      default: key_role<16>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     switch (p.a.c.bits) {
-      case 2: value_role<2>(p, sm, ring, wk, warp & 3, lane); break;
-      case 4: value_role<4>(p, sm, ring, wk, warp & 3, lane); break;
-      case 8: value_role<8>(p, sm, ring, wk, warp & 3, lane); break;
-      default: value_role<16>(p, sm, ring, wk, warp & 3, lane); break;
+      case 2: value_role<2>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      case 4: value_role<4>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      case 8: value_role<8>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+      default: value_role<16>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");

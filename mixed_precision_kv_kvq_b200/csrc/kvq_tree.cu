@@ -58,12 +58,31 @@ namespace {
 
 constexpr int kTile = 128;           // tokens per tile
 constexpr int kTileGroups = kTile / kGroupTokens;
-constexpr int kTreeThreads = 640;
+constexpr int kTreeWarps = 28;
+constexpr int kTreeThreads = 32 * kTreeWarps;
 constexpr int kMaxStages = 8;
 constexpr int kHalfRows = 64;        // rows of a half's operands in shared memory
 constexpr int kQBytes = kHalfRows * kHeadDim * 2;  // one half's Q: two 64-channel slabs of [64][128 B]
 constexpr int kPBytes = kTile * 128;               // one half's P: [128 tokens][64 rows] fp16
 constexpr float kUnset = 1e30f;      // -m of a row with no token yet
+
+// How the 28 warps are divided, and the registers of each kind (setmaxnreg; 896
+// threads are launched with 72).  With few rows the widening is the larger
+// part of a tile's work and takes 16 warps; with 64 rows a half (128 rows
+// a CTA, or 64 in alternate tiles) the softmax is, and a half's rows are
+// divided over two warpgroups: 32 rows a thread is also what its registers hold.
+template <int COLS>
+struct Split {
+  static constexpr int kSoft = COLS == 64 ? 16 : 8;          // softmax warps
+  static constexpr int kWiden = COLS == 64 ? 4 : 8;          // warps for Keys, and as many for Values
+  static constexpr int kSubs = kSoft / 8;                    // warpgroups per half
+  static constexpr int kCols = COLS / kSubs;                 // rows per softmax thread
+  static constexpr int kSoftRegs = COLS == 64 ? 88 : COLS == 32 ? 104 : 80;
+  static constexpr int kWidenRegs = COLS == 64 ? 64 : COLS == 32 ? 64 : 80;
+  static constexpr int kCtlRegs = 24;
+  static_assert(kSoft + 2 * kWiden + 4 == kTreeWarps);
+  static_assert(32 * (kSoft * kSoftRegs + 2 * kWiden * kWidenRegs + 4 * kCtlRegs) <= kTreeThreads * 72);
+};
 
 // Tensor-memory columns.
 constexpr uint32_t kColS = 0, kColO = 128, kColK = 256, kColV = 384;  // + 64 per half or buffer
@@ -88,6 +107,7 @@ constexpr int kSmemMax = 227 * 1024 - 1024;  // the base is aligned by hand
 struct TreePlan {
   TreeArgs a;
   Fill f;               // progressive cache (group order)
+  int groups;           // groups of a stream's progressive cache
   int part_group, part_valid;  // the one group that may be partial, and its tokens
   int rows, block_rows, blocks;  // query rows of a stream, rows per block, blocks
   int tp, tw, td, tiles;         // progressive, window and drafted tiles of a stream
@@ -104,21 +124,38 @@ __host__ __device__ __forceinline__ int cta_of(int units, int grid, int u) {
 
 // ------------------------------------------------------------------ PTX
 
-__device__ __forceinline__ bool tree_wait_slow(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+// A test that may suspend the warp for some microseconds: fewer polls.
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait: gives up after kWaitNs or once another wait of the CTA has.
+__device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_long(b, parity)) return;
   const unsigned long long t0 = global_ns();
-  for (unsigned it = 0;; it++) {
-    if (mbar_try(bar, parity)) return true;
-    if (*abort) return false;
-    if ((it & 15) == 15 && global_ns() - t0 > kWaitNs) {
+  while (!mbar_try_long(b, parity)) {
+    if (*abort) return;
+    if (global_ns() - t0 > kWaitNs) {
       *abort = 1;
       atomicExch(err, 1);
-      return false;
+      return;
     }
   }
 }
-__device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
-  const uint32_t b = smem_u32(bar);
-  if (!mbar_try(b, parity)) (void)tree_wait_slow(b, parity, err, abort);
+// One lane of a converged warp.  MMAs and copies are issued under this
+// predicate by warps that run their loops whole: with `if (lane == 0)` instead,
+// every tcgen05.mma took ~108 cycles to issue (operands moved to uniform
+// registers lane by lane) whatever its size; so it is 30-40.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 // Also after an abort: what is in flight lands before the CTA ends.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
@@ -217,12 +254,6 @@ __device__ __forceinline__ void tc_st(uint32_t t, const uint32_t (&r)[N]) {
         "r"(t)
         : "memory");
 }
-__device__ __forceinline__ float warp_max_f32(float x) {  // one redux
-  float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Where a group lies: a stage of the ring (shared memory) or the window's
 // tiles (global memory).
 struct FromRing {
@@ -247,7 +278,6 @@ struct FromRing {
 struct FromGlobal {
   const uint8_t* at;
   __device__ __forceinline__ FromGlobal operator+(int o) const { return FromGlobal{at + o}; }
-  __device__ __forceinline__ uint32_t u32() const { return *reinterpret_cast<const uint32_t*>(at); }
   __device__ __forceinline__ uint2 u64() const { return *reinterpret_cast<const uint2*>(at); }
   __device__ __forceinline__ uint4 u128() const { return *reinterpret_cast<const uint4*>(at); }
 };
@@ -419,58 +449,97 @@ struct Walk {
 // Whether token tl (0..127) of tile t exists.
 __device__ __forceinline__ bool token_valid(const TreePlan& p, int t, int tl) {
   if (t < p.tp) {
-    const long long v = (long long)t * kTileGroups + (tl >> 4);
-    return v < p.f.gps && (v != p.part_group || (tl & 15) < p.part_valid);
+    const int v = t * kTileGroups + (tl >> 4);
+    return v < p.groups && (v != p.part_group || (tl & 15) < p.part_valid);
   }
   if (t < p.tp + p.tw) return (t - p.tp) * kTile + tl < p.a.c.n_win;
   return (t - p.tp - p.tw) * kTile + tl < p.a.n;
 }
 
-// Producer: packed progressive tiles into the ring.
-__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint8_t* ring, Walk wk) {
+// A slot of the ring and its phase, stepped tile by tile.
+struct Slot {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int stages) {
+    if (++i == stages) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Producer (one warp): packed progressive tiles into the ring, run by run (groups
+// that neighbour in one tile of the cache).
+__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t ring, Walk wk) {
   const CacheView& c = p.a.c;
-  const int bits = c.bits, gb = group_bytes(bits);
-  uint32_t rc = 0;
+  const Fill& f = p.f;
+  const int gb = group_bytes(c.bits);
+  const bool chan = c.kmc != nullptr;
+  Slot sl;
+  uint32_t sent = 0;
   while (wk.next(p)) {
+    if (wk.t0 >= p.tp) continue;
     const uint8_t* sbase = c.codes + (size_t)wk.s * c.nt * kTileBytes;
     const uint32_t* mbase = c.meta + (size_t)wk.s * c.nt * c.pf * 2;
-    for (int t = wk.t0; t < min(wk.t1, p.tp); t++, rc++) {
-      const int slot = rc % p.stages;
-      tree_wait(&sm.ring_free[slot], ((rc / p.stages) & 1) ^ 1, p.a.err, &sm.abort);
+    int tile = 0, grp = 0, groups = 0, e = 0;
+    if (!chan) {
+      const GroupLoc loc = locate_group(f, (long long)wk.t0 * kTileGroups);
+      tile = loc.tile;
+      grp = loc.grp;
+      groups = loc.tile_groups;
+    }
+    for (int t = wk.t0; t < min(wk.t1, p.tp); t++, sent++) {
+      tree_wait(&sm.ring_free[sl.i], sl.phase ^ 1, p.a.err, &sm.abort);
       if (sm.abort) goto out;
-      uint8_t* st = ring + (size_t)slot * p.stage_bytes;
-      const uint32_t bar = smem_u32(&sm.ring_full[slot]);
-      const int n = (int)min((long long)kTileGroups, p.f.gps - (long long)t * kTileGroups);
-      mbar_expect_tx(bar, (uint32_t)n * (gb + 128u) + (c.kmc ? 4u * kHeadDim : 0u));
-      for (int g = 0; g < n;) {
-        int tile, grp, run;
-        if (c.kmc) {  // a block in the order of arrival: whole runs of its epochs
-          const Place pl = place_of(c.ep, t * kTile + g * kGroupTokens);
-          tile = pl.tile;
-          grp = pl.slot >> 4;
-          int e = 0;
-          while (e + 1 < c.ep.n && t * kTile + g * kGroupTokens >= c.ep.start[e + 1]) e++;
-          run = min(n - g, (c.ep.h[e] + (1 << c.ep.lg_ee[e]) - pl.slot) >> 4);
-        } else {
-          const GroupLoc loc = locate_group(p.f, (long long)t * kTileGroups + g);
-          tile = loc.tile;
-          grp = loc.grp;
-          run = min(n - g, loc.tile_groups - loc.grp);
-        }
-        bulk_g2s(smem_u32(st + g * gb), sbase + (size_t)tile * kTileBytes + (size_t)grp * gb, (uint32_t)(run * gb), bar);
-        bulk_g2s(smem_u32(st + kTileGroups * gb + g * 128), mbase + ((size_t)tile * c.pf + (size_t)grp * 16) * 2,
-                 (uint32_t)run * 128u, bar);
-        g += run;
+      const uint32_t st = ring + (uint32_t)(sl.i * p.stage_bytes);
+      const uint32_t bar = smem_u32(&sm.ring_full[sl.i]);
+      const int n = min(kTileGroups, p.groups - t * kTileGroups);
+      if (elect_one()) {
+        mbar_expect_tx(bar, (uint32_t)n * (gb + 128u) + (chan ? 4u * kHeadDim : 0u));
+        if (chan)
+          bulk_g2s(st + kTileGroups * (gb + 128), c.kmc + ((size_t)wk.s * c.blocks_max + t) * kHeadDim, 4u * kHeadDim, bar);
       }
-      if (c.kmc)
-        bulk_g2s(smem_u32(st + kTileGroups * (gb + 128)), c.kmc + ((size_t)wk.s * c.blocks_max + t) * kHeadDim, 4u * kHeadDim,
-                 bar);
+      __syncwarp();
+      for (int g = 0; g < n;) {
+        int run;
+        if (chan) {  // a block in the order of arrival: whole or partial runs of its epochs
+          const int i = t * kTile + g * kGroupTokens;
+          while (e + 1 < c.ep.n && i >= c.ep.start[e + 1]) e++;
+          const int m = i - c.ep.start[e], lg = c.ep.lg_ee[e], off = m & ((1 << lg) - 1);
+          tile = m >> lg;
+          grp = (c.ep.h[e] + off) >> 4;
+          run = min(n - g, ((1 << lg) - off) >> 4);
+        } else {
+          run = min(n - g, groups - grp);
+        }
+        if (elect_one()) {
+          bulk_g2s(st + g * gb, sbase + (size_t)tile * kTileBytes + (size_t)(grp * gb), (uint32_t)(run * gb), bar);
+          bulk_g2s(st + kTileGroups * gb + g * 128, mbase + ((size_t)tile * c.pf + (size_t)(grp * kGroupTokens)) * 2,
+                   (uint32_t)run * 128u, bar);
+        }
+        __syncwarp();
+        g += run;
+        if (!chan) {
+          grp += run;
+          if (grp == groups) {  // the next tile: full, the partial tile k, or half full
+            tile++;
+            grp = 0;
+            groups = tile < f.k ? f.gpt : tile == f.k ? f.gk : f.gh;
+          }
+        }
+      }
+      sl.step(p.stages);
     }
   }
 out:
-  if (sm.abort)  // copies in flight land before the CTA ends
-    for (uint32_t i = rc > (uint32_t)p.stages ? rc - p.stages : 0; i < rc; i++)
-      drain_wait(&sm.ring_full[i % p.stages], (i / p.stages) & 1);
+  if (sm.abort) {  // copies in flight land before the CTA ends
+    const uint32_t k = min(sent, (uint32_t)p.stages);
+    for (uint32_t i = 0; i < k; i++) {
+      sl.i = sl.i == 0 ? p.stages - 1 : sl.i - 1;
+      if (sl.i == p.stages - 1) sl.phase ^= 1;
+      drain_wait(&sm.ring_full[sl.i], sl.phase);
+    }
+  }
 }
 
 // Group gi (0..7) of window tile t; null if it does not exist.
@@ -552,47 +621,50 @@ __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, f
   }
 }
 
-// Four warps: Keys of every tile into tensor memory, the tokens' (Rk, Zk) and,
-// for drafted tiles, which rows see them.  Warp w: tokens 32 w .. 32 w + 31.
-template <int BITS>
-__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int w, int lane) {
+// Keys of every tile into tensor memory, the tokens' (Rk, Zk) and, for drafted
+// tiles, which rows see them.  Warp w of WARPS: tokens 32 (w % 4) .. + 31, of 8
+// warps each takes one of the two groups.
+template <int BITS, int WARPS>
+__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int warp, int lane) {
   const CacheView& c = p.a.c;
-  constexpr int gb = group_bytes(BITS);
-  uint32_t ct = 0, rc = 0;
+  constexpr int gb = group_bytes(BITS), kEach = 8 / WARPS;  // groups per warp and tile
+  const int w = warp & 3, i0 = kEach == 1 ? warp >> 2 : 0;
+  uint32_t ct = 0;
+  Slot sl;
+  const uint32_t tm = sm.tmem;
   while (wk.next(p)) {
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
-      const uint32_t ta = sm.tmem + kColK + 64 * buf + ((uint32_t)(32 * w) << 16);
+      const uint32_t ta = tm + kColK + 64 * buf + ((uint32_t)(32 * w) << 16);
       tree_wait(&sm.k_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
       float2 kz = make_float2(0.f, 0.f);
-      const int tl = 32 * w + lane;
+      const int tl = 32 * w + 16 * i0 + (kEach == 1 ? lane & 15 : lane);
       if (t < p.tp) {
-        const int slot = rc % p.stages;
-        tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
+        tree_wait(&sm.ring_full[sl.i], sl.phase, p.a.err, &sm.abort);
         tc_after();
-        const FromRing st{ring + (uint32_t)(slot * p.stage_bytes)};
+        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
         const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
         // groups that do not exist are read as whatever the stage holds: those rows of S are not used
         if (c.kmc) {
 #pragma unroll 1
-          for (int i = 0; i < 2; i++)
+          for (int i = i0; i < i0 + kEach; i++)
             widen_keys<BITS, true>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), ta + ((uint32_t)(16 * i) << 16), lane);
           kz = make_float2(1.0f / value_scale(BITS), 0.f);
         } else {
 #pragma unroll
-          for (int i = 0; i < 2; i++)
-            widen_keys<BITS, false>(st + (2 * w + i) * gb, st, ta + ((uint32_t)(16 * i) << 16), lane);
+          for (int i = 0; i < kEach; i++)
+            widen_keys<BITS, false>(st + (2 * w + i0 + i) * gb, st, ta + ((uint32_t)(16 * (i0 + i)) << 16), lane);
           const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
                            ((float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u));
           kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
-        rc++;
+        if (lane == 0) mbar_arrive(&sm.ring_free[sl.i]);
+        sl.step(p.stages);
       } else if (t < p.tp + p.tw) {
         tc_after();
 #pragma unroll 1
-        for (int i = 0; i < 2; i++) {
+        for (int i = i0; i < i0 + kEach; i++) {
           const WindowGroup at = window_group(p, wk.s, t, 2 * w + i);
           if (at.code) widen_keys<16, false>(FromGlobal{at.code}, FromRing{0}, ta + ((uint32_t)(16 * i) << 16), lane);
         }
@@ -606,22 +678,23 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t 
         tc_after();
         const int j0 = (t - p.tp - p.tw) * kTile;
 #pragma unroll 1
-        for (int i = 0; i < 2; i++)
+        for (int i = i0; i < i0 + kEach; i++)
           if (j0 + 32 * w + 16 * i < p.a.n)
             draft_keys(p, wk.s, j0 + 32 * w + 16 * i, ta + ((uint32_t)(16 * i) << 16), lane);
         kz = make_float2(2.f, 0.f);
-        // one word per row: which of the warp's 32 tokens its node sees
-        const int b = wk.s / c.kv_heads, j = j0 + tl;
-        const int r0 = wk.block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
-        for (int node = r0 / p.a.group; node * p.a.group < r1; node++) {
-          bool see = j < p.a.n;
-          if (see) see = p.a.mask ? p.a.mask[b * p.a.mask_b + (long long)node * p.a.n + j] != 0 : j <= node;
-          const uint32_t bitsw = __ballot_sync(0xffffffffu, see);
-          const int row = node * p.a.group + lane - r0;
-          if (lane < p.a.group && row >= 0 && row < r1 - r0) sm.seen[ct & 3][row][w] = bitsw;
+        if (i0 == 0) {  // one word per row: which of the 32 tokens its node sees
+          const int b = wk.s / c.kv_heads, j = j0 + 32 * w + lane;
+          const int r0 = wk.block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
+          for (int node = r0 / p.a.group; node * p.a.group < r1; node++) {
+            bool see = j < p.a.n;
+            if (see) see = p.a.mask ? p.a.mask[b * p.a.mask_b + (long long)node * p.a.n + j] != 0 : j <= node;
+            const uint32_t bitsw = __ballot_sync(0xffffffffu, see);
+            const int row = node * p.a.group + lane - r0;
+            if (lane < p.a.group && row >= 0 && row < r1 - r0) sm.seen[ct & 3][row][w] = bitsw;
+          }
         }
       }
-      sm.kz[ct & 3][tl] = kz;
+      sm.kz[ct & 3][tl] = kz;  // 8 warps: lanes 16-31 repeat lanes 0-15
       tc_wait_st();
       tc_before();
       __syncwarp();
@@ -633,13 +706,14 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t 
 // Values of a packed tile in the ring.  CHECK: some of its tokens do not exist
 // (n groups do; group part only its first valid tokens): they become zeros, as
 // P is zero there and stale codes with a stale range may be anything.
-template <int BITS, bool CHECK>
-__device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int n, int part, int valid, int w, int lane) {
+template <int BITS, bool CHECK, int GROUPS>
+__device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int n, int part, int valid, int w, int lane) {
   constexpr int gb = group_bytes(BITS);
   const int t = lane & 3;
   const uint32_t gh = splat_h(value_scale_h(BITS));
-#pragma unroll 2
-  for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
+#pragma unroll
+  for (int k2 = 0; k2 < GROUPS; k2 += 2) {
+    const int g2 = g0 + k2;
     uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -669,34 +743,38 @@ __device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int n, int 
   }
 }
 
-// Four warps: Values of every tile.  Warp w: the channels of lane units 2 w, 2 w + 1.
-template <int BITS>
-__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int w, int lane) {
-  const int t4 = lane & 3;
-  uint32_t ct = 0, rc = 0;
+// Values of every tile.  Warp w of WARPS: the channels of lane units 2 (w % 4)
+// and + 1, of 8 warps each half of the groups.
+template <int BITS, int WARPS>
+__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int warp, int lane) {
+  const int t4 = lane & 3, w = warp & 3;
+  constexpr int kEach = 4 * kTileGroups / WARPS;  // groups per warp and tile
+  const int g0 = (warp >> 2) * kEach;
+  uint32_t ct = 0;
+  Slot sl;
+  const uint32_t tm = sm.tmem;
   while (wk.next(p)) {
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
-      const uint32_t ta = sm.tmem + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
+      const uint32_t ta = tm + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
       tree_wait(&sm.v_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
       if (t < p.tp) {
-        const int slot = rc % p.stages;
-        tree_wait(&sm.ring_full[slot], (rc / p.stages) & 1, p.a.err, &sm.abort);
+        tree_wait(&sm.ring_full[sl.i], sl.phase, p.a.err, &sm.abort);
         tc_after();
-        const FromRing st{ring + (uint32_t)(slot * p.stage_bytes)};
-        const int n = (int)min((long long)kTileGroups, p.f.gps - (long long)t * kTileGroups);
+        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
+        const int n = min(kTileGroups, p.groups - t * kTileGroups);
         const int part = p.part_group - t * kTileGroups;
         if (n == kTileGroups && (unsigned)part >= (unsigned)kTileGroups)
-          value_tile<BITS, false>(st, ta, n, part, p.part_valid, w, lane);
+          value_tile<BITS, false, kEach>(st, ta, g0, n, part, p.part_valid, w, lane);
         else
-          value_tile<BITS, true>(st, ta, n, part, p.part_valid, w, lane);
-        rc++;
+          value_tile<BITS, true, kEach>(st, ta, g0, n, part, p.part_valid, w, lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
+        if (lane == 0) mbar_arrive(&sm.ring_free[sl.i]);
+        sl.step(p.stages);
       } else {
         tc_after();
 #pragma unroll 1
-        for (int g2 = 0; g2 < kTileGroups; g2 += 2) {
+        for (int g2 = g0; g2 < g0 + kEach; g2 += 2) {
           uint32_t o0[8], o1[8];
 #pragma unroll
           for (int i = 0; i < 2; i++) {
@@ -743,22 +821,26 @@ __device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_
   }
 }
 
-// One thread per half: the MMAs of the half's tiles.
+// One warp per half: the MMAs of the half's tiles.
 template <int COLS, bool DUAL>
 __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t q_smem, uint32_t p_smem, Walk wk, int half) {
   constexpr uint32_t kDescQk = mma_desc(COLS, false), kDescPv = mma_desc(COLS, true);
   const uint32_t tm = sm.tmem;
+  const uint64_t q_desc = smem_desc(q_smem), p_desc = smem_desc(p_smem);
   uint32_t ct = 0, n = 0, seg = 0;  // tiles of the CTA, tiles of this half, segments with tiles of this half
   auto pv = [&](uint32_t tile, uint32_t i, bool first) {
     const int buf = tile & 1;
     tree_wait(&sm.v_full[buf], (tile >> 1) & 1, p.a.err, &sm.abort);
     tree_wait(&sm.p_full[half], i & 1, p.a.err, &sm.abort);
     tc_after();
+    if (elect_one()) {
 #pragma unroll
-    for (int k = 0; k < 8; k++)
-      tc_mma(tm + kColO + 64 * half, tm + kColV + 64 * buf + 8 * k, smem_desc(p_smem + 2048 * k), kDescPv, !(first && k == 0));
-    tc_commit(&sm.v_free[buf]);
-    tc_commit(&sm.pv_done[half]);
+      for (int k = 0; k < 8; k++)
+        tc_mma(tm + kColO + 64 * half, tm + kColV + 64 * buf + 8 * k, p_desc + (2048 >> 4) * k, kDescPv, !(first && k == 0));
+      tc_commit(&sm.v_free[buf]);
+      tc_commit(&sm.pv_done[half]);
+    }
+    __syncwarp();
   };
   while (wk.next(p)) {
     bool any = false;
@@ -771,12 +853,15 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
       tree_wait(&sm.k_full[buf], (ct >> 1) & 1, p.a.err, &sm.abort);
       tree_wait(&sm.s_free[half], (n & 1) ^ 1, p.a.err, &sm.abort);
       tc_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 8; k++)
-        tc_mma(tm + kColS + 64 * half, tm + kColK + 64 * buf + 8 * k, smem_desc(q_smem + (k >> 2) * (kQBytes / 2) + 32 * (k & 3)),
-               kDescQk, k > 0);
-      tc_commit(&sm.k_free[buf]);
-      tc_commit(&sm.s_full[half]);
+        for (int k = 0; k < 8; k++)
+          tc_mma(tm + kColS + 64 * half, tm + kColK + 64 * buf + 8 * k,
+                 q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, k > 0);
+        tc_commit(&sm.k_free[buf]);
+        tc_commit(&sm.s_full[half]);
+      }
+      __syncwarp();
       if (any) pv(prev, n - 1, prev_first);
       prev = ct;
       prev_first = !any;
@@ -788,60 +873,93 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
       seg++;
     }
   }
-  tc_commit(&sm.drain[half]);
+  if (elect_one()) tc_commit(&sm.drain[half]);
+  __syncwarp();
   drain_wait(&sm.drain[half], 0);
 }
 
-// A warpgroup: softmax of the half's tiles, and the segment's results.
+// Sum or maximum over the warp's lanes of N values a lane: every exchange halves
+// the values a lane carries.  N >= 32: lane L ends with values 0 .. N/32 - 1 of
+// columns L N/32 ...; N = 16: with column L / 2.
+template <int N, bool MAX>
+__device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int o = 16, len = N; o; o >>= 1) {
+    if (len > 1) {
+      len /= 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; i++) {
+        if (i < len) {
+          const float keep = (lane & o) ? v[i + len] : v[i], send = (lane & o) ? v[i] : v[i + len];
+          v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      }
+    } else {
+      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+}
+
+// A warpgroup: softmax of C of the half's columns (from column cb on) in the
+// half's tiles, and the segment's results for them.
 template <int COLS, bool DUAL>
-__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8_t* q_smem, uint8_t* p_all, Walk wk, int half,
+__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8_t* q_smem, uint8_t* p_all, Walk wk, int wg,
                                              int tl) {
-  constexpr int CH = COLS < 32 ? COLS : 32;
+  using S = Split<COLS>;
+  constexpr int C = S::kCols;
+  static_assert(C == 16 || C == 32);
+  constexpr int kSoftThreads = 32 * S::kSoft;
   const TreeArgs& a = p.a;
+  const int half = wg / S::kSubs, cb = (wg % S::kSubs) * C;
   const int w = tl >> 5, lane = tl & 31;
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
-  const uint32_t ts = sm.tmem + kColS + 64 * half + lanes, to = sm.tmem + kColO + 64 * half + lanes;
+  const uint32_t ts = sm.tmem + kColS + 64 * half + cb + lanes, to = sm.tmem + kColO + 64 * half + cb + lanes;
   uint8_t* p_smem = p_all + half * kPBytes;
-  float4* col = sm.col[half];
-  const int id = 1 + half;
+  float4* col = sm.col[half] + cb / 2;
+  const int id = 1 + wg;  // barriers 1 .. 4: one warpgroup; 5: every softmax thread; 6, 7: one half
   uint32_t ct = 0, n = 0;
   const float out_scale = 1.0f / value_scale(a.c.bits);
   while (wk.next(p)) {
     const int b = wk.s / a.c.kv_heads, j = wk.s - b * a.c.kv_heads;
-    const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0);
-    const int nr = max(0, min(p.rows, wk.block * p.block_rows + p.block_rows) - r0);  // rows of this half (may exceed COLS in no case)
-    const int first_ct = ct;
-    (void)first_ct;
-    int mine = 0;  // tiles of this half in the segment
-    if (DUAL)
-      mine = wk.t1 - wk.t0;
-    else
-      mine = (int)((wk.t1 - wk.t0 + ((ct & 1) == (uint32_t)half ? 1 : 0)) >> 1);
-    float2 l2[COLS / 2];
+    const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0) + cb;  // first row of these columns
+    const int nr = min(C, min(p.rows, (wk.block + 1) * p.block_rows) - r0);       // rows that exist (may be <= 0)
+    // tiles of this half in the segment
+    const int mine = DUAL ? wk.t1 - wk.t0 : (wk.t1 - wk.t0 + ((ct & 1) == (uint32_t)half ? 1 : 0)) >> 1;
+    float2 l2[C / 2];
 #pragma unroll
-    for (int i = 0; i < COLS / 2; i++) l2[i] = make_float2(0.f, 0.f);
+    for (int i = 0; i < C / 2; i++) l2[i] = make_float2(0.f, 0.f);
     if (mine > 0) {
       // ---- q' = q lambda sm_scale log2(e) as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
       const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
                                  : make_float4(1.f, 1.f, 1.f, 1.f);
-#pragma unroll 4
-      for (int r = w; r < COLS; r += 4) {
-        uint2 raw = make_uint2(0u, 0u);
+      uint2 raw[C / 4];
+#pragma unroll
+      for (int i = 0; i < C / 4; i++) {
+        const int r = w + 4 * i;
+        raw[i] = make_uint2(0u, 0u);
         if (r < nr) {
           const int row = r0 + r, node = row / a.group, g = row - node * a.group;
-          raw = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t +
-                                                (long long)(j * a.group + g) * a.q_h + 4 * lane);
+          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t +
+                                                   (long long)(j * a.group + g) * a.q_h + 4 * lane);
         }
-        const float x0 = __uint_as_float(raw.x << 16) * a.qscale * lam.x, x1 = __uint_as_float(raw.x & 0xffff0000u) * a.qscale * lam.y;
-        const float x2 = __uint_as_float(raw.y << 16) * a.qscale * lam.z, x3 = __uint_as_float(raw.y & 0xffff0000u) * a.qscale * lam.w;
+      }
+#pragma unroll
+      for (int i = 0; i < C / 4; i++) {
+        const int r = w + 4 * i, rs = cb + r;  // row of the half's Q
+        const float x0 = __uint_as_float(raw[i].x << 16) * a.qscale * lam.x;
+        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * a.qscale * lam.y;
+        const float x2 = __uint_as_float(raw[i].y << 16) * a.qscale * lam.z;
+        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * a.qscale * lam.w;
         const uint32_t h02 = sat_h2(x0, x2), h13 = sat_h2(x1, x3);
-        const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02)), f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
+        const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02));
+        const float2 f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
         float sum = (f02.x + f02.y) + (f13.x + f13.y);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int chunk = (lane & 15) >> 1;
-        *reinterpret_cast<uint2*>(q_smem + half * kQBytes + (lane >> 4) * (kQBytes / 2) + r * 128 + ((chunk ^ (r & 7)) << 4) +
-                                  8 * (lane & 1)) = make_uint2(h02, h13);
+        *reinterpret_cast<uint2*>(q_smem + half * kQBytes + (lane >> 4) * (kQBytes / 2) + rs * 128 +
+                                  ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) = make_uint2(h02, h13);
         if (lane == 0) {
           float* cp = reinterpret_cast<float*>(&col[r >> 1]);
           cp[r & 1] = sum;
@@ -856,104 +974,99 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
     int done = 0;
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       if (!DUAL && (ct & 1) != (uint32_t)half) continue;
+      // which columns' rows do not see this thread's token
+      uint32_t hide = 0u;
+      if (t >= p.tp || t * kTileGroups + kTileGroups > p.groups || (unsigned)(p.part_group - t * kTileGroups) < (unsigned)kTileGroups)
+        hide = token_valid(p, t, tl) ? 0u : 0xffffffffu;
       tree_wait(&sm.s_full[half], n & 1, a.err, &sm.abort);
       tc_after();
       const float2 kz = sm.kz[ct & 3][tl];
-      const bool valid = token_valid(p, t, tl);
-      const bool draft = t >= p.tp + p.tw;
-      const uint32_t(*seen)[4] = sm.seen[ct & 3] + (DUAL ? half * kHalfRows : 0);
+      if (t >= p.tp + p.tw && hide == 0u) {
+        const uint32_t(*seen)[4] = sm.seen[ct & 3] + (DUAL ? half * kHalfRows : 0) + cb;
 #pragma unroll
-      for (int c0 = 0; c0 < COLS; c0 += CH) {
-        uint32_t d[CH];
-        tc_ld(d, ts + c0);
-        float2 x[CH / 2];
-        const float2 rk = splat2(kz.x), zk = splat2(kz.y);
-        float mx = -INFINITY;
+        for (int i = 0; i < C; i++) hide |= (seen[i][w] >> lane & 1u) ? 0u : 1u << i;
+      }
+      const float2 rk = splat2(kz.x), zk = splat2(kz.y);
+      float2 x[C / 2];
+      auto scores = [&](bool relative) {  // into x, less the running maxima or not
+        uint32_t d[C];
+        tc_ld(d, ts);
 #pragma unroll
-        for (int i = 0; i < CH / 2; i++) {
-          const float4 cp = col[c0 / 2 + i];
+        for (int i = 0; i < C / 2; i++) {
+          const float4 cp = col[i];
           x[i] = fma2(rk, make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])),
-                      fma2(make_float2(cp.x, cp.y), zk, make_float2(cp.z, cp.w)));
-        }
-        // rows that do not see the token
-        uint32_t hide = valid ? 0u : 0xffffffffu;  // bit i: row c0 + i does not see this token
-        if (draft && valid) {
-#pragma unroll
-          for (int i = 0; i < CH; i++) hide |= ((seen[c0 + i][w] >> lane) & 1u) ? 0u : 1u << i;
+                      fma2(make_float2(cp.x, cp.y), zk, relative ? make_float2(cp.z, cp.w) : make_float2(0.f, 0.f)));
         }
         if (hide) {
 #pragma unroll
-          for (int i = 0; i < CH / 2; i++) {
+          for (int i = 0; i < C / 2; i++) {
             if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
             if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
           }
         }
+      };
+      scores(true);
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < CH / 2; i++) mx = fmaxf(mx, fmaxf(x[i].x, x[i].y));
-        if (bar_or(id, 128, mx > kRebase)) {
-          // From the scores themselves (a row's first ones were taken against no
-          // maximum); S and O are read again rather than held beside each other.
-          auto score = [&](int i) {
-            const float4 cp = col[c0 / 2 + i / 2];
-            return (hide >> i & 1u) ? -INFINITY : fmaf(kz.x, __uint_as_float(d[i]), (i & 1 ? cp.y : cp.x) * kz.y);
-          };
-          tc_ld(d, ts + c0);
-          float mine_max = -INFINITY;
+      for (int i = 0; i < C / 2; i++) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(x[i].x, x[i].y));
+      if (bar_or(id, 128, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
+        // Column maxima from the scores themselves (a row's first ones were taken
+        // against no maximum); S is read again rather than held.
+        scores(false);
+        {
+          float v[C];
 #pragma unroll
-          for (int i = 0; i < CH; i++) {
-            const float m = warp_max_f32(score(i));
-            if (lane == i) mine_max = m;
-          }
-          if (lane < CH) sm.red[half][w][c0 + lane] = mine_max;
-          bar_sync(id, 128);
-          if (tl < CH) {
-            const int c = c0 + tl;
-            float* cp = reinterpret_cast<float*>(&col[c >> 1]) + 2 + (c & 1);
-            const float neg = *cp;
-            float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
-            float f = 0.f;
-            if (neg != kUnset) {
-              m = fmaxf(m, -neg);
-              f = ex2(-neg - m);
-            }
-            sm.alpha[half][c] = f;
-            *cp = m == -INFINITY ? kUnset : -m;  // a row that has seen nothing stays unset
-          }
-          bar_sync(id, 128);
-          if (done > 0) {  // O so far, once the last product is in
-            tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
-            tc_after();
-            tc_ld(d, to + c0);
-#pragma unroll
-            for (int i = 0; i < CH; i++) d[i] = __float_as_uint(__uint_as_float(d[i]) * sm.alpha[half][c0 + i]);
-            tc_st(to + c0, d);
-            tc_wait_st();
-          }
-          tc_ld(d, ts + c0);
-#pragma unroll
-          for (int i = 0; i < CH / 2; i++) {
-            const float4 cp = col[c0 / 2 + i];
-            l2[c0 / 2 + i] = mul2(l2[c0 / 2 + i], make_float2(sm.alpha[half][c0 + 2 * i], sm.alpha[half][c0 + 2 * i + 1]));
-            x[i] = add2(make_float2(score(2 * i), score(2 * i + 1)), make_float2(cp.z, cp.w));
-          }
+          for (int i = 0; i < C / 2; i++) { v[2 * i] = x[i].x; v[2 * i + 1] = x[i].y; }
+          warp_columns<C, true>(v, lane);
+          sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
         }
-        if (c0 + CH == COLS) {  // S is in registers: the next tile's product may start
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_free[half]);
-        }
-        if (c0 == 0 && done > 0) tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);  // P is free again
-#pragma unroll
-        for (int q = 0; q < CH / 8; q++) {
-          uint32_t h[4];
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float2 pr = make_float2(ex2(x[4 * q + e].x), ex2(x[4 * q + e].y));
-            l2[c0 / 2 + 4 * q + e] = add2(l2[c0 / 2 + 4 * q + e], pr);
-            h[e] = pack_h2(pr.x, pr.y);
+        bar_sync(id, 128);
+        if (tl < C) {
+          const int c = cb + tl;
+          float* cp = reinterpret_cast<float*>(&col[tl >> 1]) + 2 + (tl & 1);
+          const float neg = *cp;
+          float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
+          float f = 0.f;
+          if (neg != kUnset) {
+            m = fmaxf(m, -neg);
+            f = ex2(-neg - m);
           }
-          *reinterpret_cast<uint4*>(p_smem + tl * 128 + (((c0 / 8 + q) ^ (tl & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          sm.alpha[half][c] = f;
+          *cp = m == -INFINITY ? kUnset : -m;  // a row that has seen nothing stays unset
         }
+        bar_sync(id, 128);
+        const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
+        if (done > 0) {  // O so far, once the last product is in
+          tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
+          tc_after();
+          uint32_t o[C];
+          tc_ld(o, to);
+#pragma unroll
+          for (int i = 0; i < C / 2; i++) {
+            const float2 f = al[i];
+            o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * f.x);
+            o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * f.y);
+            l2[i] = mul2(l2[i], f);
+          }
+          tc_st(to, o);
+          tc_wait_st();
+        }
+        scores(true);
+      }
+      tc_before();  // S is in registers: the next tile's product may start
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.s_free[half]);
+      if (done > 0) tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);  // P is free again
+#pragma unroll
+      for (int q = 0; q < C / 8; q++) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float2 pr = make_float2(ex2(x[4 * q + e].x), ex2(x[4 * q + e].y));
+          l2[4 * q + e] = add2(l2[4 * q + e], pr);
+          h[e] = pack_h2(pr.x, pr.y);
+        }
+        *reinterpret_cast<uint4*>(p_smem + tl * 128 + (((cb / 8 + q) ^ (tl & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
       fence_async_smem();
       tc_before();
@@ -963,38 +1076,19 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       done++;
     }
     // ---- the segment's results ----
-    // row sums: halve the rows a lane carries with every exchange
     {
-      float v[COLS];
+      float v[C];
 #pragma unroll
-      for (int i = 0; i < COLS / 2; i++) { v[2 * i] = l2[i].x; v[2 * i + 1] = l2[i].y; }
-      int len = COLS;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        if (len > 1) {
-          len /= 2;
-#pragma unroll
-          for (int i = 0; i < COLS / 2; i++) {
-            if (i < len) {
-              const float keep = (lane & o) ? v[i + len] : v[i], send = (lane & o) ? v[i] : v[i + len];
-              v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
-          }
-        } else {
-          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        }
-      }
-      constexpr int kLeft = COLS >= 32 ? COLS / 32 : 1;
-      const int c = COLS >= 32 ? lane * kLeft : lane / (32 / COLS);
-#pragma unroll
-      for (int i = 0; i < kLeft; i++) sm.red[half][w][c + i] = v[i];
+      for (int i = 0; i < C / 2; i++) { v[2 * i] = l2[i].x; v[2 * i + 1] = l2[i].y; }
+      warp_columns<C, false>(v, lane);
+      sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
     }
     bar_sync(id, 128);
-    if (tl < COLS) {
-      const float* r = &sm.red[half][0][tl];
+    if (tl < C) {
+      const float* r = &sm.red[half][0][cb + tl];
       const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
       const float neg = mine > 0 ? reinterpret_cast<const float*>(&col[tl >> 1])[2 + (tl & 1)] : kUnset;
-      sm.ml[half][tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
+      sm.ml[half][cb + tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
     }
     if (mine > 0) {
       tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
@@ -1002,120 +1096,120 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
     }
     const bool whole = wk.t0 == 0 && wk.t1 == p.tiles;
     // this CTA's records: 0 for the segment its share begins in, else 1
-    const int x = wk.s * p.blocks + wk.block, begin = cta_begin(p.units, p.grid, blockIdx.x);
-    float* rec = p.parts + ((size_t)blockIdx.x * 2 + (x * p.tiles + wk.t0 == begin ? 0 : 1)) * p.rec;
-    __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(a.out);
-    auto row_at = [&](int r) {  // output row of row r of this half
-      const int row = r0 + r, node = row / a.group, g = row - node * a.group;
-      return outp + (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim;
-    };
-    // rows of bf16 leave from shared memory, 16 bytes a thread
-    auto flush = [&](const uint8_t* sh, int c0, int cnt) {
-      for (int i = tl; i < cnt * 16; i += 128) {
+    const int xi = wk.s * p.blocks + wk.block, begin = cta_begin(p.units, p.grid, blockIdx.x);
+    float* rec = p.parts + ((size_t)blockIdx.x * 2 + (xi * p.tiles + wk.t0 == begin ? 0 : 1)) * p.rec;
+    const int rr = (DUAL ? half * kHalfRows : 0) + cb;  // first row within the block
+    // C rows of bf16 leave from shared memory, 16 bytes a thread
+    auto flush = [&](const uint8_t* sh) {
+      for (int i = tl; i < C * 16; i += 128) {
         const int r = i >> 4, q = i & 15;
-        if (c0 + r < nr) reinterpret_cast<uint4*>(row_at(c0 + r))[q] = *reinterpret_cast<const uint4*>(sh + r * 256 + 16 * q);
+        if (r < nr) {
+          const int row = r0 + r, node = row / a.group, g = row - node * a.group;
+          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                   (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim)[q] =
+              *reinterpret_cast<const uint4*>(sh + r * 256 + 16 * q);
+        }
       }
     };
     const int ch = channel_of(tl);
     if constexpr (DUAL) {
       bar_sync(id, 128);  // ml
-#pragma unroll 1
-      for (int c0 = 0; c0 < COLS; c0 += CH) {
-        uint32_t o[CH];
-        tc_ld(o, to + c0);
-        if (whole) {
-#pragma unroll
-          for (int i = 0; i < CH; i++) {
-            const float l = sm.ml[half][c0 + i].y;
-            reinterpret_cast<__nv_bfloat16*>(p_smem)[(c0 + i) * kHeadDim + ch] =
-                __float2bfloat16_rn(l != 0.f ? __uint_as_float(o[i]) * out_scale / l : 0.f);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < CH; i++)
-            if (c0 + i < nr) rec[2 * p.block_rows + (half * kHalfRows + c0 + i) * kHeadDim + tl] = __uint_as_float(o[i]);
-        }
-      }
+      uint32_t o[C];
+      tc_ld(o, to);
       tc_before();
       if (whole) {
+        uint8_t* sh = p_smem + (wg % S::kSubs) * (C * 256);
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+          const float l = sm.ml[half][cb + i].y;
+          reinterpret_cast<__nv_bfloat16*>(sh)[i * kHeadDim + ch] =
+              __float2bfloat16_rn(l != 0.f ? __uint_as_float(o[i]) * out_scale / l : 0.f);
+        }
         bar_sync(id, 128);
-        flush(p_smem, 0, COLS);
-        bar_sync(id, 128);  // P is written again
-      } else if (tl < nr) {
-        rec[half * kHalfRows + tl] = sm.ml[half][tl].x;
-        rec[p.block_rows + half * kHalfRows + tl] = sm.ml[half][tl].y;
+        flush(sh);
+        bar_sync(6 + half, kSoftThreads / 2);  // P is written again
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; i++)
+          if (i < nr) rec[2 * p.block_rows + (rr + i) * kHeadDim + tl] = __uint_as_float(o[i]);
+        if (tl < nr) {
+          rec[rr + tl] = sm.ml[half][cb + tl].x;
+          rec[p.block_rows + rr + tl] = sm.ml[half][cb + tl].y;
+        }
       }
     } else {
       // join the halves: half 1 hands its O over in shared memory (both P areas: [COLS][128] fp32)
-      bar_sync(3, 256);  // ml of both; every product of both halves is in
-      float* xb = reinterpret_cast<float*>(p_all);
-      auto joint = [&](int c, float& f0, float& f1, float& m, float& l) {
-        const float2 m0 = sm.ml[0][c], m1 = sm.ml[1][c];
-        m = fmaxf(m0.x, m1.x);
-        f0 = m0.y != 0.f ? ex2(m0.x - m) : 0.f;
-        f1 = m1.y != 0.f ? ex2(m1.x - m) : 0.f;
-        l = m0.y * f0 + m1.y * f1;
-      };
+      bar_sync(5, kSoftThreads);  // ml of both; every product of both halves is in
+      float* xb = reinterpret_cast<float*>(p_all) + cb * kTile;
       if (half == 1 && mine > 0) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < COLS; c0 += CH) {
-          uint32_t o[CH];
-          tc_ld(o, to + c0);
+        uint32_t o[C];
+        tc_ld(o, to);
 #pragma unroll
-          for (int i = 0; i < CH; i++) xb[(c0 + i) * kTile + tl] = __uint_as_float(o[i]);
-        }
+        for (int i = 0; i < C; i++) xb[i * kTile + tl] = __uint_as_float(o[i]);
       }
       tc_before();
-      bar_sync(3, 256);
+      bar_sync(5, kSoftThreads);
       if (half == 0) {
         const int other = wk.t1 - wk.t0 - mine;
-#pragma unroll 1
-        for (int c0 = 0; c0 < COLS; c0 += CH) {
-          uint32_t o[CH];
-          if (mine > 0) tc_ld(o, to + c0);
+        uint32_t o[C];
+        if (mine > 0) {
+          tc_ld(o, to);
+          tc_before();
+        }
 #pragma unroll
-          for (int i = 0; i < CH; i++) {
-            float f0, f1, m, l;
-            joint(c0 + i, f0, f1, m, l);
-            float v = mine > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
-            if (other > 0) v = fmaf(xb[(c0 + i) * kTile + tl], f1, v);
-            if (whole)
-              o[i] = __float_as_uint(l != 0.f ? v * out_scale / l : 0.f);
-            else if (c0 + i < nr)
-              rec[2 * p.block_rows + (c0 + i) * kHeadDim + tl] = v;
-          }
+        for (int i = 0; i < C; i++) {
+          const float2 m0 = sm.ml[0][cb + i], m1 = sm.ml[1][cb + i];
+          const float m = fmaxf(m0.x, m1.x);
+          const float f0 = m0.y != 0.f ? ex2(m0.x - m) : 0.f, f1 = m1.y != 0.f ? ex2(m1.x - m) : 0.f;
+          float v = mine > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
+          if (other > 0) v = fmaf(xb[i * kTile + tl], f1, v);
+          const float l = m0.y * f0 + m1.y * f1;
           if (whole) {
-            bar_sync(id, 128);  // these rows of xb are read
-#pragma unroll
-            for (int i = 0; i < CH; i++)
-              reinterpret_cast<__nv_bfloat16*>(p_all + c0 * kTile * 4)[i * kHeadDim + ch] = __float2bfloat16_rn(__uint_as_float(o[i]));
-            bar_sync(id, 128);
-            flush(p_all + c0 * kTile * 4, c0, CH);
+            o[i] = __float_as_uint(l != 0.f ? v * out_scale / l : 0.f);
+          } else if (i < nr) {
+            rec[2 * p.block_rows + (rr + i) * kHeadDim + tl] = v;
+            if (tl == i) {
+              rec[rr + i] = m;
+              rec[p.block_rows + rr + i] = l;
+            }
           }
         }
-        if (!whole && tl < nr) {
-          float f0, f1, m, l;
-          joint(tl, f0, f1, m, l);
-          rec[tl] = m;
-          rec[p.block_rows + tl] = l;
+        if (whole) {
+          bar_sync(id, 128);  // xb is read
+          uint8_t* sh = reinterpret_cast<uint8_t*>(xb);
+#pragma unroll
+          for (int i = 0; i < C; i++)
+            reinterpret_cast<__nv_bfloat16*>(sh)[i * kHeadDim + ch] = __float2bfloat16_rn(__uint_as_float(o[i]));
+          bar_sync(id, 128);
+          flush(sh);
         }
-        tc_before();
       }
-      bar_sync(3, 256);  // P and ml are written again
+      bar_sync(5, kSoftThreads);  // P and ml are written again
     }
   }
 }
 
+template <int REGS>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 template <int COLS, bool DUAL>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreePlan p) {
+  using S = Split<COLS>;
+  constexpr int kKey0 = S::kSoft, kValue0 = kKey0 + S::kWiden, kCtl0 = kValue0 + S::kWiden;
   extern __shared__ uint8_t raw[];
   uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint8_t* q_smem = base;
   uint8_t* p_smem = base + 2 * kQBytes;
   Small& sm = *reinterpret_cast<Small*>(base + 2 * kQBytes + 2 * kPBytes);
   uint8_t* ring = base + kFixedBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 19) {
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (warp == kCtl0 + 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -1123,17 +1217,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     sm.abort = 0;
     for (int i = 0; i < kMaxStages; i++) {
       mbar_init(smem_u32(&sm.ring_full[i]), 1);
-      mbar_init(smem_u32(&sm.ring_free[i]), 8);
+      mbar_init(smem_u32(&sm.ring_free[i]), 2 * S::kWiden);
     }
     for (int i = 0; i < 2; i++) {
-      mbar_init(smem_u32(&sm.k_full[i]), 4);
+      mbar_init(smem_u32(&sm.k_full[i]), S::kWiden);
       mbar_init(smem_u32(&sm.k_free[i]), DUAL ? 2 : 1);
-      mbar_init(smem_u32(&sm.v_full[i]), 4);
+      mbar_init(smem_u32(&sm.v_full[i]), S::kWiden);
       mbar_init(smem_u32(&sm.v_free[i]), DUAL ? 2 : 1);
-      mbar_init(smem_u32(&sm.q_full[i]), 4);
+      mbar_init(smem_u32(&sm.q_full[i]), S::kSoft / 2);
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.s_free[i]), 4);
-      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.s_free[i]), S::kSoft / 2);
+      mbar_init(smem_u32(&sm.p_full[i]), S::kSoft / 2);
       mbar_init(smem_u32(&sm.pv_done[i]), 1);
       mbar_init(smem_u32(&sm.drain[i]), 1);
     }
@@ -1143,35 +1237,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   __syncthreads();
   tc_after();
   pdl_wait();  // the cache, q, k, v and the mask may be written by earlier kernels
-  Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
-  // 640 x 96 registers at launch; 2 x 128 x 144 + 2 x 128 x 80 + 128 x 32 = 61440
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+  const Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
+  if (warp < kKey0) {
+    if constexpr (S::kSoftRegs > 72) regs_up<S::kSoftRegs>(); else regs_down<S::kSoftRegs>();
     softmax_role<COLS, DUAL>(p, sm, q_smem, p_smem, wk, warp >> 2, threadIdx.x & 127);
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    switch (p.a.c.bits) {
-      case 2: key_role<2>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      case 4: key_role<4>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      case 8: key_role<8>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      default: key_role<16>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-    }
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    switch (p.a.c.bits) {
-      case 2: value_role<2>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      case 4: value_role<4>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      case 8: value_role<8>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
-      default: value_role<16>(p, sm, smem_u32(ring), wk, warp & 3, lane); break;
+  } else if (warp < kCtl0) {
+    if constexpr (S::kWidenRegs > 72) regs_up<S::kWidenRegs>(); else regs_down<S::kWidenRegs>();
+    if (warp < kValue0) {
+      switch (p.a.c.bits) {
+        case 2: key_role<2, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
+        case 4: key_role<4, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
+        case 8: key_role<8, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
+        default: key_role<16, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
+      }
+    } else {
+      switch (p.a.c.bits) {
+        case 2: value_role<2, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
+        case 4: value_role<4, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
+        case 8: value_role<8, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
+        default: value_role<16, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
+      }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (warp == 16) {
-      if (lane == 0) produce(p, sm, ring, wk);
-    } else if (warp < 19) {
-      const int half = warp - 17;
-      if (lane == 0)
-        mma_role<COLS, DUAL>(p, sm, smem_u32(q_smem) + half * kQBytes, smem_u32(p_smem) + half * kPBytes, wk, half);
+    regs_down<S::kCtlRegs>();
+    if (warp == kCtl0) {
+      produce(p, sm, smem_u32(ring), wk);
+    } else if (warp < kCtl0 + 3) {
+      const int half = warp - kCtl0 - 1;
+      mma_role<COLS, DUAL>(p, sm, smem_u32(q_smem) + half * kQBytes, smem_u32(p_smem) + half * kPBytes, wk, half);
     }
     __syncwarp();
   }
@@ -1179,7 +1272,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   __syncthreads();
   pdl_launch_dependents();
   tc_after();
-  if (warp == 19) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
+  if (warp == kCtl0 + 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
 }
 
 // Joins the partial records of one block of rows: a CTA per (stream, block of
@@ -1250,14 +1343,12 @@ cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
   p.blocks = (p.rows + p.block_rows - 1) / p.block_rows;
   p.part_group = -1;
   if (a.c.n_prog > 0) {
-    if (a.c.kmc) p.f.gps = a.c.n_prog / kGroupTokens;  // whole blocks, all full
-    p.tp = (int)((p.f.gps + kTileGroups - 1) / kTileGroups);
+    p.groups = (int)(a.c.kmc ? a.c.n_prog / kGroupTokens : f.gps);  // per-channel groups: whole blocks, all full
+    p.tp = (p.groups + kTileGroups - 1) / kTileGroups;
     if (!a.c.kmc && f.k < f.nt && (f.h + f.r) % kGroupTokens) {  // tile k's last group
       p.part_group = f.k * f.gpt + f.gk - 1;
       p.part_valid = (f.h + f.r) % kGroupTokens;
     }
-  } else {
-    p.f.gps = 0;
   }
   p.tw = (a.c.n_win + kTile - 1) / kTile;
   p.td = (a.n + kTile - 1) / kTile;

@@ -124,27 +124,22 @@ __host__ __device__ __forceinline__ int cta_of(int units, int grid, int u) {
 
 // ------------------------------------------------------------------ PTX
 
-// A test that may suspend the warp for some microseconds: fewer polls.
-__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait: gives up after kWaitNs or once another wait of the CTA has.
-__device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort) {
-  const uint32_t b = smem_u32(bar);
-  if (mbar_try_long(b, parity)) return;
-  const unsigned long long t0 = global_ns();
-  while (!mbar_try_long(b, parity)) {
+// Bounded wait: gives up after kWaitNs or once another wait of the CTA has.  The
+// test itself suspends the warp for a while; the clock is read on few of them.
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+  if (mbar_try(bar, parity)) return;
+  unsigned it = 0;
+  unsigned long long t0 = 0;
+  while (!mbar_try(bar, parity)) {
     if (*abort) return;
-    if (global_ns() - t0 > kWaitNs) {
-      *abort = 1;
-      atomicExch(err, 1);
-      return;
+    if ((++it & 255u) == 0u) {
+      const unsigned long long now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) {
+        *abort = 1;
+        atomicExch(err, 1);
+        return;
+      }
     }
   }
 }
@@ -158,19 +153,19 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // Also after an abort: what is in flight lands before the CTA ends.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = global_ns();
-  while (!mbar_try(smem_u32(bar), parity))
+  while (!mbar_try(bar, parity))
     if (global_ns() - t0 > kWaitNs) break;
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -430,6 +425,9 @@ __device__ __forceinline__ float value_scale(int bits) {
 
 // ------------------------------------------------------------------ roles
 
+// Shared address of barrier i of an array in Small, from that of Small (sb).
+#define KVQ_BAR(array, i) (sb + (uint32_t)offsetof(Small, array) + 8u * (uint32_t)(i))
+
 // One CTA's walk over its share: segments (a stream's block of rows), tiles.
 struct Walk {
   int u, end;               // units left
@@ -470,7 +468,7 @@ struct Slot {
 
 // Producer (one warp): packed progressive tiles into the ring, run by run (groups
 // that neighbour in one tile of the cache).
-__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t ring, Walk wk) {
+__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk) {
   const CacheView& c = p.a.c;
   const Fill& f = p.f;
   const int gb = group_bytes(c.bits);
@@ -489,10 +487,10 @@ __device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t r
       groups = loc.tile_groups;
     }
     for (int t = wk.t0; t < min(wk.t1, p.tp); t++, sent++) {
-      tree_wait(&sm.ring_free[sl.i], sl.phase ^ 1, p.a.err, &sm.abort);
+      tree_wait(KVQ_BAR(ring_free, sl.i), sl.phase ^ 1, p.a.err, &sm.abort);
       if (sm.abort) goto out;
       const uint32_t st = ring + (uint32_t)(sl.i * p.stage_bytes);
-      const uint32_t bar = smem_u32(&sm.ring_full[sl.i]);
+      const uint32_t bar = KVQ_BAR(ring_full, sl.i);
       const int n = min(kTileGroups, p.groups - t * kTileGroups);
       if (elect_one()) {
         mbar_expect_tx(bar, (uint32_t)n * (gb + 128u) + (chan ? 4u * kHeadDim : 0u));
@@ -537,7 +535,7 @@ out:
     for (uint32_t i = 0; i < k; i++) {
       sl.i = sl.i == 0 ? p.stages - 1 : sl.i - 1;
       if (sl.i == p.stages - 1) sl.phase ^= 1;
-      drain_wait(&sm.ring_full[sl.i], sl.phase);
+      drain_wait(KVQ_BAR(ring_full, sl.i), sl.phase);
     }
   }
 }
@@ -625,7 +623,7 @@ __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, f
 // tiles, which rows see them.  Warp w of WARPS: tokens 32 (w % 4) .. + 31, of 8
 // warps each takes one of the two groups.
 template <int BITS, int WARPS>
-__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int warp, int lane) {
+__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int warp, int lane) {
   const CacheView& c = p.a.c;
   constexpr int gb = group_bytes(BITS), kEach = 8 / WARPS;  // groups per warp and tile
   const int w = warp & 3, i0 = kEach == 1 ? warp >> 2 : 0;
@@ -636,11 +634,11 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t 
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
       const uint32_t ta = tm + kColK + 64 * buf + ((uint32_t)(32 * w) << 16);
-      tree_wait(&sm.k_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
+      tree_wait(KVQ_BAR(k_free, buf), ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
       float2 kz = make_float2(0.f, 0.f);
       const int tl = 32 * w + 16 * i0 + (kEach == 1 ? lane & 15 : lane);
       if (t < p.tp) {
-        tree_wait(&sm.ring_full[sl.i], sl.phase, p.a.err, &sm.abort);
+        tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
         tc_after();
         const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
         const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
@@ -659,7 +657,7 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t 
           kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_free[sl.i]);
+        if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
         sl.step(p.stages);
       } else if (t < p.tp + p.tw) {
         tc_after();
@@ -698,7 +696,7 @@ __device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t 
       tc_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[buf]);
+      if (lane == 0) mbar_arrive(KVQ_BAR(k_full, buf));
     }
   }
 }
@@ -746,7 +744,7 @@ __device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int
 // Values of every tile.  Warp w of WARPS: the channels of lane units 2 (w % 4)
 // and + 1, of 8 warps each half of the groups.
 template <int BITS, int WARPS>
-__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t ring, Walk wk, int warp, int lane) {
+__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int warp, int lane) {
   const int t4 = lane & 3, w = warp & 3;
   constexpr int kEach = 4 * kTileGroups / WARPS;  // groups per warp and tile
   const int g0 = (warp >> 2) * kEach;
@@ -757,9 +755,9 @@ __device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
       const uint32_t ta = tm + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
-      tree_wait(&sm.v_free[buf], ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
+      tree_wait(KVQ_BAR(v_free, buf), ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
       if (t < p.tp) {
-        tree_wait(&sm.ring_full[sl.i], sl.phase, p.a.err, &sm.abort);
+        tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
         tc_after();
         const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
         const int n = min(kTileGroups, p.groups - t * kTileGroups);
@@ -769,7 +767,7 @@ __device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_
         else
           value_tile<BITS, true, kEach>(st, ta, g0, n, part, p.part_valid, w, lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_free[sl.i]);
+        if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
         sl.step(p.stages);
       } else {
         tc_after();
@@ -816,29 +814,29 @@ __device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_
       tc_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[buf]);
+      if (lane == 0) mbar_arrive(KVQ_BAR(v_full, buf));
     }
   }
 }
 
 // One warp per half: the MMAs of the half's tiles.
 template <int COLS, bool DUAL>
-__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t q_smem, uint32_t p_smem, Walk wk, int half) {
+__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t q_smem, uint32_t p_smem, Walk wk, int half) {
   constexpr uint32_t kDescQk = mma_desc(COLS, false), kDescPv = mma_desc(COLS, true);
   const uint32_t tm = sm.tmem;
   const uint64_t q_desc = smem_desc(q_smem), p_desc = smem_desc(p_smem);
   uint32_t ct = 0, n = 0, seg = 0;  // tiles of the CTA, tiles of this half, segments with tiles of this half
   auto pv = [&](uint32_t tile, uint32_t i, bool first) {
     const int buf = tile & 1;
-    tree_wait(&sm.v_full[buf], (tile >> 1) & 1, p.a.err, &sm.abort);
-    tree_wait(&sm.p_full[half], i & 1, p.a.err, &sm.abort);
+    tree_wait(KVQ_BAR(v_full, buf), (tile >> 1) & 1, p.a.err, &sm.abort);
+    tree_wait(KVQ_BAR(p_full, half), i & 1, p.a.err, &sm.abort);
     tc_after();
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 8; k++)
         tc_mma(tm + kColO + 64 * half, tm + kColV + 64 * buf + 8 * k, p_desc + (2048 >> 4) * k, kDescPv, !(first && k == 0));
-      tc_commit(&sm.v_free[buf]);
-      tc_commit(&sm.pv_done[half]);
+      tc_commit(KVQ_BAR(v_free, buf));
+      tc_commit(KVQ_BAR(pv_done, half));
     }
     __syncwarp();
   };
@@ -849,17 +847,17 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
       if (!DUAL && buf != half) continue;
-      if (!any) tree_wait(&sm.q_full[half], seg & 1, p.a.err, &sm.abort);
-      tree_wait(&sm.k_full[buf], (ct >> 1) & 1, p.a.err, &sm.abort);
-      tree_wait(&sm.s_free[half], (n & 1) ^ 1, p.a.err, &sm.abort);
+      if (!any) tree_wait(KVQ_BAR(q_full, half), seg & 1, p.a.err, &sm.abort);
+      tree_wait(KVQ_BAR(k_full, buf), (ct >> 1) & 1, p.a.err, &sm.abort);
+      tree_wait(KVQ_BAR(s_free, half), (n & 1) ^ 1, p.a.err, &sm.abort);
       tc_after();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 8; k++)
           tc_mma(tm + kColS + 64 * half, tm + kColK + 64 * buf + 8 * k,
                  q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, k > 0);
-        tc_commit(&sm.k_free[buf]);
-        tc_commit(&sm.s_full[half]);
+        tc_commit(KVQ_BAR(k_free, buf));
+        tc_commit(KVQ_BAR(s_full, half));
       }
       __syncwarp();
       if (any) pv(prev, n - 1, prev_first);
@@ -873,9 +871,9 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
       seg++;
     }
   }
-  if (elect_one()) tc_commit(&sm.drain[half]);
+  if (elect_one()) tc_commit(KVQ_BAR(drain, half));
   __syncwarp();
-  drain_wait(&sm.drain[half], 0);
+  drain_wait(KVQ_BAR(drain, half), 0);
 }
 
 // Sum or maximum over the warp's lanes of N values a lane: every exchange halves
@@ -904,7 +902,7 @@ __device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
 // A warpgroup: softmax of C of the half's columns (from column cb on) in the
 // half's tiles, and the segment's results for them.
 template <int COLS, bool DUAL>
-__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8_t* q_smem, uint8_t* p_all, Walk wk, int wg,
+__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint32_t sb, uint8_t* q_smem, uint8_t* p_all, Walk wk, int wg,
                                              int tl) {
   using S = Split<COLS>;
   constexpr int C = S::kCols;
@@ -968,7 +966,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full[half]);
+      if (lane == 0) mbar_arrive(KVQ_BAR(q_full, half));
       bar_sync(id, 128);
     }
     int done = 0;
@@ -978,7 +976,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       uint32_t hide = 0u;
       if (t >= p.tp || t * kTileGroups + kTileGroups > p.groups || (unsigned)(p.part_group - t * kTileGroups) < (unsigned)kTileGroups)
         hide = token_valid(p, t, tl) ? 0u : 0xffffffffu;
-      tree_wait(&sm.s_full[half], n & 1, a.err, &sm.abort);
+      tree_wait(KVQ_BAR(s_full, half), n & 1, a.err, &sm.abort);
       tc_after();
       const float2 kz = sm.kz[ct & 3][tl];
       if (t >= p.tp + p.tw && hide == 0u) {
@@ -1037,7 +1035,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
         bar_sync(id, 128);
         const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
         if (done > 0) {  // O so far, once the last product is in
-          tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
+          tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);
           tc_after();
           uint32_t o[C];
           tc_ld(o, to);
@@ -1055,8 +1053,8 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       }
       tc_before();  // S is in registers: the next tile's product may start
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_free[half]);
-      if (done > 0) tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);  // P is free again
+      if (lane == 0) mbar_arrive(KVQ_BAR(s_free, half));
+      if (done > 0) tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);  // P is free again
 #pragma unroll
       for (int q = 0; q < C / 8; q++) {
         uint32_t h[4];
@@ -1071,7 +1069,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       fence_async_smem();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[half]);
+      if (lane == 0) mbar_arrive(KVQ_BAR(p_full, half));
       n++;
       done++;
     }
@@ -1091,7 +1089,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint8
       sm.ml[half][cb + tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
     }
     if (mine > 0) {
-      tree_wait(&sm.pv_done[half], (n - 1) & 1, a.err, &sm.abort);
+      tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);
       tc_after();
     }
     const bool whole = wk.t0 == 0 && wk.t1 == p.tiles;
@@ -1203,11 +1201,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   using S = Split<COLS>;
   constexpr int kKey0 = S::kSoft, kValue0 = kKey0 + S::kWiden, kCtl0 = kValue0 + S::kWiden;
   extern __shared__ uint8_t raw[];
-  uint8_t* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t raw_at = smem_u32(raw), smem_at = (raw_at + 1023u) & ~1023u;
+  const uint32_t sb = smem_at + 2 * kQBytes + 2 * kPBytes, ring_at = smem_at + kFixedBytes;
+  uint8_t* base = raw + (smem_at - raw_at);
   uint8_t* q_smem = base;
   uint8_t* p_smem = base + 2 * kQBytes;
   Small& sm = *reinterpret_cast<Small*>(base + 2 * kQBytes + 2 * kPBytes);
-  uint8_t* ring = base + kFixedBytes;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == kCtl0 + 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
@@ -1240,31 +1239,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   const Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
   if (warp < kKey0) {
     if constexpr (S::kSoftRegs > 72) regs_up<S::kSoftRegs>(); else regs_down<S::kSoftRegs>();
-    softmax_role<COLS, DUAL>(p, sm, q_smem, p_smem, wk, warp >> 2, threadIdx.x & 127);
+    softmax_role<COLS, DUAL>(p, sm, sb, q_smem, p_smem, wk, warp >> 2, threadIdx.x & 127);
   } else if (warp < kCtl0) {
     if constexpr (S::kWidenRegs > 72) regs_up<S::kWidenRegs>(); else regs_down<S::kWidenRegs>();
     if (warp < kValue0) {
       switch (p.a.c.bits) {
-        case 2: key_role<2, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
-        case 4: key_role<4, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
-        case 8: key_role<8, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
-        default: key_role<16, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kKey0, lane); break;
+        case 2: key_role<2, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
+        case 4: key_role<4, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
+        case 8: key_role<8, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
+        default: key_role<16, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
       }
     } else {
       switch (p.a.c.bits) {
-        case 2: value_role<2, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
-        case 4: value_role<4, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
-        case 8: value_role<8, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
-        default: value_role<16, S::kWiden>(p, sm, smem_u32(ring), wk, warp - kValue0, lane); break;
+        case 2: value_role<2, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
+        case 4: value_role<4, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
+        case 8: value_role<8, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
+        default: value_role<16, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
       }
     }
   } else {
     regs_down<S::kCtlRegs>();
     if (warp == kCtl0) {
-      produce(p, sm, smem_u32(ring), wk);
+      produce(p, sm, sb, ring_at, wk);
     } else if (warp < kCtl0 + 3) {
       const int half = warp - kCtl0 - 1;
-      mma_role<COLS, DUAL>(p, sm, smem_u32(q_smem) + half * kQBytes, smem_u32(p_smem) + half * kPBytes, wk, half);
+      mma_role<COLS, DUAL>(p, sm, sb, smem_at + half * kQBytes, smem_at + 2 * kQBytes + half * kPBytes, wk, half);
     }
     __syncwarp();
   }

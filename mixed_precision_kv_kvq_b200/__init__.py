@@ -10,6 +10,7 @@ used for device memory and streams only; all arithmetic runs in libkvq.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -17,7 +18,7 @@ import torch
 
 from ._lib import (KVQ_DTYPE_BF16, KVQ_DTYPE_F32, KVQ_POS_I32, KVQ_POS_I64, KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED,  # noqa: F401
                    KVQ_ROPE_LINEAR, KVQ_ROPE_NONE, KVQ_ROPE_NTK, KVQ_ROPE_YARN, TREE_MAX_NODES, KVQ_OPT_KEY_CHANNEL, KVQ_OPT_SINK_WINDOW, KVQ_SHIFT_DIRECT,  # noqa: F401
-                   KVQ_SHIFT_EQUIVALENT, KEY_BLOCK, Rows, WINDOW_TOKENS, KVQError, check, load)
+                   KVQ_SHIFT_EQUIVALENT, KEY_BLOCK, WINDOW_TOKENS, KVQError, check, load)
 
 HEAD_DIM = 128
 
@@ -159,33 +160,42 @@ def kvq_decode_attn_noalloc(cache, layer: int, q: torch.Tensor, sm_scale: float,
                                          _stream_ptr(stream)))
 
 
+_ROWS = struct.Struct("Pqqq").pack  # kvq_rows
+
+
 def _rows(t: Optional[torch.Tensor]):
     """kvq_rows of a [batch][n][heads][128] tensor or view (None: NULL)."""
     if t is None:
         return None
-    s = t.stride()
-    return C.byref(Rows(t.data_ptr(), s[0], s[1], s[2]))
+    b, n, h, _ = t.stride()
+    return _ROWS(t.data_ptr(), b, n, h)
 
 
 def _check_rows(name: str, t: torch.Tensor, dtype, shape=None) -> None:
-    if not t.is_cuda or t.dim() != 4 or t.shape[-1] != HEAD_DIM or (t.stride(-1) != 1 and t.numel()):
+    if not t.is_cuda or t.dim() != 4 or t.shape[3] != HEAD_DIM or (t.stride(3) != 1 and t.numel()):
         raise ValueError(f"{name} must be a CUDA tensor [batch][n][heads][128] with neighbouring channels")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 class _On:
-    """Device guard and launch stream of one call on `device`: the given
-    stream, or the device's current one."""
+    """Device guard, launch stream and allocator of one call on `device`: the
+    given stream, or the device's current one."""
+
+    __slots__ = ("device", "guard", "stream", "ptr")
 
     def __init__(self, device, stream):
+        self.device = device
         self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self.stream = None
         if stream is None:
-            stream = torch.cuda.current_stream(device)
-        self.torch_stream = stream if isinstance(stream, torch.cuda.Stream) else None
-        self.ptr = C.c_void_p(stream.cuda_stream if self.torch_stream is not None else int(stream))
+            self.ptr = torch._C._cuda_getCurrentRawStream(device.index)
+        elif isinstance(stream, torch.cuda.Stream):
+            self.stream, self.ptr = stream, stream.cuda_stream
+        else:
+            self.ptr = int(stream)  # a raw handle: torch's allocator knows nothing of it
 
     def __enter__(self):
         if self.guard is not None:
@@ -195,6 +205,13 @@ class _On:
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        """A new tensor that belongs to the call's stream."""
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
 
 _SCALINGS = {"none": KVQ_ROPE_NONE, "linear": KVQ_ROPE_LINEAR, "ntk": KVQ_ROPE_NTK, "yarn": KVQ_ROPE_YARN}
@@ -263,7 +280,7 @@ def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: 
                 raise ValueError("inputs and outputs must be on one device")
     if positions.dtype not in (torch.int32, torch.int64) or positions.device != first.device:
         raise ValueError("positions must be an int32 or int64 tensor on the device of q and k")
-    if tuple(positions.shape) == tuple(lead):
+    if positions.shape == lead:
         pb, pt = positions.stride()
     elif positions.dim() == 1 and positions.shape[0] == lead[1]:
         pb, pt = 0, positions.stride(0)
@@ -271,22 +288,14 @@ def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: 
         raise ValueError(f"positions must be {list(lead)} or [{lead[1]}], got {list(positions.shape)}")
     with _On(first.device, stream) as on:
         if q is not None and q_out is None:
-            q_out = _fresh(q.shape, q.dtype, first.device, on)
+            q_out = on.empty(q.shape, q.dtype)
         if k is not None and k_out is None:
-            k_out = _fresh(k.shape, k.dtype, first.device, on)
+            k_out = on.empty(k.shape, k.dtype)
         check(load().kvq_rope(rope.rot_dim, rope._code, rope._ptr, rope.magnitude, _dptr(positions),
                               KVQ_POS_I64 if positions.dtype == torch.int64 else KVQ_POS_I32, pb, pt, lead[0], lead[1], dtype,
                               _rows(q), _rows(q_out), q.shape[2] if q is not None else 0,
                               _rows(k), _rows(k_out), k.shape[2] if k is not None else 0, on.ptr))
     return q_out, k_out
-
-
-def _fresh(shape, dtype, device, on: "_On") -> torch.Tensor:
-    """A new tensor that belongs to the call's stream."""
-    if on.torch_stream is None:  # a raw stream handle: torch knows nothing of it
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(on.torch_stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def kvq_tree_workspace(cache, layer: int, q_heads: int, n_nodes: int) -> int:
@@ -512,9 +521,9 @@ class KVQCache:
             # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
             nbytes = kvq_tree_workspace(self.handle, layer, q.shape[2], q.shape[1])
             if out is None:
-                out = _fresh(q.shape, torch.bfloat16, q.device, on)
-            ws = _fresh(((nbytes + 15) // 16 * 4,), torch.float32, q.device, on)
-            kvq_tree_attn(self.handle, layer, q, k, v, mask, sm_scale, out, ws, on.ptr.value or 0)
+                out = on.empty(q.shape, torch.bfloat16)
+            ws = on.empty((nbytes,), torch.uint8)
+            kvq_tree_attn(self.handle, layer, q, k, v, mask, sm_scale, out, ws, on.ptr)
         return out
 
     def read(self, layer: int, start: int = 0, count: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -530,11 +539,11 @@ class KVQCache:
         with _On(device, stream) as on:
             if k_out is None and v_out is None:
                 shape = (self.batch, count, self.kv_heads, HEAD_DIM)
-                k_out, v_out = _fresh(shape, dtype, device, on), _fresh(shape, dtype, device, on)
+                k_out, v_out = on.empty(shape, dtype), on.empty(shape, dtype)
             for name, x in (("k_out", k_out), ("v_out", v_out)):
                 if x is not None:
                     self._check_batch(name, x, self.kv_heads)
-            kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr.value or 0)
+            kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr)
         return k_out, v_out
 
     def _check_batch(self, name: str, t: torch.Tensor, heads: Optional[int]) -> None:

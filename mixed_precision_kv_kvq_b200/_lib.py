@@ -76,12 +76,6 @@ SIGNATURES = {
     "kvq_free": (None, [P]),
 }
 
-class Rows(C.Structure):
-    """kvq_rows of include/kvq.h."""
-    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_longlong), ("stride_t", C.c_longlong),
-                ("stride_h", C.c_longlong)]
-
-
 _lib = None
 
 

@@ -963,9 +963,9 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
     if (!(std::fabs(w) <= 1048576.0)) return fail(KVQ_ERR_INVALID, "inv_freq[%d] = %g is not within 2^20", p, w);
     // 2^64 w / (2 pi) modulo 2^64, in 64-bit significands (the whole turns of
     // a frequency above 2 pi drop out)
-    const long double turns = (long double)w * 0.159154943091895335768883763372514362L;
-    const long double part = turns - floorl(turns);  // [0, 1]
-    const long double scaled = roundl(ldexpl(part, 64));
+    long double turns = (long double)w * 0.159154943091895335768883763372514362L;
+    if (!(turns >= 0.0L && turns < 1.0L)) turns -= floorl(turns);  // [0, 1]
+    const long double scaled = turns * 18446744073709551616.0L + 0.5L;
     a.turn[p] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
   }
   const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;

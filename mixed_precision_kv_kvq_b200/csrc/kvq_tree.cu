@@ -18,28 +18,38 @@
 // (16x256b: rows lane / 4 and + 8, two columns a lane), and one channel of two
 // neighbouring tokens in each Value pair (16x128b, one column a lane), so
 // codes are widened in registers and stored once, with no transposition.
-//   Keys go in as val = (c - 2^(b-1)) 2^(1-b), exact in fp16 (rounded to 11
-//   bits at 16-bit codes); with Rk = R 2^(b-1) / (2^b - 1), Zk = Z + Rk the
-//   score is Rk (q' . val) + Zk sum(q'), applied in fp32 by the thread that
-//   owns the token.  Per-channel Key groups and drafted Keys go in as fp16
-//   values (Rk, Zk constant).
-//   Values go in as fp16(v g), g = (1 - 2^-b) / 2: v g = val R/4 + (Z g + R/4),
-//   so R/4 is exact, and nothing in binary16's range overflows.
+// Codes become val = (c - 2^(b-1)) 2^(1-b) first, exact in fp16 at 8 bits and
+// fewer (rounded to 11 bits at 16), then one fma gives the value times
+// g = (1 - 2^-b) / 2: x g = val R/4 + (Z g + R/4).  With this g R/4 is exact,
+// the value is rounded twice (its centre Z g + R/4, then itself), and nothing
+// in binary16's range overflows.  1/g goes into the query and the output.
 // S has a token per tensor-memory lane: a thread owns one token and walks the
-// rows, so a token's range, zero and validity are registers, P is written row
-// by row as the K-slices that an MN-major operand wants (16-byte stores,
-// 128-byte swizzle), and row sums are per-thread partial sums until the end.
-// A running maximum m_r is shared by the 128 threads; it moves only when some
-// score exceeds it by more than 2^8 (one vote per 32 rows), and only then are
-// column maxima formed and O rescaled in tensor memory.
+// rows, so whether a token counts is a register, P is written row by row as the
+// K-slices that an MN-major operand wants (16-byte stores, 128-byte swizzle),
+// and row sums are per-thread partial sums until the end.  A row's running
+// maximum m_r is shared by the 128 threads and subtracted by the MMA itself:
+// one more k-step multiplies a constant left operand (256, 256, 0, ...) with
+// -m_r / 256 as an fp16 pair (high + low part), so a thread's score is ready for
+// the exponential as it comes out of tensor memory.  (Read from shared memory
+// instead, the per-row terms took 16 LDS.128 per 32 rows and thread, ~1000 cycles
+// of a tile's 3800.)  m_r moves only when some score exceeds it by more than
+// 2^8 (one vote per 32 rows), and only then are column maxima formed and O
+// rescaled in tensor memory.
 //
-// Roles (20 warps, one CTA per SM, which holds all 512 tensor-memory columns):
-// two softmax warpgroups, four warps widening Keys, four widening Values, one
-// warp streaming packed tiles with bulk copies, two issuing MMAs.  Each softmax
-// warpgroup with its issuer, its S, P, Q and O forms a half.  With up to 64
-// rows the halves take alternate tiles of the same rows (two independent
-// softmax states, joined at the end); above, each takes 64 of 128 rows of every
-// tile.  K and V tiles are double-buffered in tensor memory.
+// Roles (one CTA per SM, which holds all 512 tensor-memory columns): 8 or 16
+// softmax warps, groups of four widening warps, one warp streaming packed tiles
+// with bulk copies, two issuing MMAs.  The softmax warps form two halves, each
+// with an issuer, S, P, Q and O of its own.  With up to 64 rows the halves take
+// alternate tiles of the same rows (two independent softmax states, joined at
+// the end); above, each takes 64 of 128 rows of every tile.  Two widened tiles
+// fit beside S and O; the widening warps of a buffer (four, or eight that share
+// a tile's groups where few rows leave them more of the work) take every second
+// tile whole, so the fixed cost of a tile (waits, fences) falls on few warps.
+//
+// Phases.  A wait tells apart only two successive phases of a barrier, so every
+// waiter has to see each phase of the barriers it waits on: the ring is one
+// ring per buffer (its slots are never read by the other buffer's warps), and
+// in alternate tiles a buffer belongs to one half.
 //
 // Work split: the (stream, block of rows, tile) units form one line that is cut
 // evenly over the grid; a CTA writes the rows it covers whole, and leaves a
@@ -50,6 +60,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "kvq_decode_common.cuh"
 #include "kvq_view.cuh"
 
@@ -58,39 +71,43 @@ namespace {
 
 constexpr int kTile = 128;           // tokens per tile
 constexpr int kTileGroups = kTile / kGroupTokens;
-constexpr int kTreeWarps = 28;
-constexpr int kTreeThreads = 32 * kTreeWarps;
 constexpr int kMaxStages = 8;
 constexpr int kHalfRows = 64;        // rows of a half's operands in shared memory
 constexpr int kQBytes = kHalfRows * kHeadDim * 2;  // one half's Q: two 64-channel slabs of [64][128 B]
 constexpr int kPBytes = kTile * 128;               // one half's P: [128 tokens][64 rows] fp16
 constexpr float kUnset = 1e30f;      // -m of a row with no token yet
 
-// How the 28 warps are divided, and the registers of each kind (setmaxnreg; 896
-// threads are launched with 72).  With few rows the widening is the larger
-// part of a tile's work and takes 16 warps; with 64 rows a half (128 rows
-// a CTA, or 64 in alternate tiles) the softmax is, and a half's rows are
-// divided over two warpgroups: 32 rows a thread is also what its registers hold.
+// How the warps are divided, the registers of each kind (setmaxnreg from what the
+// launch gives) and tensor memory's columns.  With 64 rows a half (128 rows a
+// CTA, or 64 in alternate tiles) a half's rows are divided over two
+// warpgroups: 32 rows a thread is what its registers hold.
 template <int COLS>
 struct Split {
-  static constexpr int kSoft = COLS == 64 ? 16 : 8;          // softmax warps
-  static constexpr int kWiden = COLS == 64 ? 4 : 8;          // warps for Keys, and as many for Values
-  static constexpr int kSubs = kSoft / 8;                    // warpgroups per half
-  static constexpr int kCols = COLS / kSubs;                 // rows per softmax thread
-  static constexpr int kSoftRegs = COLS == 64 ? 88 : COLS == 32 ? 104 : 80;
-  static constexpr int kWidenRegs = COLS == 64 ? 64 : COLS == 32 ? 64 : 80;
+  static constexpr int kSoft = COLS == 64 ? 16 : 8;       // softmax warps
+  static constexpr int kShare = COLS == 64 ? 1 : 2;       // widening groups that share a tile
+  static constexpr int kWiden = 8 * kShare;               // widening warps: groups of 4 for each of the two buffers
+  static constexpr int kWarps = kSoft + kWiden + 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kSubs = kSoft / 8;                 // softmax warpgroups per half
+  static constexpr int kCols = COLS / kSubs;              // rows per softmax thread
+  static constexpr int kRegs = 72;                        // at launch
+  static constexpr int kSoftRegs = COLS == 64 ? 88 : COLS == 32 ? 96 : 80;
+  static constexpr int kWidenRegs = COLS == 64 ? 64 : COLS == 32 ? 72 : 80;
   static constexpr int kCtlRegs = 24;
-  static_assert(kSoft + 2 * kWiden + 4 == kTreeWarps);
-  static_assert(32 * (kSoft * kSoftRegs + 2 * kWiden * kWidenRegs + 4 * kCtlRegs) <= kTreeThreads * 72);
+  static_assert(kWarps == 28 && 65536 / kThreads / 8 * 8 == kRegs);
+  static_assert(32 * (kSoft * kSoftRegs + kWiden * kWidenRegs + 4 * kCtlRegs) <= kThreads * kRegs);
+  static constexpr uint32_t kStep = COLS == 64 ? 64 : 32;  // columns of one half's S or O
+  static constexpr uint32_t kColS = 0, kColO = 2 * kStep, kColK = 4 * kStep, kColV = kColK + 128;
+  static_assert(kColV + 128 <= 512);
 };
-
-// Tensor-memory columns.
-constexpr uint32_t kColS = 0, kColO = 128, kColK = 256, kColV = 384;  // + 64 per half or buffer
+constexpr int kOnesBytes = kTile * 32;             // constant left operand of the extra k-step: [128][16] fp16
+constexpr int kNegBytes = kHalfRows * 32;          // one half's -m / 256: [64][16] fp16
+constexpr float kNegScale = 256.0f;                // -m up to 1.6e7, to 22 bits
 
 struct Small {
-  float2 kz[4][kTile];               // (Rk, Zk) of the tokens of tile t, ring of 4
-  float4 col[2][kHalfRows / 2];      // per half, rows 2i and 2i + 1: sum(q') twice, -m twice
+  float neg[2][kHalfRows];           // per half: -m as the MMA subtracts it (kUnset: no token yet, 0 there)
   float alpha[2][kHalfRows];         // factor of the last rescaling
+  float shift[2][kHalfRows];         // and what it added to the scores
   float red[2][4][kHalfRows];        // per warp: column maxima, then row sums
   float2 ml[2][kHalfRows];           // final (m, l)
   uint32_t seen[4][kTile][4];        // drafted tile t: bit i of word w: the row sees token 32 w + i
@@ -101,7 +118,8 @@ struct Small {
   volatile int abort;
 };
 constexpr int kSmallBytes = (sizeof(Small) + 1023) / 1024 * 1024;
-constexpr int kFixedBytes = 2 * kQBytes + 2 * kPBytes + kSmallBytes;
+constexpr int kSmallAt = 2 * kQBytes + 2 * kPBytes + kOnesBytes + 2 * kNegBytes;
+constexpr int kFixedBytes = kSmallAt + kSmallBytes;
 constexpr int kSmemMax = 227 * 1024 - 1024;  // the base is aligned by hand
 
 struct TreePlan {
@@ -186,6 +204,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t bdesc, u
       "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// The same with A in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
 // Instruction descriptor: fp16 A and B, fp32 D, M = 128; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
@@ -196,6 +222,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
          ((uint64_t)2 << 61);
 }
+
+// [rows][16] fp16, K-major without swizzle: 8 x 16-byte core matrices, the two
+// along K 128 bytes apart, 256 bytes between 8-row groups.
+__device__ __forceinline__ uint64_t narrow_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+__host__ __device__ constexpr int narrow_at(int row) { return (row >> 3) * 256 + (row & 7) * 16; }  // elements 0 .. 7
 
 #define KVQ_R4(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3])
 #define KVQ_R16(r, i) KVQ_R4(r, i), KVQ_R4(r, (i) + 4), KVQ_R4(r, (i) + 8), KVQ_R4(r, (i) + 12)
@@ -306,6 +339,18 @@ __device__ __forceinline__ uint32_t code_val16(uint32_t w) {
   // hi / 128 - 1 - 2^-5 is exact; (8 + lo / 128) 2^-8 adds 2^-5 + lo 2^-15
   return hfma2_u(lo, splat_h(pow2_h(-8)), hadd2_u(hi, splat_h(0xc884u)));  // - 9.03125
 }
+// g = (1 - 2^-b) / 2, as fp16 and fp32 (16 bits: 1/2, off by 2^-16)
+template <int BITS>
+__host__ __device__ constexpr uint32_t value_scale_h() {
+  return BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
+}
+template <int BITS>
+__host__ __device__ constexpr float value_scale() {
+  return BITS == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << BITS);
+}
+__device__ __forceinline__ float value_scale_of(int bits) {
+  return bits == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << bits);
+}
 __device__ __forceinline__ uint32_t sat_h2(float lo, float hi) {
   return pack_h2(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
 }
@@ -330,10 +375,31 @@ __device__ __forceinline__ void key_pairs(const uint32_t* u, int p, uint32_t& a,
   }
 }
 
+// Factors of a token's group from its (R, Z) word at the cache's width: R/4 and
+// Z g + R/4, for two tokens or twice for one.
+template <int BITS>
+__device__ __forceinline__ void group_factors(uint32_t m0, uint32_t m1, uint32_t& rc, uint32_t& zc) {
+  rc = hmul2_u(__byte_perm(m0, m1, 0x5410), splat_h(pow2_h(-2)));
+  zc = hfma2_u(__byte_perm(m0, m1, 0x7632), splat_h(value_scale_h<BITS>()), rc);
+}
+// The same for 16-bit codes in a cache of another width: R g / 2 is not exact
+// then, so the centre is formed in fp32.
+template <int BITS>
+__device__ __forceinline__ void window_factors(uint32_t m0, uint32_t m1, uint32_t& rc, uint32_t& zc) {
+  constexpr float g = value_scale<BITS>(), f = g * (32768.0f / 65535.0f);
+  const uint32_t r2 = __byte_perm(m0, m1, 0x5410), z2 = __byte_perm(m0, m1, 0x7632);
+  const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&r2));
+  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&z2));
+  rc = pack_h2(r.x * f, r.y * f);
+  zc = pack_h2(fmaf(r.x, f, z.x * g), fmaf(r.y, f, z.y * g));
+}
+
 // Keys of one group into 16 tensor-memory rows, 64 channels at a time.  part:
-// the group's Key part; CHAN: per-channel groups, their (R, Z) words at kmc.
+// the group's Key part; rc, zc: factors of tokens g and g + 8; CHAN:
+// per-channel groups, their (R, Z) words at kmc (the cache's width).
 template <int BITS, bool CHAN, typename From>
-__device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t taddr, int lane) {
+__device__ __forceinline__ void widen_keys(From part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], FromRing kmc,
+                                           uint32_t taddr, int lane) {
   constexpr int kHalfWords = BITS / 2;  // words of 4 quad positions of one token
   const From unit = part + lane * unit_bytes(BITS);
 #pragma unroll
@@ -357,20 +423,18 @@ __device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t tad
     }
 #pragma unroll
     for (int p = 0; p < 4; p++) {
-#pragma unroll
-      for (int x = 0; x < 2; x++) key_pairs<BITS>(u[x], p, r[4 * p + 2 * x], r[4 * p + 2 * x + 1]);
-      if constexpr (CHAN) {  // k (1 - 2^-b) / 2 = val R/4 + (Z (1 - 2^-b) / 2 + R/4)
-        constexpr uint32_t g = BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
+      uint32_t ra[2], za[2];  // CHAN: of members (0, 2) and (1, 3)
+      if constexpr (CHAN) {
         const uint4 w = (kmc + 4 * (16 * (4 * hf + p) + 4 * (lane & 3))).u128();
-        const uint32_t ra = hmul2_u(__byte_perm(w.x, w.z, 0x5410), splat_h(pow2_h(-2)));
-        const uint32_t rb = hmul2_u(__byte_perm(w.y, w.w, 0x5410), splat_h(pow2_h(-2)));
-        const uint32_t za = hfma2_u(__byte_perm(w.x, w.z, 0x7632), splat_h(g), ra);
-        const uint32_t zb = hfma2_u(__byte_perm(w.y, w.w, 0x7632), splat_h(g), rb);
+        group_factors<BITS>(w.x, w.z, ra[0], za[0]);
+        group_factors<BITS>(w.y, w.w, ra[1], za[1]);
+      }
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
-          r[4 * p + 2 * x] = hfma2_u(r[4 * p + 2 * x], ra, za);
-          r[4 * p + 2 * x + 1] = hfma2_u(r[4 * p + 2 * x + 1], rb, zb);
-        }
+      for (int x = 0; x < 2; x++) {
+        uint32_t k0, k1;
+        key_pairs<BITS>(u[x], p, k0, k1);
+        r[4 * p + 2 * x] = hfma2_u(k0, CHAN ? ra[0] : rc[x], CHAN ? za[0] : zc[x]);
+        r[4 * p + 2 * x + 1] = hfma2_u(k1, CHAN ? ra[1] : rc[x], CHAN ? za[1] : zc[x]);
       }
     }
     tc_st_16x256_x4(taddr + 32 * hf, r);
@@ -415,14 +479,6 @@ __device__ __forceinline__ void widen_values(From part, const uint32_t (&rc)[2],
 __device__ __forceinline__ int channel_of(int rho) {
   return 16 * (rho & 7) + 8 * ((rho >> 3) & 1) + 2 * (rho >> 5) + ((rho >> 4) & 1);
 }
-// (1 - 2^-b) / 2 as fp16 (16 bits: 1/2, off by 2^-16)
-__device__ __forceinline__ uint32_t value_scale_h(int bits) {
-  return bits == 2 ? 0x3600u : bits == 4 ? 0x3780u : bits == 8 ? 0x37f8u : 0x3800u;
-}
-__device__ __forceinline__ float value_scale(int bits) {
-  return bits == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << bits);
-}
-
 // ------------------------------------------------------------------ roles
 
 // Shared address of barrier i of an array in Small, from that of Small (sb).
@@ -454,13 +510,15 @@ __device__ __forceinline__ bool token_valid(const TreePlan& p, int t, int tl) {
   return (t - p.tp - p.tw) * kTile + tl < p.a.n;
 }
 
-// A slot of the ring and its phase, stepped tile by tile.
+// One buffer's ring: slots buf, buf + 2, ... of the stages, in turn.
 struct Slot {
-  int i = 0;
+  int i;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Slot(int buf) : i(buf) {}
   __device__ __forceinline__ void step(int stages) {
-    if (++i == stages) {
-      i = 0;
+    i += 2;
+    if (i >= stages) {
+      i &= 1;
       phase ^= 1;
     }
   }
@@ -473,9 +531,11 @@ __device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t s
   const Fill& f = p.f;
   const int gb = group_bytes(c.bits);
   const bool chan = c.kmc != nullptr;
-  Slot sl;
-  uint32_t sent = 0;
+  Slot even(0), odd(1);
+  uint32_t ct = 0;
   while (wk.next(p)) {
+    const uint32_t ct0 = ct;
+    ct += wk.t1 - wk.t0;
     if (wk.t0 >= p.tp) continue;
     const uint8_t* sbase = c.codes + (size_t)wk.s * c.nt * kTileBytes;
     const uint32_t* mbase = c.meta + (size_t)wk.s * c.nt * c.pf * 2;
@@ -486,7 +546,9 @@ __device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t s
       grp = loc.grp;
       groups = loc.tile_groups;
     }
-    for (int t = wk.t0; t < min(wk.t1, p.tp); t++, sent++) {
+    for (int t = wk.t0; t < min(wk.t1, p.tp); t++) {
+      const bool second = (ct0 + (uint32_t)(t - wk.t0)) & 1u;
+      const Slot sl = second ? odd : even;
       tree_wait(KVQ_BAR(ring_free, sl.i), sl.phase ^ 1, p.a.err, &sm.abort);
       if (sm.abort) goto out;
       const uint32_t st = ring + (uint32_t)(sl.i * p.stage_bytes);
@@ -526,16 +588,18 @@ __device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t s
           }
         }
       }
-      sl.step(p.stages);
+      if (second)
+        odd.step(p.stages);
+      else
+        even.step(p.stages);
     }
   }
 out:
-  if (sm.abort) {  // copies in flight land before the CTA ends
-    const uint32_t k = min(sent, (uint32_t)p.stages);
-    for (uint32_t i = 0; i < k; i++) {
-      sl.i = sl.i == 0 ? p.stages - 1 : sl.i - 1;
-      if (sl.i == p.stages - 1) sl.phase ^= 1;
-      drain_wait(KVQ_BAR(ring_full, sl.i), sl.phase);
+  if (sm.abort) {  // copies in flight land before the CTA ends: of each slot the last use, if any
+    for (int i = 0; i < p.stages; i++) {
+      const Slot& r = i & 1 ? odd : even;
+      const uint32_t uses_phase = i < r.i ? r.phase : r.phase ^ 1;  // of the slot's last use; the phase before the first reads as done
+      drain_wait(KVQ_BAR(ring_full, i), uses_phase);
     }
   }
 }
@@ -554,12 +618,12 @@ __device__ __forceinline__ WindowGroup window_group(const TreePlan& p, int s, in
                      p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
 }
 
-// Drafted Keys: rows g and g + 8 of the group, channels 16 p + 4 t .. + 3, as k / (2 lambda).
-__device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, uint32_t taddr, int lane) {
+// Drafted Keys of a group, as k g / lambda.
+__device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, float scale, uint32_t taddr, int lane) {
   const TreeArgs& a = p.a;
   const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll
+#pragma unroll 1
   for (int hf = 0; hf < 2; hf++) {
     uint32_t r[16];
 #pragma unroll
@@ -581,8 +645,8 @@ __device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, uin
         float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
         if (a.c.lam_inv)
           l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 64 * hf + 16 * q + 4 * t));
-        r[4 * q + 2 * x] = sat_h2(0.5f * k.x * l.x, 0.5f * k.z * l.z);
-        r[4 * q + 2 * x + 1] = sat_h2(0.5f * k.y * l.y, 0.5f * k.w * l.w);
+        r[4 * q + 2 * x] = sat_h2(scale * k.x * l.x, scale * k.z * l.z);
+        r[4 * q + 2 * x + 1] = sat_h2(scale * k.y * l.y, scale * k.w * l.w);
       }
     }
     tc_st_16x256_x4(taddr + 32 * hf, r);
@@ -619,88 +683,6 @@ __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, f
   }
 }
 
-// Keys of every tile into tensor memory, the tokens' (Rk, Zk) and, for drafted
-// tiles, which rows see them.  Warp w of WARPS: tokens 32 (w % 4) .. + 31, of 8
-// warps each takes one of the two groups.
-template <int BITS, int WARPS>
-__device__ __forceinline__ void key_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int warp, int lane) {
-  const CacheView& c = p.a.c;
-  constexpr int gb = group_bytes(BITS), kEach = 8 / WARPS;  // groups per warp and tile
-  const int w = warp & 3, i0 = kEach == 1 ? warp >> 2 : 0;
-  uint32_t ct = 0;
-  Slot sl;
-  const uint32_t tm = sm.tmem;
-  while (wk.next(p)) {
-    for (int t = wk.t0; t < wk.t1; t++, ct++) {
-      const int buf = ct & 1;
-      const uint32_t ta = tm + kColK + 64 * buf + ((uint32_t)(32 * w) << 16);
-      tree_wait(KVQ_BAR(k_free, buf), ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
-      float2 kz = make_float2(0.f, 0.f);
-      const int tl = 32 * w + 16 * i0 + (kEach == 1 ? lane & 15 : lane);
-      if (t < p.tp) {
-        tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
-        tc_after();
-        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
-        const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
-        // groups that do not exist are read as whatever the stage holds: those rows of S are not used
-        if (c.kmc) {
-#pragma unroll 1
-          for (int i = i0; i < i0 + kEach; i++)
-            widen_keys<BITS, true>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), ta + ((uint32_t)(16 * i) << 16), lane);
-          kz = make_float2(1.0f / value_scale(BITS), 0.f);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kEach; i++)
-            widen_keys<BITS, false>(st + (2 * w + i0 + i) * gb, st, ta + ((uint32_t)(16 * (i0 + i)) << 16), lane);
-          const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
-                           ((float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u));
-          kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
-        sl.step(p.stages);
-      } else if (t < p.tp + p.tw) {
-        tc_after();
-#pragma unroll 1
-        for (int i = i0; i < i0 + kEach; i++) {
-          const WindowGroup at = window_group(p, wk.s, t, 2 * w + i);
-          if (at.code) widen_keys<16, false>(FromGlobal{at.code}, FromRing{0}, ta + ((uint32_t)(16 * i) << 16), lane);
-        }
-        const WindowGroup at = window_group(p, wk.s, t, tl >> 4);
-        if (at.meta) {
-          const uint32_t m = at.meta[2 * (tl & 15)];
-          const float rk = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * (32768.0f / 65535.0f);
-          kz = make_float2(rk, __half2float(__ushort_as_half((unsigned short)(m >> 16))) + rk);
-        }
-      } else {
-        tc_after();
-        const int j0 = (t - p.tp - p.tw) * kTile;
-#pragma unroll 1
-        for (int i = i0; i < i0 + kEach; i++)
-          if (j0 + 32 * w + 16 * i < p.a.n)
-            draft_keys(p, wk.s, j0 + 32 * w + 16 * i, ta + ((uint32_t)(16 * i) << 16), lane);
-        kz = make_float2(2.f, 0.f);
-        if (i0 == 0) {  // one word per row: which of the 32 tokens its node sees
-          const int b = wk.s / c.kv_heads, j = j0 + 32 * w + lane;
-          const int r0 = wk.block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
-          for (int node = r0 / p.a.group; node * p.a.group < r1; node++) {
-            bool see = j < p.a.n;
-            if (see) see = p.a.mask ? p.a.mask[b * p.a.mask_b + (long long)node * p.a.n + j] != 0 : j <= node;
-            const uint32_t bitsw = __ballot_sync(0xffffffffu, see);
-            const int row = node * p.a.group + lane - r0;
-            if (lane < p.a.group && row >= 0 && row < r1 - r0) sm.seen[ct & 3][row][w] = bitsw;
-          }
-        }
-      }
-      sm.kz[ct & 3][tl] = kz;  // 8 warps: lanes 16-31 repeat lanes 0-15
-      tc_wait_st();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(k_full, buf));
-    }
-  }
-}
-
 // Values of a packed tile in the ring.  CHECK: some of its tokens do not exist
 // (n groups do; group part only its first valid tokens): they become zeros, as
 // P is zero there and stale codes with a stale range may be anything.
@@ -708,10 +690,8 @@ template <int BITS, bool CHECK, int GROUPS>
 __device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int n, int part, int valid, int w, int lane) {
   constexpr int gb = group_bytes(BITS);
   const int t = lane & 3;
-  const uint32_t gh = splat_h(value_scale_h(BITS));
-#pragma unroll
-  for (int k2 = 0; k2 < GROUPS; k2 += 2) {
-    const int g2 = g0 + k2;
+#pragma unroll 2
+  for (int g2 = g0; g2 < g0 + GROUPS; g2 += 2) {
     uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -725,9 +705,7 @@ __device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int
           if (first >= have) m.y = 0u;
           if (first + 1 >= have) m.w = 0u;
         }
-        const uint32_t r2 = __byte_perm(m.y, m.w, 0x5410), z2 = __byte_perm(m.y, m.w, 0x7632);
-        rc[u] = hmul2_u(r2, splat_h(pow2_h(-2)));  // R g 2^(b-1) / (2^b - 1) = R / 4
-        zc[u] = hfma2_u(z2, gh, rc[u]);
+        group_factors<BITS>(m.y, m.w, rc[u], zc[u]);
       }
       widen_values<BITS>(st + (gi * gb + part_bytes(BITS)), rc, zc, w, lane, out);
 #pragma unroll
@@ -741,90 +719,166 @@ __device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int
   }
 }
 
-// Values of every tile.  Warp w of WARPS: the channels of lane units 2 (w % 4)
-// and + 1, of 8 warps each half of the groups.
-template <int BITS, int WARPS>
-__device__ __forceinline__ void value_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int warp, int lane) {
-  const int t4 = lane & 3, w = warp & 3;
-  constexpr int kEach = 4 * kTileGroups / WARPS;  // groups per warp and tile
-  const int g0 = (warp >> 2) * kEach;
-  uint32_t ct = 0;
-  Slot sl;
-  const uint32_t tm = sm.tmem;
-  while (wk.next(p)) {
-    for (int t = wk.t0; t < wk.t1; t++, ct++) {
-      const int buf = ct & 1;
-      const uint32_t ta = tm + kColV + 64 * buf + ((uint32_t)(32 * w) << 16);
-      tree_wait(KVQ_BAR(v_free, buf), ((ct >> 1) & 1) ^ 1, p.a.err, &sm.abort);
-      if (t < p.tp) {
-        tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
-        tc_after();
-        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
-        const int n = min(kTileGroups, p.groups - t * kTileGroups);
-        const int part = p.part_group - t * kTileGroups;
-        if (n == kTileGroups && (unsigned)part >= (unsigned)kTileGroups)
-          value_tile<BITS, false, kEach>(st, ta, g0, n, part, p.part_valid, w, lane);
-        else
-          value_tile<BITS, true, kEach>(st, ta, g0, n, part, p.part_valid, w, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
-        sl.step(p.stages);
-      } else {
-        tc_after();
-#pragma unroll 1
-        for (int g2 = g0; g2 < g0 + kEach; g2 += 2) {
-          uint32_t o0[8], o1[8];
+// Which rows see drafted tokens 32 w .. + 31 of tile t: one word per row.
+__device__ __forceinline__ void draft_seen(const TreePlan& p, uint32_t (*seen)[4], int s, int block, int t, int w, int lane) {
+  const TreeArgs& a = p.a;
+  const int b = s / a.c.kv_heads, j = (t - p.tp - p.tw) * kTile + 32 * w + lane;
+  const int r0 = block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
+  const unsigned char* m = a.mask ? a.mask + b * a.mask_b + j : nullptr;
+  constexpr int kBatch = 8;  // mask bytes in flight
+  for (int n0 = r0 / a.group; n0 * a.group < r1; n0 += kBatch) {
+    bool see[kBatch];
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
-            uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-            if (t < p.tp + p.tw) {
-              const WindowGroup at = window_group(p, wk.s, t, g2 + i);
-              if (at.code) {
-                // 16-bit codes beside another width: R g / 2 is not exact, so the centre is formed in fp32
-                const float g = value_scale(BITS), f = g * (32768.0f / 65535.0f);
-                uint32_t rcv[2], zcv[2];
+    for (int i = 0; i < kBatch; i++) {
+      const int node = n0 + i;
+      see[i] = j < a.n && node < a.n;
+      if (see[i]) see[i] = m ? m[(long long)node * a.n] != 0 : j <= node;
+    }
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                  const uint4 m = *reinterpret_cast<const uint4*>(at.meta + 2 * (8 * u + 2 * t4));
-                  const bool v0 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4);
-                  const bool v1 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4 + 1);
-                  const uint32_t r2 = __byte_perm(v0 ? m.y : 0u, v1 ? m.w : 0u, 0x5410);
-                  const uint32_t z2 = __byte_perm(v0 ? m.y : 0u, v1 ? m.w : 0u, 0x7632);
-                  const float2 rf = __half22float2(*reinterpret_cast<const __half2*>(&r2));
-                  const float2 zf = __half22float2(*reinterpret_cast<const __half2*>(&z2));
-                  rcv[u] = pack_h2(rf.x * f, rf.y * f);
-                  zcv[u] = pack_h2(fmaf(rf.x, f, zf.x * g), fmaf(rf.y, f, zf.y * g));
-                }
-                widen_values<16>(FromGlobal{at.code + part_bytes(16)}, rcv, zcv, w, lane, out);
-              }
-            } else {
-              const int j0 = (t - p.tp - p.tw) * kTile + 16 * (g2 + i);
-              if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale(BITS), w, lane, out);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              o0[4 * i + e] = out[0][e];
-              o1[4 * i + e] = out[1][e];
-            }
-          }
-          tc_st_16x128_x4(ta + 8 * g2, o0);
-          tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
-        }
-      }
-      tc_wait_st();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(v_full, buf));
+    for (int i = 0; i < kBatch; i++) {
+      const uint32_t word = __ballot_sync(0xffffffffu, see[i]);
+      const int row = (n0 + i) * a.group + lane - r0;
+      if (lane < a.group && row >= 0 && row < r1 - r0) seen[row][w] = word;
     }
   }
 }
 
-// One warp per half: the MMAs of the half's tiles.
+// Widening: Keys, then Values of buffer buf's tiles (every second one), and for
+// drafted tiles which rows see them.  Warp w of a group writes tensor-memory rows
+// 32 w .. + 31: Keys of tokens 32 w .. + 31, Values of the channels of lane units
+// 2 w and 2 w + 1; of two groups that share a tile each takes one of the two Key
+// groups and half of the Value groups (part).
+template <int BITS, int COLS>
+__device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int buf, int part,
+                                           int w, int lane) {
+  using S = Split<COLS>;
+  constexpr int kKeys = 2 / S::kShare, kValues = kTileGroups / S::kShare;
+  const int i0 = part * kKeys, v0 = part * kValues;
+  const CacheView& c = p.a.c;
+  constexpr int gb = group_bytes(BITS);
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t tk = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColK + 64 * buf;
+  const uint32_t tv = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColV + 64 * buf;
+  uint32_t phase = 1;  // of k_free and v_free
+  uint32_t ct = 0;
+  Slot sl(buf);
+  while (wk.next(p)) {
+    for (int t = wk.t0; t < wk.t1; t++, ct++) {
+      if ((ct & 1) == (uint32_t)buf) {
+        const bool packed = t < p.tp;
+        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
+        if (packed) tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
+        tree_wait(KVQ_BAR(k_free, buf), phase, p.a.err, &sm.abort);
+        tc_after();
+        // ---- Keys ----
+        if (packed) {
+          // groups that do not exist are read as whatever the stage holds: those rows of S are not used
+#pragma unroll 1
+          for (int i = i0; i < i0 + kKeys; i++) {
+            const uint32_t ti = tk + ((uint32_t)(16 * i) << 16);
+            const FromRing codes = st + (2 * w + i) * gb;
+            uint32_t rc[2] = {0u, 0u}, zc[2] = {0u, 0u};
+            if (c.kmc) {
+              widen_keys<BITS, true>(codes, rc, zc, st + kTileGroups * (gb + 128), ti, lane);
+            } else {
+              const FromRing meta = st + (kTileGroups * gb + (2 * w + i) * 128 + 8 * g);
+              const uint32_t m0 = meta.u32(), m1 = (meta + 64).u32();
+              group_factors<BITS>(m0, m0, rc[0], zc[0]);
+              group_factors<BITS>(m1, m1, rc[1], zc[1]);
+              widen_keys<BITS, false>(codes, rc, zc, st, ti, lane);
+            }
+          }
+        } else if (t < p.tp + p.tw) {
+#pragma unroll 1
+          for (int i = i0; i < i0 + kKeys; i++) {
+            const WindowGroup wg = window_group(p, wk.s, t, 2 * w + i);
+            if (wg.code) {
+              uint32_t rc[2], zc[2];
+              const uint32_t m0 = wg.meta[2 * g], m1 = wg.meta[2 * g + 16];
+              window_factors<BITS>(m0, m0, rc[0], zc[0]);
+              window_factors<BITS>(m1, m1, rc[1], zc[1]);
+              widen_keys<16, false>(FromGlobal{wg.code}, rc, zc, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
+            }
+          }
+        } else {
+          const int j0 = (t - p.tp - p.tw) * kTile + 32 * w;
+#pragma unroll 1
+          for (int i = i0; i < i0 + kKeys; i++)
+            if (j0 + 16 * i < p.a.n)
+              draft_keys(p, wk.s, j0 + 16 * i, value_scale<BITS>(), tk + ((uint32_t)(16 * i) << 16), lane);
+          if (part == 0) draft_seen(p, sm.seen[ct & 3], wk.s, wk.block, t, w, lane);
+        }
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(KVQ_BAR(k_full, buf));
+        // ---- Values ----
+        tree_wait(KVQ_BAR(v_free, buf), phase, p.a.err, &sm.abort);
+        tc_after();
+        if (packed) {
+          const int n = min(kTileGroups, p.groups - t * kTileGroups);
+          const int pg = p.part_group - t * kTileGroups;
+          if (n == kTileGroups && (unsigned)pg >= (unsigned)kTileGroups)
+            value_tile<BITS, false, kValues>(st, tv, v0, n, pg, p.part_valid, w, lane);
+          else
+            value_tile<BITS, true, kValues>(st, tv, v0, n, pg, p.part_valid, w, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
+        } else {
+#pragma unroll 1
+          for (int g2 = v0; g2 < v0 + kValues; g2 += 2) {
+            uint32_t o0[8], o1[8];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+              if (t < p.tp + p.tw) {
+                const WindowGroup wg = window_group(p, wk.s, t, g2 + i);
+                if (wg.code) {
+                  uint32_t rc[2], zc[2];
+#pragma unroll
+                  for (int u = 0; u < 2; u++) {
+                    const uint4 m = *reinterpret_cast<const uint4*>(wg.meta + 2 * (8 * u + 2 * t4));
+                    const bool ok0 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4);
+                    const bool ok1 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4 + 1);
+                    window_factors<BITS>(ok0 ? m.y : 0u, ok1 ? m.w : 0u, rc[u], zc[u]);
+                  }
+                  widen_values<16>(FromGlobal{wg.code + part_bytes(16)}, rc, zc, w, lane, out);
+                }
+              } else {
+                const int j0 = (t - p.tp - p.tw) * kTile + 16 * (g2 + i);
+                if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale<BITS>(), w, lane, out);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; e++) {
+                o0[4 * i + e] = out[0][e];
+                o1[4 * i + e] = out[1][e];
+              }
+            }
+            tc_st_16x128_x4(tv + 8 * g2, o0);
+            tc_st_16x128_x4(tv + 8 * g2 + (16u << 16), o1);
+          }
+        }
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(KVQ_BAR(v_full, buf));
+        phase ^= 1;
+        if (packed) sl.step(p.stages);
+      }
+    }
+  }
+}
+
+// One warp per half: the MMAs of the half's tiles.  at: shared address of the CTA's data.
 template <int COLS, bool DUAL>
-__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t q_smem, uint32_t p_smem, Walk wk, int half) {
+__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t at, Walk wk, int half) {
+  using S = Split<COLS>;
   constexpr uint32_t kDescQk = mma_desc(COLS, false), kDescPv = mma_desc(COLS, true);
-  const uint32_t tm = sm.tmem;
-  const uint64_t q_desc = smem_desc(q_smem), p_desc = smem_desc(p_smem);
+  const uint32_t ts = sm.tmem + S::kColS + S::kStep * half, to = sm.tmem + S::kColO + S::kStep * half;
+  const uint32_t tk = sm.tmem + S::kColK, tv = sm.tmem + S::kColV;
+  const uint64_t q_desc = smem_desc(at + half * kQBytes), p_desc = smem_desc(at + 2 * kQBytes + half * kPBytes);
+  const uint64_t ones_desc = narrow_desc(at + 2 * kQBytes + 2 * kPBytes);
+  const uint64_t neg_desc = narrow_desc(at + 2 * kQBytes + 2 * kPBytes + kOnesBytes + half * kNegBytes);
   uint32_t ct = 0, n = 0, seg = 0;  // tiles of the CTA, tiles of this half, segments with tiles of this half
   auto pv = [&](uint32_t tile, uint32_t i, bool first) {
     const int buf = tile & 1;
@@ -834,16 +888,15 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
     if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 8; k++)
-        tc_mma(tm + kColO + 64 * half, tm + kColV + 64 * buf + 8 * k, p_desc + (2048 >> 4) * k, kDescPv, !(first && k == 0));
+        tc_mma(to, tv + 64 * buf + 8 * k, p_desc + (2048 >> 4) * k, kDescPv, !(first && k == 0));
       tc_commit(KVQ_BAR(v_free, buf));
       tc_commit(KVQ_BAR(pv_done, half));
     }
     __syncwarp();
   };
   while (wk.next(p)) {
-    bool any = false;
+    bool any = false, prev_first = false;
     uint32_t prev = 0;
-    bool prev_first = false;
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
       const int buf = ct & 1;
       if (!DUAL && buf != half) continue;
@@ -852,10 +905,10 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
       tree_wait(KVQ_BAR(s_free, half), (n & 1) ^ 1, p.a.err, &sm.abort);
       tc_after();
       if (elect_one()) {
+        tc_mma_ss(ts, ones_desc, neg_desc, kDescQk, false);  // - m
 #pragma unroll
         for (int k = 0; k < 8; k++)
-          tc_mma(tm + kColS + 64 * half, tm + kColK + 64 * buf + 8 * k,
-                 q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, k > 0);
+          tc_mma(ts, tk + 64 * buf + 8 * k, q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, true);
         tc_commit(KVQ_BAR(k_free, buf));
         tc_commit(KVQ_BAR(s_full, half));
       }
@@ -902,8 +955,7 @@ __device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
 // A warpgroup: softmax of C of the half's columns (from column cb on) in the
 // half's tiles, and the segment's results for them.
 template <int COLS, bool DUAL>
-__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint32_t sb, uint8_t* q_smem, uint8_t* p_all, Walk wk, int wg,
-                                             int tl) {
+__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint32_t sb, uint8_t* base, Walk wk, int wg, int tl) {
   using S = Split<COLS>;
   constexpr int C = S::kCols;
   static_assert(C == 16 || C == 32);
@@ -912,12 +964,14 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
   const int half = wg / S::kSubs, cb = (wg % S::kSubs) * C;
   const int w = tl >> 5, lane = tl & 31;
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
-  const uint32_t ts = sm.tmem + kColS + 64 * half + cb + lanes, to = sm.tmem + kColO + 64 * half + cb + lanes;
+  const uint32_t ts = sm.tmem + S::kColS + S::kStep * half + cb + lanes, to = sm.tmem + S::kColO + S::kStep * half + cb + lanes;
+  uint8_t* q_smem = base + half * kQBytes;
+  uint8_t* p_all = base + 2 * kQBytes;
   uint8_t* p_smem = p_all + half * kPBytes;
-  float4* col = sm.col[half] + cb / 2;
+  uint8_t* neg_smem = p_all + 2 * kPBytes + kOnesBytes + half * kNegBytes;
   const int id = 1 + wg;  // barriers 1 .. 4: one warpgroup; 5: every softmax thread; 6, 7: one half
   uint32_t ct = 0, n = 0;
-  const float out_scale = 1.0f / value_scale(a.c.bits);
+  const float out_scale = 1.0f / value_scale_of(a.c.bits), q_scale = a.qscale * out_scale;
   while (wk.next(p)) {
     const int b = wk.s / a.c.kv_heads, j = wk.s - b * a.c.kv_heads;
     const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0) + cb;  // first row of these columns
@@ -928,7 +982,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
     for (int i = 0; i < C / 2; i++) l2[i] = make_float2(0.f, 0.f);
     if (mine > 0) {
-      // ---- q' = q lambda sm_scale log2(e) as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
+      // ---- q' = q lambda sm_scale log2(e) / g as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
       const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
                                  : make_float4(1.f, 1.f, 1.f, 1.f);
       uint2 raw[C / 4];
@@ -944,30 +998,23 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
       }
 #pragma unroll
       for (int i = 0; i < C / 4; i++) {
-        const int r = w + 4 * i, rs = cb + r;  // row of the half's Q
-        const float x0 = __uint_as_float(raw[i].x << 16) * a.qscale * lam.x;
-        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * a.qscale * lam.y;
-        const float x2 = __uint_as_float(raw[i].y << 16) * a.qscale * lam.z;
-        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * a.qscale * lam.w;
-        const uint32_t h02 = sat_h2(x0, x2), h13 = sat_h2(x1, x3);
-        const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02));
-        const float2 f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
-        float sum = (f02.x + f02.y) + (f13.x + f13.y);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int rs = cb + w + 4 * i;  // row of the half's Q
+        const float x0 = __uint_as_float(raw[i].x << 16) * q_scale * lam.x;
+        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * q_scale * lam.y;
+        const float x2 = __uint_as_float(raw[i].y << 16) * q_scale * lam.z;
+        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * q_scale * lam.w;
         const int chunk = (lane & 15) >> 1;
-        *reinterpret_cast<uint2*>(q_smem + half * kQBytes + (lane >> 4) * (kQBytes / 2) + rs * 128 +
-                                  ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) = make_uint2(h02, h13);
-        if (lane == 0) {
-          float* cp = reinterpret_cast<float*>(&col[r >> 1]);
-          cp[r & 1] = sum;
-          cp[2 + (r & 1)] = kUnset;
-        }
+        *reinterpret_cast<uint2*>(q_smem + (lane >> 4) * (kQBytes / 2) + rs * 128 + ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) =
+            make_uint2(sat_h2(x0, x2), sat_h2(x1, x3));
+      }
+      if (tl < C) {  // no maximum yet
+        sm.neg[half][cb + tl] = kUnset;
+        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl)) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl) + 128) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(KVQ_BAR(q_full, half));
-      bar_sync(id, 128);
     }
     int done = 0;
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
@@ -978,78 +1025,70 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
         hide = token_valid(p, t, tl) ? 0u : 0xffffffffu;
       tree_wait(KVQ_BAR(s_full, half), n & 1, a.err, &sm.abort);
       tc_after();
-      const float2 kz = sm.kz[ct & 3][tl];
       if (t >= p.tp + p.tw && hide == 0u) {
         const uint32_t(*seen)[4] = sm.seen[ct & 3] + (DUAL ? half * kHalfRows : 0) + cb;
 #pragma unroll
         for (int i = 0; i < C; i++) hide |= (seen[i][w] >> lane & 1u) ? 0u : 1u << i;
       }
-      const float2 rk = splat2(kz.x), zk = splat2(kz.y);
-      float2 x[C / 2];
-      auto scores = [&](bool relative) {  // into x, less the running maxima or not
-        uint32_t d[C];
-        tc_ld(d, ts);
+      uint32_t xb[C];  // scores less the running maxima, as bits
+      tc_ld(xb, ts);
+      if (hide) {
 #pragma unroll
-        for (int i = 0; i < C / 2; i++) {
-          const float4 cp = col[i];
-          x[i] = fma2(rk, make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])),
-                      fma2(make_float2(cp.x, cp.y), zk, relative ? make_float2(cp.z, cp.w) : make_float2(0.f, 0.f)));
-        }
-        if (hide) {
-#pragma unroll
-          for (int i = 0; i < C / 2; i++) {
-            if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
-            if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
-          }
-        }
-      };
-      scores(true);
+        for (int i = 0; i < C; i++)
+          if (hide >> i & 1u) xb[i] = 0xff800000u;  // - infinity
+      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < C / 2; i++) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(x[i].x, x[i].y));
-      if (bar_or(id, 128, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
-        // Column maxima from the scores themselves (a row's first ones were taken
-        // against no maximum); S is read again rather than held.
-        scores(false);
+      for (int i = 0; i < C; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(xb[i]), __uint_as_float(xb[i + 1])));
+      // A segment's first tile has no maxima: its scores come out as they are.  So
+      // do those of a row that has seen nothing yet, which only drafted tiles leave.
+      if (bar_or(id, 128, done == 0 || t >= p.tp + p.tw || fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
         {
           float v[C];
 #pragma unroll
-          for (int i = 0; i < C / 2; i++) { v[2 * i] = x[i].x; v[2 * i + 1] = x[i].y; }
+          for (int i = 0; i < C; i++) v[i] = __uint_as_float(xb[i]);
           warp_columns<C, true>(v, lane);
           sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
         }
         bar_sync(id, 128);
         if (tl < C) {
           const int c = cb + tl;
-          float* cp = reinterpret_cast<float*>(&col[tl >> 1]) + 2 + (tl & 1);
-          const float neg = *cp;
-          float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
-          float f = 0.f;
-          if (neg != kUnset) {
-            m = fmaxf(m, -neg);
-            f = ex2(-neg - m);
+          const float old = sm.neg[half][c];
+          const float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
+          float shift = 0.f, f = 1.f;
+          if (old == kUnset ? m > -INFINITY : m > 0.f) {  // a row that has seen nothing stays unset
+            const float base_neg = old == kUnset ? 0.f : old;
+            const float want = (base_neg - m) * (1.0f / kNegScale);
+            const float hi = __half2float(__float2half_rn(want)), lo = __half2float(__float2half_rn(want - hi));
+            const float neg = (hi + lo) * kNegScale;  // what the MMA will add
+            shift = neg - base_neg;
+            f = old == kUnset ? 0.f : ex2(shift);
+            sm.neg[half][c] = neg;
+            *reinterpret_cast<uint32_t*>(neg_smem + narrow_at(c)) = pack_h2(hi, lo);
+            fence_async_smem();
           }
           sm.alpha[half][c] = f;
-          *cp = m == -INFINITY ? kUnset : -m;  // a row that has seen nothing stays unset
+          sm.shift[half][c] = shift;
         }
         bar_sync(id, 128);
-        const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
         if (done > 0) {  // O so far, once the last product is in
+          const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
           tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);
           tc_after();
-          uint32_t o[C];
-          tc_ld(o, to);
+#pragma unroll 1
+          for (int c0 = 0; c0 < C; c0 += 16) {
+            uint32_t o[16];
+            tc_ld(o, to + c0);
 #pragma unroll
-          for (int i = 0; i < C / 2; i++) {
-            const float2 f = al[i];
-            o[2 * i] = __float_as_uint(__uint_as_float(o[2 * i]) * f.x);
-            o[2 * i + 1] = __float_as_uint(__uint_as_float(o[2 * i + 1]) * f.y);
-            l2[i] = mul2(l2[i], f);
+            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.alpha[half][cb + c0 + i]);
+            tc_st(to + c0, o);
           }
-          tc_st(to, o);
+#pragma unroll
+          for (int i = 0; i < C / 2; i++) l2[i] = mul2(l2[i], al[i]);
           tc_wait_st();
         }
-        scores(true);
+#pragma unroll
+        for (int i = 0; i < C; i++) xb[i] = __float_as_uint(__uint_as_float(xb[i]) + sm.shift[half][cb + i]);
       }
       tc_before();  // S is in registers: the next tile's product may start
       __syncwarp();
@@ -1060,8 +1099,9 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float2 pr = make_float2(ex2(x[4 * q + e].x), ex2(x[4 * q + e].y));
-          l2[4 * q + e] = add2(l2[4 * q + e], pr);
+          const int i = 4 * q + e;
+          const float2 pr = make_float2(ex2(__uint_as_float(xb[2 * i])), ex2(__uint_as_float(xb[2 * i + 1])));
+          l2[i] = add2(l2[i], pr);
           h[e] = pack_h2(pr.x, pr.y);
         }
         *reinterpret_cast<uint4*>(p_smem + tl * 128 + (((cb / 8 + q) ^ (tl & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -1085,7 +1125,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
     if (tl < C) {
       const float* r = &sm.red[half][0][cb + tl];
       const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
-      const float neg = mine > 0 ? reinterpret_cast<const float*>(&col[tl >> 1])[2 + (tl & 1)] : kUnset;
+      const float neg = mine > 0 ? sm.neg[half][cb + tl] : kUnset;
       sm.ml[half][cb + tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
     }
     if (mine > 0) {
@@ -1138,12 +1178,12 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
     } else {
       // join the halves: half 1 hands its O over in shared memory (both P areas: [COLS][128] fp32)
       bar_sync(5, kSoftThreads);  // ml of both; every product of both halves is in
-      float* xb = reinterpret_cast<float*>(p_all) + cb * kTile;
+      float* other_o = reinterpret_cast<float*>(p_all) + cb * kTile;
       if (half == 1 && mine > 0) {
         uint32_t o[C];
         tc_ld(o, to);
 #pragma unroll
-        for (int i = 0; i < C; i++) xb[i * kTile + tl] = __uint_as_float(o[i]);
+        for (int i = 0; i < C; i++) other_o[i * kTile + tl] = __uint_as_float(o[i]);
       }
       tc_before();
       bar_sync(5, kSoftThreads);
@@ -1160,7 +1200,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
           const float m = fmaxf(m0.x, m1.x);
           const float f0 = m0.y != 0.f ? ex2(m0.x - m) : 0.f, f1 = m1.y != 0.f ? ex2(m1.x - m) : 0.f;
           float v = mine > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
-          if (other > 0) v = fmaf(xb[i * kTile + tl], f1, v);
+          if (other > 0) v = fmaf(other_o[i * kTile + tl], f1, v);
           const float l = m0.y * f0 + m1.y * f1;
           if (whole) {
             o[i] = __float_as_uint(l != 0.f ? v * out_scale / l : 0.f);
@@ -1173,8 +1213,8 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
           }
         }
         if (whole) {
-          bar_sync(id, 128);  // xb is read
-          uint8_t* sh = reinterpret_cast<uint8_t*>(xb);
+          bar_sync(id, 128);  // other_o is read
+          uint8_t* sh = reinterpret_cast<uint8_t*>(other_o);
 #pragma unroll
           for (int i = 0; i < C; i++)
             reinterpret_cast<__nv_bfloat16*>(sh)[i * kHeadDim + ch] = __float2bfloat16_rn(__uint_as_float(o[i]));
@@ -1197,16 +1237,14 @@ __device__ __forceinline__ void regs_down() {
 }
 
 template <int COLS, bool DUAL>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreePlan p) {
+__global__ void __launch_bounds__(Split<COLS>::kThreads, 1) tree_kernel(const __grid_constant__ TreePlan p) {
   using S = Split<COLS>;
-  constexpr int kKey0 = S::kSoft, kValue0 = kKey0 + S::kWiden, kCtl0 = kValue0 + S::kWiden;
+  constexpr int kWiden0 = S::kSoft, kCtl0 = kWiden0 + S::kWiden;
   extern __shared__ uint8_t raw[];
   const uint32_t raw_at = smem_u32(raw), smem_at = (raw_at + 1023u) & ~1023u;
-  const uint32_t sb = smem_at + 2 * kQBytes + 2 * kPBytes, ring_at = smem_at + kFixedBytes;
+  const uint32_t sb = smem_at + kSmallAt, ring_at = smem_at + kFixedBytes;
   uint8_t* base = raw + (smem_at - raw_at);
-  uint8_t* q_smem = base;
-  uint8_t* p_smem = base + 2 * kQBytes;
-  Small& sm = *reinterpret_cast<Small*>(base + 2 * kQBytes + 2 * kPBytes);
+  Small& sm = *reinterpret_cast<Small*>(base + kSmallAt);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == kCtl0 + 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
@@ -1215,56 +1253,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int i = 0; i < kMaxStages; i++) {
-      mbar_init(smem_u32(&sm.ring_full[i]), 1);
-      mbar_init(smem_u32(&sm.ring_free[i]), 2 * S::kWiden);
+      mbar_init(KVQ_BAR(ring_full, i), 1);
+      mbar_init(KVQ_BAR(ring_free, i), 4 * S::kShare);
     }
     for (int i = 0; i < 2; i++) {
-      mbar_init(smem_u32(&sm.k_full[i]), S::kWiden);
-      mbar_init(smem_u32(&sm.k_free[i]), DUAL ? 2 : 1);
-      mbar_init(smem_u32(&sm.v_full[i]), S::kWiden);
-      mbar_init(smem_u32(&sm.v_free[i]), DUAL ? 2 : 1);
-      mbar_init(smem_u32(&sm.q_full[i]), S::kSoft / 2);
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.s_free[i]), S::kSoft / 2);
-      mbar_init(smem_u32(&sm.p_full[i]), S::kSoft / 2);
-      mbar_init(smem_u32(&sm.pv_done[i]), 1);
-      mbar_init(smem_u32(&sm.drain[i]), 1);
+      mbar_init(KVQ_BAR(k_full, i), 4 * S::kShare);
+      mbar_init(KVQ_BAR(k_free, i), DUAL ? 2 : 1);
+      mbar_init(KVQ_BAR(v_full, i), 4 * S::kShare);
+      mbar_init(KVQ_BAR(v_free, i), DUAL ? 2 : 1);
+      mbar_init(KVQ_BAR(q_full, i), S::kSoft / 2);
+      mbar_init(KVQ_BAR(s_full, i), 1);
+      mbar_init(KVQ_BAR(s_free, i), S::kSoft / 2);
+      mbar_init(KVQ_BAR(p_full, i), S::kSoft / 2);
+      mbar_init(KVQ_BAR(pv_done, i), 1);
+      mbar_init(KVQ_BAR(drain, i), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x < kTile) {  // the constant operand of the extra k-step
+    uint8_t* ones = base + 2 * kQBytes + 2 * kPBytes + narrow_at(threadIdx.x);
+    *reinterpret_cast<uint4*>(ones) = make_uint4(splat_h(pow2_h(8)), 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(ones + 128) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
   }
   tc_before();
   __syncthreads();
   tc_after();
   pdl_wait();  // the cache, q, k, v and the mask may be written by earlier kernels
   const Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
-  if (warp < kKey0) {
-    if constexpr (S::kSoftRegs > 72) regs_up<S::kSoftRegs>(); else regs_down<S::kSoftRegs>();
-    softmax_role<COLS, DUAL>(p, sm, sb, q_smem, p_smem, wk, warp >> 2, threadIdx.x & 127);
+  if (warp < kWiden0) {
+    regs_up<S::kSoftRegs>();
+    softmax_role<COLS, DUAL>(p, sm, sb, base, wk, warp >> 2, threadIdx.x & 127);
   } else if (warp < kCtl0) {
-    if constexpr (S::kWidenRegs > 72) regs_up<S::kWidenRegs>(); else regs_down<S::kWidenRegs>();
-    if (warp < kValue0) {
-      switch (p.a.c.bits) {
-        case 2: key_role<2, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
-        case 4: key_role<4, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
-        case 8: key_role<8, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
-        default: key_role<16, S::kWiden>(p, sm, sb, ring_at, wk, warp - kKey0, lane); break;
-      }
-    } else {
-      switch (p.a.c.bits) {
-        case 2: value_role<2, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
-        case 4: value_role<4, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
-        case 8: value_role<8, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
-        default: value_role<16, S::kWiden>(p, sm, sb, ring_at, wk, warp - kValue0, lane); break;
-      }
+    if constexpr (S::kWidenRegs > S::kRegs) regs_up<S::kWidenRegs>();
+    if constexpr (S::kWidenRegs < S::kRegs) regs_down<S::kWidenRegs>();
+    const int group = (warp - kWiden0) >> 2, buf = group & 1, part = group >> 1, w = warp & 3;
+    switch (p.a.c.bits) {
+      case 2: widen_role<2, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
+      case 4: widen_role<4, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
+      case 8: widen_role<8, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
+      default: widen_role<16, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
     }
   } else {
     regs_down<S::kCtlRegs>();
-    if (warp == kCtl0) {
+    if (warp == kCtl0)
       produce(p, sm, sb, ring_at, wk);
-    } else if (warp < kCtl0 + 3) {
-      const int half = warp - kCtl0 - 1;
-      mma_role<COLS, DUAL>(p, sm, sb, smem_at + half * kQBytes, smem_at + 2 * kQBytes + half * kPBytes, wk, half);
-    }
+    else if (warp < kCtl0 + 3)
+      mma_role<COLS, DUAL>(p, sm, sb, smem_at, wk, warp - kCtl0 - 1);
     __syncwarp();
   }
   tc_before();
@@ -1275,55 +1310,89 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 }
 
 // Joins the partial records of one block of rows: a CTA per (stream, block of
-// rows, 8 rows); a thread per tensor-memory row (channel).
+// rows, 4 rows), a thread per tensor-memory row (channel).  Every record's max
+// and sum come first, all in flight at once; then the weights; then the outputs.
 constexpr int kMergeRows = 4;
+constexpr int kMergeRecords = 256;  // more than CTAs of a launch
 __global__ void __launch_bounds__(kHeadDim) tree_merge_kernel(const __grid_constant__ TreePlan p) {
-  pdl_wait();
+  __shared__ float wt[kMergeRows][kMergeRecords], ls[kMergeRows][kMergeRecords], sum[kMergeRows];
+  __shared__ __align__(16) __nv_bfloat16 sh[kMergeRows][kHeadDim];
   const TreeArgs& a = p.a;
   const int x = blockIdx.x, s = x / p.blocks, block = x - s * p.blocks;
   const int c0 = cta_of(p.units, p.grid, x * p.tiles), c1 = cta_of(p.units, p.grid, x * p.tiles + p.tiles - 1);
-  if (c0 == c1) return;
   const int b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
   const int first = cta_begin(p.units, p.grid, c0) == x * p.tiles ? 0 : 1;  // the record of CTA c0
-  const float out_scale = 1.0f / value_scale(a.c.bits);
-  __shared__ __align__(16) __nv_bfloat16 sh[kMergeRows][kHeadDim];
-  const int ch = channel_of(threadIdx.x);
-  const int rb = blockIdx.y * kMergeRows;
-  for (int i = 0; i < kMergeRows; i++) {
-    const int r = rb + i;
-    if (r >= p.block_rows || block * p.block_rows + r >= p.rows) break;
-    const float* rec = p.parts + ((size_t)c0 * 2 + first) * p.rec;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int c = c0; c <= c1; c++) {
-      const float* q = c == c0 ? rec : p.parts + (size_t)c * 2 * p.rec;
-      const float mk = q[r], lk = q[p.block_rows + r], ok = q[2 * p.block_rows + r * kHeadDim + threadIdx.x];
-      if (lk == 0.f) continue;
-      const float mn = fmaxf(m, mk), f = ex2(m - mn), fk = ex2(mk - mn);
-      l = l * f + lk * fk;
-      o = o * f + ok * fk;
-      m = mn;
-    }
-    sh[i][ch] = __float2bfloat16_rn(l != 0.f ? o * out_scale / l : 0.f);
+  const float* p0 = p.parts + ((size_t)c0 * 2 + first) * p.rec;
+  const float* p1 = p.parts + (size_t)(c0 + 1) * 2 * p.rec;  // record k >= 1 at p1 + (k - 1) 2 rec
+  const int nrec = c1 - c0 + 1, rb = blockIdx.y * kMergeRows;
+  const int rows = min(kMergeRows, min(p.block_rows, p.rows - block * p.block_rows) - rb);
+  pdl_wait();
+  if (nrec == 1 || rows <= 0) return;
+  auto record = [&](int k) { return k == 0 ? p0 : p1 + (size_t)(k - 1) * 2 * p.rec; };
+  for (int i = threadIdx.x; i < nrec * kMergeRows; i += kHeadDim) {
+    const int k = i / kMergeRows, r = i % kMergeRows;
+    wt[r][k] = r < rows ? __ldcg(record(k) + rb + r) : 0.f;
+    ls[r][k] = r < rows ? __ldcg(record(k) + p.block_rows + rb + r) : 0.f;
   }
   __syncthreads();
+  {  // warp r: row r
+    const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f;
+    for (int k = lane; k < nrec; k += 32)
+      if (ls[r][k] != 0.f) m = fmaxf(m, wt[r][k]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k = lane; k < nrec; k += 32) {
+      const float w = ls[r][k] != 0.f ? ex2(wt[r][k] - m) : 0.f;
+      wt[r][k] = w;
+      l = fmaf(w, ls[r][k], l);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) sum[r] = l != 0.f ? 1.0f / (value_scale_of(a.c.bits) * l) : 0.f;
+  }
+  __syncthreads();
+  const int ch = channel_of(threadIdx.x);
+  float acc[kMergeRows] = {0.f, 0.f, 0.f, 0.f};
+  // a record's O is uninitialised where its sum is zero (no tile of the half, or no row)
+#pragma unroll 4
+  for (int k = 0; k < nrec; k++) {
+    const float* o = record(k) + 2 * p.block_rows + rb * kHeadDim + threadIdx.x;
+#pragma unroll
+    for (int r = 0; r < kMergeRows; r++) {
+      const float v = r < rows ? __ldcg(o + r * kHeadDim) : 0.f;
+      acc[r] += wt[r][k] != 0.f ? wt[r][k] * v : 0.f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kMergeRows; r++) sh[r][ch] = __float2bfloat16_rn(acc[r] * sum[r]);
+  __syncthreads();
   if (threadIdx.x < kMergeRows * 16) {
-    const int i = threadIdx.x >> 4, q = threadIdx.x & 15, r = rb + i;
-    const int row = block * p.block_rows + r;
-    if (r < p.block_rows && row < p.rows) {
-      const int node = row / a.group, g = row - node * a.group;
+    const int i = threadIdx.x >> 4, q = threadIdx.x & 15;
+    if (i < rows) {
+      const int row = block * p.block_rows + rb + i, node = row / a.group, g = row - node * a.group;
       reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim)[q] =
           reinterpret_cast<const uint4*>(sh[i])[q];
     }
   }
 }
+static_assert(kMergeRows * 32 == kHeadDim, "a warp per row");
 
 template <int COLS, bool DUAL>
 cudaError_t launch_cols(const TreePlan& p, cudaStream_t s) {
   const size_t smem = kFixedBytes + (size_t)p.stages * p.stage_bytes + 1024;
-  if (cudaError_t e = cudaFuncSetAttribute(tree_kernel<COLS, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
-    return e;
-  return launch_pdl(tree_kernel<COLS, DUAL>, dim3(p.grid), dim3(kTreeThreads), smem, s, p);
+  // once per device: the attribute is the kernel's on that device
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev > 63 || !(set.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(tree_kernel<COLS, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024))
+      return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_pdl(tree_kernel<COLS, DUAL>, dim3(p.grid), dim3(Split<COLS>::kThreads), smem, s, p);
 }
 
 }  // namespace
@@ -1355,10 +1424,10 @@ cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
   const long long units = (long long)a.c.batch * a.c.kv_heads * p.blocks * p.tiles;
   if (units > 0x7fffffffLL || a.num_sms < 1) return cudaErrorInvalidValue;
   p.units = (int)units;
-  p.grid = (int)(units < a.num_sms ? units : a.num_sms);
+  p.grid = (int)std::min<long long>(units, std::min(a.num_sms, kMergeRecords));
   p.stage_bytes = kTileGroups * (group_bytes(a.c.bits) + 128) + 4 * kHeadDim;
   p.stages = (kSmemMax - kFixedBytes) / p.stage_bytes;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages = std::min(p.stages, kMaxStages) & ~1;  // one ring per buffer
   if (p.stages < 2) return cudaErrorInvalidValue;
   p.rec = p.block_rows * (2 + kHeadDim);
   p.parts = static_cast<float*>(a.ws);

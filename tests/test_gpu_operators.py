@@ -191,9 +191,10 @@ def test_rope_refusals(kvq):
 MODES = ["plain", "window", "channel"]
 
 
-def make_cache(kvq, mode, B, H, T, fbit, n_f, seed=0, lam=True, direct=False, chunk=0):
+def make_cache(kvq, mode, B, H, T, fbit, n_f, seed=0, lam=True, direct=False, chunk=0, sample=None):
     """A cache of T random tokens (Keys with loud channels) and the values it holds, fp32 [B][H][T][128] each, by the
-    codes and meta that export gives (lambda undone).  ks.centre, vs.centre: the centres of their groups."""
+    codes and meta that export gives (lambda undone).  ks.centre, vs.centre: the centres of their groups.
+    sample: of the one stream (b, h) only."""
     per = B * H * 2 * (16 * fbit + 4)
     cache = kvq.KVQCache(1, B, H, n_f * per, [fbit], sink_window=mode == "window", key_channel=mode == "channel")
     k, v = S.keys_values(seed, 0, B, max(T, 1), H, 0, 4, dtype=torch.float32)
@@ -209,15 +210,18 @@ def make_cache(kvq, mode, B, H, T, fbit, n_f, seed=0, lam=True, direct=False, ch
         n = min(chunk or T, T - at)
         cache.append(0, k[:, at:at + n].contiguous().cuda(), v[:, at:at + n].contiguous().cuda())
         at += n
-    return (cache, scale) + held(kvq, cache, mode, B, H, T, scale)
+    return (cache, scale) + held(kvq, cache, mode, B, H, T, scale, sample)
 
 
 def half(bits):
     return bits.view(np.float16).astype(np.float32)
 
 
-def held(kvq, cache, mode, B, H, T, scale):
+def held(kvq, cache, mode, B, H, T, scale, sample=None):
     bits = cache.query(0)["bits"]
+    streams = [sample] if sample else [(b, j) for b in range(B) for j in range(H)]
+    if sample:
+        B = H = 1
     ks, vs = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 128), np.float32)
 
     kcen, vcen = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 1), np.float32)
@@ -228,29 +232,29 @@ def held(kvq, cache, mode, B, H, T, scale):
     def values(codes, r, z, b):
         return (codes.astype(np.float32) * (r / np.float32(2 ** b - 1)) + z).astype(np.float32)
 
-    for b in range(B):
-        for j in range(H):
-            kc, vc, km, vm = cache.export(0, b, j)
-            n = len(kc)
-            off = 1 if mode == "window" else 0
-            if n:
-                if mode == "channel":
-                    kr = np.repeat(half(km[:, 0]).reshape(-1, 128), 128, 0)
-                    kz = np.repeat(half(km[:, 1]).reshape(-1, 128), 128, 0)
-                else:
-                    kr, kz = half(km[:, 0])[:, None], half(km[:, 1])[:, None]
-                ks[b, j, off:off + n] = values(kc, kr, kz, bits)
-                vs[b, j, off:off + n] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
-                kcen[b, j, off:off + n] = centre(kr, kz, bits)
-                vcen[b, j, off:off + n] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
-            if mode != "plain":
-                kc, vc, km, vm = cache.export_window(0, b, j)
-                m = len(kc)
-                at = list(range(T - m, T)) if mode == "channel" else ([0] + list(range(T - m + 1, T)) if m else [])
-                ks[b, j, at] = values(kc, half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
-                vs[b, j, at] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
-                kcen[b, j, at] = centre(half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
-                vcen[b, j, at] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
+    for sb, sj in streams:
+        b, j = (0, 0) if sample else (sb, sj)
+        kc, vc, km, vm = cache.export(0, sb, sj)
+        n = len(kc)
+        off = 1 if mode == "window" else 0
+        if n:
+            if mode == "channel":
+                kr = np.repeat(half(km[:, 0]).reshape(-1, 128), 128, 0)
+                kz = np.repeat(half(km[:, 1]).reshape(-1, 128), 128, 0)
+            else:
+                kr, kz = half(km[:, 0])[:, None], half(km[:, 1])[:, None]
+            ks[b, j, off:off + n] = values(kc, kr, kz, bits)
+            vs[b, j, off:off + n] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
+            kcen[b, j, off:off + n] = centre(kr, kz, bits)
+            vcen[b, j, off:off + n] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
+        if mode != "plain":
+            kc, vc, km, vm = cache.export_window(0, sb, sj)
+            m = len(kc)
+            at = list(range(T - m, T)) if mode == "channel" else ([0] + list(range(T - m + 1, T)) if m else [])
+            ks[b, j, at] = values(kc, half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
+            vs[b, j, at] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
+            kcen[b, j, at] = centre(half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
+            vcen[b, j, at] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
     if scale is not None:
         ks = ks * scale.numpy()[None, :, None, :]
         kcen = kcen * scale.numpy()[None, :, None, :]
@@ -421,6 +425,22 @@ def test_tree_lengths(kvq, T, fbit):
     q, dk, dv = tree_inputs(T, 1, 5, 1, 6)
     out = cache.tree_attn(0, q, dk, dv)
     tree_check(q, dk, dv, None, ks, vs, out)
+
+
+@pytest.mark.parametrize("fbit", [2, 4, 8, 16])
+@pytest.mark.parametrize("n,G", [(1, 5), (4, 7), (9, 6), (15, 7), (40, 7)])
+def test_tree_many_tiles(kvq, fbit, n, G):
+    """Shares of many tiles and several streams a CTA at every width and division of the warps: the ring and the
+    buffers wrap many times, and drafted tiles (an odd number of them here) change which buffer a tile takes."""
+    B, H, T = 16, 4, 4500
+    cache, _, ks, vs = make_cache(kvq, "plain", B, H, T, fbit, 4608, lam=False, sample=(B - 1, H - 1))
+    q, dk, dv = tree_inputs(fbit + n, B, n, H, G)
+    outs = [cache.tree_attn(0, q, dk, dv) for _ in range(3)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    one = slice(B - 1, B), slice(H - 1, H)
+    tree_check(q[one[0], :, (H - 1) * G:], dk[one[0], :, one[1]], dv[one[0], :, one[1]], None, ks, vs,
+               outs[0][one[0], :, (H - 1) * G:])
+    cache.device_status()
 
 
 def test_tree_long(kvq):

@@ -81,8 +81,13 @@ def test_rope_schedule_object(kvq):
 
 # ---------------------------------------------------------------- refusals
 
+class Rows(C.Structure):
+    """kvq_rows of include/kvq.h."""
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_longlong), ("stride_t", C.c_longlong), ("stride_h", C.c_longlong)]
+
+
 def _rows(kvq, ptr, b=512, t=256, h=128):
-    return kvq.Rows(ptr, b, t, h)
+    return Rows(ptr, b, t, h)
 
 
 def _rope(kvq, **kw):

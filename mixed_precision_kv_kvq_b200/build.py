@@ -11,11 +11,11 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libkvq.so"
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_shrink.cu", "kvq_decode.cu", "kvq_bitalloc.cu", "kvq_rope.cu", "kvq_read.cu",
-           "kvq_tree.cu"]
+           "kvq_tree.cu", "kvq_tree_2.cu", "kvq_tree_4.cu", "kvq_tree_8.cu", "kvq_tree_16.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC", "-shared", "--threads", "0",
     "-I", str(ROOT / "include"),
 ]
 

@@ -1,1313 +1,15 @@
-// kvq_tree.cu -- attention of a tree of drafted tokens over the packed cache
-// and over one another (kvq_tree_attn).
-//
-// For one (sequence, KV head) stream the n nodes' G query heads are R = n G
-// rows r, and with s the scores in log2 units
-//   s[t][r] = (q_r lambda sm_scale log2 e) . k^_t          (cached token t)
-//   out_r   = sum_t 2^(s[t][r] - m_r) v^_t / sum_t 2^(s[t][r] - m_r),
-// the drafted tokens being further tokens t that a mask hides from some rows.
-//
-// Products on tcgen05, tokens as rows.  A tile is 128 tokens.  Both products
-// take their left operand from tensor memory and a narrow right operand from
-// shared memory, so their cost follows the number of query rows (16, 32 or 64
-// columns a half, below) and not a fixed 128:
-//   S[token][row]   = K[token][channel]   Q[row][channel]^T
-//   O[channel][row] += V[token][channel]^T P[token][row]
-// The cache's lane units are what tcgen05.st takes: lane 4g + t of a warp
-// holds tokens g, g + 8 and four neighbouring channels of each Key quad
-// (16x256b: rows lane / 4 and + 8, two columns a lane), and one channel of two
-// neighbouring tokens in each Value pair (16x128b, one column a lane), so
-// codes are widened in registers and stored once, with no transposition.
-// Codes become val = (c - 2^(b-1)) 2^(1-b) first, exact in fp16 at 8 bits and
-// fewer (rounded to 11 bits at 16), then one fma gives the value times
-// g = (1 - 2^-b) / 2: x g = val R/4 + (Z g + R/4).  With this g R/4 is exact,
-// the value is rounded twice (its centre Z g + R/4, then itself), and nothing
-// in binary16's range overflows.  1/g goes into the query and the output.
-// S has a token per tensor-memory lane: a thread owns one token and walks the
-// rows, so whether a token counts is a register, P is written row by row as the
-// K-slices that an MN-major operand wants (16-byte stores, 128-byte swizzle),
-// and row sums are per-thread partial sums until the end.  A row's running
-// maximum m_r is shared by the 128 threads and subtracted by the MMA itself:
-// one more k-step multiplies a constant left operand (256, 256, 0, ...) with
-// -m_r / 256 as an fp16 pair (high + low part), so a thread's score is ready for
-// the exponential as it comes out of tensor memory.  (Read from shared memory
-// instead, the per-row terms took 16 LDS.128 per 32 rows and thread, ~1000 cycles
-// of a tile's 3800.)  m_r moves only when some score exceeds it by more than
-// 2^8 (one vote per 32 rows), and only then are column maxima formed and O
-// rescaled in tensor memory.
-//
-// Roles (one CTA per SM, which holds all 512 tensor-memory columns): 8 or 16
-// softmax warps, groups of four widening warps, one warp streaming packed tiles
-// with bulk copies, two issuing MMAs.  The softmax warps form two halves, each
-// with an issuer, S, P, Q and O of its own.  With up to 64 rows the halves take
-// alternate tiles of the same rows (two independent softmax states, joined at
-// the end); above, each takes 64 of 128 rows of every tile.  Two widened tiles
-// fit beside S and O; the widening warps of a buffer (four, or eight that share
-// a tile's groups where few rows leave them more of the work) take every second
-// tile whole, so the fixed cost of a tile (waits, fences) falls on few warps.
-//
-// Phases.  A wait tells apart only two successive phases of a barrier, so every
-// waiter has to see each phase of the barriers it waits on: the ring is one
-// ring per buffer (its slots are never read by the other buffer's warps), and
-// in alternate tiles a buffer belongs to one half.
-//
-// Work split: the (stream, block of rows, tile) units form one line that is cut
-// evenly over the grid; a CTA writes the rows it covers whole, and leaves a
-// partial (max, sum, O) of at most two others in the workspace, which
-// tree_merge_kernel joins.  Every wait is bounded: a wait that gives up raises
-// the cache's error flag and the CTA's abort flag, after which all waits return
-// at once and the loops run out.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <algorithm>
-#include <atomic>
-
-#include "kvq_decode_common.cuh"
-#include "kvq_view.cuh"
+// kvq_tree.cu -- tree attention, host side: how a call's work is divided
+// (kvq_tree.cuh has the kernel), and the kernel that joins partial results.
+#include "kvq_tree.cuh"
 
 namespace kvq {
+
+extern template cudaError_t launch_tree_bits<2>(const TreePlan& p, cudaStream_t s);
+extern template cudaError_t launch_tree_bits<4>(const TreePlan& p, cudaStream_t s);
+extern template cudaError_t launch_tree_bits<8>(const TreePlan& p, cudaStream_t s);
+extern template cudaError_t launch_tree_bits<16>(const TreePlan& p, cudaStream_t s);
+
 namespace {
-
-constexpr int kTile = 128;           // tokens per tile
-constexpr int kTileGroups = kTile / kGroupTokens;
-constexpr int kMaxStages = 8;
-constexpr int kHalfRows = 64;        // rows of a half's operands in shared memory
-constexpr int kQBytes = kHalfRows * kHeadDim * 2;  // one half's Q: two 64-channel slabs of [64][128 B]
-constexpr int kPBytes = kTile * 128;               // one half's P: [128 tokens][64 rows] fp16
-constexpr float kUnset = 1e30f;      // -m of a row with no token yet
-
-// How the warps are divided, the registers of each kind (setmaxnreg from what the
-// launch gives) and tensor memory's columns.  With 64 rows a half (128 rows a
-// CTA, or 64 in alternate tiles) a half's rows are divided over two
-// warpgroups: 32 rows a thread is what its registers hold.
-template <int COLS>
-struct Split {
-  static constexpr int kSoft = COLS == 64 ? 16 : 8;       // softmax warps
-  static constexpr int kShare = COLS == 64 ? 1 : 2;       // widening groups that share a tile
-  static constexpr int kWiden = 8 * kShare;               // widening warps: groups of 4 for each of the two buffers
-  static constexpr int kWarps = kSoft + kWiden + 4;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kSubs = kSoft / 8;                 // softmax warpgroups per half
-  static constexpr int kCols = COLS / kSubs;              // rows per softmax thread
-  static constexpr int kRegs = 72;                        // at launch
-  static constexpr int kSoftRegs = COLS == 64 ? 88 : COLS == 32 ? 96 : 80;
-  static constexpr int kWidenRegs = COLS == 64 ? 64 : COLS == 32 ? 72 : 80;
-  static constexpr int kCtlRegs = 24;
-  static_assert(kWarps == 28 && 65536 / kThreads / 8 * 8 == kRegs);
-  static_assert(32 * (kSoft * kSoftRegs + kWiden * kWidenRegs + 4 * kCtlRegs) <= kThreads * kRegs);
-  static constexpr uint32_t kStep = COLS == 64 ? 64 : 32;  // columns of one half's S or O
-  static constexpr uint32_t kColS = 0, kColO = 2 * kStep, kColK = 4 * kStep, kColV = kColK + 128;
-  static_assert(kColV + 128 <= 512);
-};
-constexpr int kOnesBytes = kTile * 32;             // constant left operand of the extra k-step: [128][16] fp16
-constexpr int kNegBytes = kHalfRows * 32;          // one half's -m / 256: [64][16] fp16
-constexpr float kNegScale = 256.0f;                // -m up to 1.6e7, to 22 bits
-
-struct Small {
-  float neg[2][kHalfRows];           // per half: -m as the MMA subtracts it (kUnset: no token yet, 0 there)
-  float alpha[2][kHalfRows];         // factor of the last rescaling
-  float shift[2][kHalfRows];         // and what it added to the scores
-  float red[2][4][kHalfRows];        // per warp: column maxima, then row sums
-  float2 ml[2][kHalfRows];           // final (m, l)
-  uint32_t seen[4][kTile][4];        // drafted tile t: bit i of word w: the row sees token 32 w + i
-  uint64_t ring_full[kMaxStages], ring_free[kMaxStages];
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
-  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
-  uint32_t tmem;
-  volatile int abort;
-};
-constexpr int kSmallBytes = (sizeof(Small) + 1023) / 1024 * 1024;
-constexpr int kSmallAt = 2 * kQBytes + 2 * kPBytes + kOnesBytes + 2 * kNegBytes;
-constexpr int kFixedBytes = kSmallAt + kSmallBytes;
-constexpr int kSmemMax = 227 * 1024 - 1024;  // the base is aligned by hand
-
-struct TreePlan {
-  TreeArgs a;
-  Fill f;               // progressive cache (group order)
-  int groups;           // groups of a stream's progressive cache
-  int part_group, part_valid;  // the one group that may be partial, and its tokens
-  int rows, block_rows, blocks;  // query rows of a stream, rows per block, blocks
-  int tp, tw, td, tiles;         // progressive, window and drafted tiles of a stream
-  int units, grid;
-  int stages, stage_bytes;
-  int rec;              // floats of one partial record
-  float* parts;         // [grid][2][rec]: m[block_rows], l[block_rows], O[block_rows][128]
-};
-
-__host__ __device__ __forceinline__ int cta_begin(int units, int grid, int i) { return (int)((long long)units * i / grid); }
-__host__ __device__ __forceinline__ int cta_of(int units, int grid, int u) {
-  return (int)((((long long)u + 1) * grid - 1) / units);
-}
-
-// ------------------------------------------------------------------ PTX
-
-// Bounded wait: gives up after kWaitNs or once another wait of the CTA has.  The
-// test itself suspends the warp for a while; the clock is read on few of them.
-__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
-  if (mbar_try(bar, parity)) return;
-  unsigned it = 0;
-  unsigned long long t0 = 0;
-  while (!mbar_try(bar, parity)) {
-    if (*abort) return;
-    if ((++it & 255u) == 0u) {
-      const unsigned long long now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitNs) {
-        *abort = 1;
-        atomicExch(err, 1);
-        return;
-      }
-    }
-  }
-}
-// One lane of a converged warp.  MMAs and copies are issued under this
-// predicate by warps that run their loops whole: with `if (lane == 0)` instead,
-// every tcgen05.mma took ~108 cycles to issue (operands moved to uniform
-// registers lane by lane) whatever its size; so it is 30-40.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-// Also after an abort: what is in flight lands before the CTA ends.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = global_ns();
-  while (!mbar_try(bar, parity))
-    if (global_ns() - t0 > kWaitNs) break;
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ bool bar_or(int id, int n, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(n), "r"((uint32_t)p)
-      : "memory");
-  return r != 0;
-}
-// One 128 x N x 16 step: A [128][16] fp16 in tensor memory, B in shared memory.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// The same with A in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// Instruction descriptor: fp16 A and B, fp32 D, M = 128; b_mn: B is MN-major.
-__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn) {
-  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
-}
-// Shared-memory descriptor: 128-byte swizzle, 1024 bytes between the 8-row
-// groups (rows of Q along N, tokens of P along K); one 64-element atom wide.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
-
-// [rows][16] fp16, K-major without swizzle: 8 x 16-byte core matrices, the two
-// along K 128 bytes apart, 256 bytes between 8-row groups.
-__device__ __forceinline__ uint64_t narrow_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-__host__ __device__ constexpr int narrow_at(int row) { return (row >> 3) * 256 + (row & 7) * 16; }  // elements 0 .. 7
-
-#define KVQ_R4(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3])
-#define KVQ_R16(r, i) KVQ_R4(r, i), KVQ_R4(r, (i) + 4), KVQ_R4(r, (i) + 8), KVQ_R4(r, (i) + 12)
-#define KVQ_W4(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3])
-#define KVQ_W16(r, i) KVQ_W4(r, i), KVQ_W4(r, (i) + 4), KVQ_W4(r, (i) + 8), KVQ_W4(r, (i) + 12)
-
-// 16 rows x 32 columns (64 channels of the Keys of a group).
-__device__ __forceinline__ void tc_st_16x256_x4(uint32_t t, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16(r, 0),
-      "r"(t)
-      : "memory");
-}
-// 16 rows x 16 columns (16 channels of the Values of two groups).
-__device__ __forceinline__ void tc_st_16x128_x4(uint32_t t, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KVQ_R4(r, 0), KVQ_R4(r, 4),
-               "r"(t)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tc_ld(uint32_t (&r)[N], uint32_t t) {
-  static_assert(N == 16 || N == 32);
-  if constexpr (N == 32)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : KVQ_W16(r, 0), KVQ_W16(r, 16)
-        : "r"(t)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : KVQ_W16(r, 0)
-        : "r"(t)
-        : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tc_st(uint32_t t, const uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32);
-  if constexpr (N == 32)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_R16(r, 0),
-        KVQ_R16(r, 16), "r"(t)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16(r, 0),
-        "r"(t)
-        : "memory");
-}
-// Where a group lies: a stage of the ring (shared memory) or the window's
-// tiles (global memory).
-struct FromRing {
-  uint32_t at;
-  __device__ __forceinline__ FromRing operator+(int o) const { return FromRing{at + (uint32_t)o}; }
-  __device__ __forceinline__ uint32_t u32() const {
-    uint32_t x;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at));
-    return x;
-  }
-  __device__ __forceinline__ uint2 u64() const {
-    uint2 x;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at));
-    return x;
-  }
-  __device__ __forceinline__ uint4 u128() const {
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
-    return x;
-  }
-};
-struct FromGlobal {
-  const uint8_t* at;
-  __device__ __forceinline__ FromGlobal operator+(int o) const { return FromGlobal{at + o}; }
-  __device__ __forceinline__ uint2 u64() const { return *reinterpret_cast<const uint2*>(at); }
-  __device__ __forceinline__ uint4 u128() const { return *reinterpret_cast<const uint4*>(at); }
-};
-
-// --------------------------------------------------------------- widening
-
-__host__ __device__ constexpr uint32_t splat_h(uint32_t h) { return h | (h << 16); }
-// fp16 bits of 2^e (normal)
-__host__ __device__ constexpr uint32_t pow2_h(int e) { return (uint32_t)(15 + e) << 10; }
-__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// Codes at bits [E, E + BITS) of both half-words -> (c - 2^(BITS-1)) 2^(1-BITS),
-// exact: the code lands in the mantissa of 2^X (1 + c 2^(E-10)) with
-// X = 11 - E - BITS, i.e. 2^X + c 2^(1-BITS); 2^X + 1 comes off.
-template <int BITS, int E>
-__device__ __forceinline__ uint32_t code_val(uint32_t w) {
-  constexpr int X = 11 - E - BITS;
-  static_assert(X >= 0 && X <= 9, "the code lies in the mantissa");
-  constexpr uint32_t m = ((1u << BITS) - 1u) << E;
-  // -(2^X + 1) in fp16: mantissa bit 10 - X (X = 0: -2)
-  constexpr uint32_t off = X == 0 ? 0xc000u : (0x8000u | pow2_h(X) | (1u << (10 - X)));
-  return hadd2_u(lop_and_or(w, splat_h(m), splat_h(pow2_h(X))), splat_h(off));
-}
-// Two 16-bit codes -> fp16((c - 2^15) 2^-15), rounded once.
-__device__ __forceinline__ uint32_t code_val16(uint32_t w) {
-  const uint32_t hi = lop_and_or(w >> 8, 0x00ff00ffu, splat_h(pow2_h(3)));  // 8 + hi / 128
-  const uint32_t lo = lop_and_or(w, 0x00ff00ffu, splat_h(pow2_h(3)));       // 8 + lo / 128
-  // hi / 128 - 1 - 2^-5 is exact; (8 + lo / 128) 2^-8 adds 2^-5 + lo 2^-15
-  return hfma2_u(lo, splat_h(pow2_h(-8)), hadd2_u(hi, splat_h(0xc884u)));  // - 9.03125
-}
-// g = (1 - 2^-b) / 2, as fp16 and fp32 (16 bits: 1/2, off by 2^-16)
-template <int BITS>
-__host__ __device__ constexpr uint32_t value_scale_h() {
-  return BITS == 2 ? 0x3600u : BITS == 4 ? 0x3780u : BITS == 8 ? 0x37f8u : 0x3800u;
-}
-template <int BITS>
-__host__ __device__ constexpr float value_scale() {
-  return BITS == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << BITS);
-}
-__device__ __forceinline__ float value_scale_of(int bits) {
-  return bits == 16 ? 0.5f : 0.5f - 0.5f / (float)(1 << bits);
-}
-__device__ __forceinline__ uint32_t sat_h2(float lo, float hi) {
-  return pack_h2(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
-}
-
-// Quad position p (channels 16 p + 4 t .. + 3) of one token: the pairs (members
-// 0, 2) and (members 1, 3).  u: the words of the token's half of the lane unit
-// from quad position p0 on.
-template <int BITS>
-__device__ __forceinline__ void key_pairs(const uint32_t* u, int p, uint32_t& a, uint32_t& b) {
-  if constexpr (BITS == 16) {
-    a = code_val16(__byte_perm(u[2 * p], u[2 * p + 1], 0x5410));
-    b = code_val16(__byte_perm(u[2 * p], u[2 * p + 1], 0x7632));
-  } else {
-    constexpr int qpw = 8 / BITS;
-    const uint32_t w = u[p / qpw], w8 = w >> 8;
-    switch (p % qpw) {  // a constant after unrolling
-      case 0: a = code_val<BITS, 0>(w); b = code_val<BITS, 0>(w8); break;
-      case 1: if constexpr (qpw > 1) { a = code_val<BITS, BITS>(w); b = code_val<BITS, BITS>(w8); } break;
-      case 2: if constexpr (qpw > 2) { a = code_val<BITS, 2 * BITS>(w); b = code_val<BITS, 2 * BITS>(w8); } break;
-      default: if constexpr (qpw > 2) { a = code_val<BITS, 3 * BITS>(w); b = code_val<BITS, 3 * BITS>(w8); } break;
-    }
-  }
-}
-
-// Factors of a token's group from its (R, Z) word at the cache's width: R/4 and
-// Z g + R/4, for two tokens or twice for one.
-template <int BITS>
-__device__ __forceinline__ void group_factors(uint32_t m0, uint32_t m1, uint32_t& rc, uint32_t& zc) {
-  rc = hmul2_u(__byte_perm(m0, m1, 0x5410), splat_h(pow2_h(-2)));
-  zc = hfma2_u(__byte_perm(m0, m1, 0x7632), splat_h(value_scale_h<BITS>()), rc);
-}
-// The same for 16-bit codes in a cache of another width: R g / 2 is not exact
-// then, so the centre is formed in fp32.
-template <int BITS>
-__device__ __forceinline__ void window_factors(uint32_t m0, uint32_t m1, uint32_t& rc, uint32_t& zc) {
-  constexpr float g = value_scale<BITS>(), f = g * (32768.0f / 65535.0f);
-  const uint32_t r2 = __byte_perm(m0, m1, 0x5410), z2 = __byte_perm(m0, m1, 0x7632);
-  const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&r2));
-  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&z2));
-  rc = pack_h2(r.x * f, r.y * f);
-  zc = pack_h2(fmaf(r.x, f, z.x * g), fmaf(r.y, f, z.y * g));
-}
-
-// Keys of one group into 16 tensor-memory rows, 64 channels at a time.  part:
-// the group's Key part; rc, zc: factors of tokens g and g + 8; CHAN:
-// per-channel groups, their (R, Z) words at kmc (the cache's width).
-template <int BITS, bool CHAN, typename From>
-__device__ __forceinline__ void widen_keys(From part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], FromRing kmc,
-                                           uint32_t taddr, int lane) {
-  constexpr int kHalfWords = BITS / 2;  // words of 4 quad positions of one token
-  const From unit = part + lane * unit_bytes(BITS);
-#pragma unroll
-  for (int hf = 0; hf < 2; hf++) {
-    uint32_t u[2][kHalfWords], r[16];
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const From at = unit + 4 * (x * BITS + hf * kHalfWords);
-      if constexpr (kHalfWords == 1) {
-        u[x][0] = at.u32();
-      } else if constexpr (kHalfWords == 2) {
-        const uint2 w = at.u64();
-        u[x][0] = w.x; u[x][1] = w.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kHalfWords; i += 4) {
-          const uint4 w = (at + 4 * i).u128();
-          u[x][i] = w.x; u[x][i + 1] = w.y; u[x][i + 2] = w.z; u[x][i + 3] = w.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-      uint32_t ra[2], za[2];  // CHAN: of members (0, 2) and (1, 3)
-      if constexpr (CHAN) {
-        const uint4 w = (kmc + 4 * (16 * (4 * hf + p) + 4 * (lane & 3))).u128();
-        group_factors<BITS>(w.x, w.z, ra[0], za[0]);
-        group_factors<BITS>(w.y, w.w, ra[1], za[1]);
-      }
-#pragma unroll
-      for (int x = 0; x < 2; x++) {
-        uint32_t k0, k1;
-        key_pairs<BITS>(u[x], p, k0, k1);
-        r[4 * p + 2 * x] = hfma2_u(k0, CHAN ? ra[0] : rc[x], CHAN ? za[0] : zc[x]);
-        r[4 * p + 2 * x + 1] = hfma2_u(k1, CHAN ? ra[1] : rc[x], CHAN ? za[1] : zc[x]);
-      }
-    }
-    tc_st_16x256_x4(taddr + 32 * hf, r);
-  }
-}
-
-// Values of one group and this warp's 32 channels.  The warp takes the channels
-// of lane units g = 2 w and 2 w + 1 (h = 0, 1): tensor-memory row 16 h + 8 r +
-// g' holds channel 16 g' + 8 r + 2 w + h, so every unit is read by one warp only;
-// lane (g', t) turns pairs 2 g', 2 g' + 1 (r = 0, 1) of unit (2 w + h, t).
-// out[h][2 u + r]: rows g' + 8 r, column 4 u + t of the group's eight.
-// rc, zc: half2 of (R, Z) factors of tokens 2t, 2t + 1 (+ 8 u).
-template <int BITS, typename From>
-__device__ __forceinline__ void widen_values(From part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], int w, int lane,
-                                             uint32_t (&out)[2][4]) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const From unit = part + (4 * (2 * w + h) + t) * unit_bytes(BITS);
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      uint32_t v0, v1;
-      if constexpr (BITS == 16) {
-        const uint2 x = (unit + 4 * (u * 16 + 2 * g)).u64();
-        v0 = code_val16(x.x);
-        v1 = code_val16(x.y);
-      } else {
-        constexpr int ppw = 16 / BITS;  // pairs per word
-        const uint32_t x = (unit + 4 * (u * BITS + 2 * g / ppw)).u32() >> (2 * BITS * (g % (ppw / 2)));
-        v0 = code_val<BITS, 0>(x);
-        if constexpr (BITS == 8)
-          v1 = code_val<8, 0>(x >> 8);
-        else
-          v1 = code_val<BITS, BITS>(x);
-      }
-      out[h][2 * u] = hfma2_u(v0, rc[u], zc[u]);
-      out[h][2 * u + 1] = hfma2_u(v1, rc[u], zc[u]);
-    }
-  }
-}
-// Channel of tensor-memory row rho of V and O.
-__device__ __forceinline__ int channel_of(int rho) {
-  return 16 * (rho & 7) + 8 * ((rho >> 3) & 1) + 2 * (rho >> 5) + ((rho >> 4) & 1);
-}
-// ------------------------------------------------------------------ roles
-
-// Shared address of barrier i of an array in Small, from that of Small (sb).
-#define KVQ_BAR(array, i) (sb + (uint32_t)offsetof(Small, array) + 8u * (uint32_t)(i))
-
-// One CTA's walk over its share: segments (a stream's block of rows), tiles.
-struct Walk {
-  int u, end;               // units left
-  int s, block, t0, t1;     // current segment
-  __device__ __forceinline__ bool next(const TreePlan& p) {
-    if (u >= end) return false;
-    const int x = u / p.tiles;
-    t0 = u - x * p.tiles;
-    t1 = min(p.tiles, t0 + end - u);
-    s = x / p.blocks;
-    block = x - s * p.blocks;
-    u += t1 - t0;
-    return true;
-  }
-};
-
-// Whether token tl (0..127) of tile t exists.
-__device__ __forceinline__ bool token_valid(const TreePlan& p, int t, int tl) {
-  if (t < p.tp) {
-    const int v = t * kTileGroups + (tl >> 4);
-    return v < p.groups && (v != p.part_group || (tl & 15) < p.part_valid);
-  }
-  if (t < p.tp + p.tw) return (t - p.tp) * kTile + tl < p.a.c.n_win;
-  return (t - p.tp - p.tw) * kTile + tl < p.a.n;
-}
-
-// One buffer's ring: slots buf, buf + 2, ... of the stages, in turn.
-struct Slot {
-  int i;
-  uint32_t phase = 0;
-  __device__ __forceinline__ explicit Slot(int buf) : i(buf) {}
-  __device__ __forceinline__ void step(int stages) {
-    i += 2;
-    if (i >= stages) {
-      i &= 1;
-      phase ^= 1;
-    }
-  }
-};
-
-// Producer (one warp): packed progressive tiles into the ring, run by run (groups
-// that neighbour in one tile of the cache).
-__device__ __forceinline__ void produce(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk) {
-  const CacheView& c = p.a.c;
-  const Fill& f = p.f;
-  const int gb = group_bytes(c.bits);
-  const bool chan = c.kmc != nullptr;
-  Slot even(0), odd(1);
-  uint32_t ct = 0;
-  while (wk.next(p)) {
-    const uint32_t ct0 = ct;
-    ct += wk.t1 - wk.t0;
-    if (wk.t0 >= p.tp) continue;
-    const uint8_t* sbase = c.codes + (size_t)wk.s * c.nt * kTileBytes;
-    const uint32_t* mbase = c.meta + (size_t)wk.s * c.nt * c.pf * 2;
-    int tile = 0, grp = 0, groups = 0, e = 0;
-    if (!chan) {
-      const GroupLoc loc = locate_group(f, (long long)wk.t0 * kTileGroups);
-      tile = loc.tile;
-      grp = loc.grp;
-      groups = loc.tile_groups;
-    }
-    for (int t = wk.t0; t < min(wk.t1, p.tp); t++) {
-      const bool second = (ct0 + (uint32_t)(t - wk.t0)) & 1u;
-      const Slot sl = second ? odd : even;
-      tree_wait(KVQ_BAR(ring_free, sl.i), sl.phase ^ 1, p.a.err, &sm.abort);
-      if (sm.abort) goto out;
-      const uint32_t st = ring + (uint32_t)(sl.i * p.stage_bytes);
-      const uint32_t bar = KVQ_BAR(ring_full, sl.i);
-      const int n = min(kTileGroups, p.groups - t * kTileGroups);
-      if (elect_one()) {
-        mbar_expect_tx(bar, (uint32_t)n * (gb + 128u) + (chan ? 4u * kHeadDim : 0u));
-        if (chan)
-          bulk_g2s(st + kTileGroups * (gb + 128), c.kmc + ((size_t)wk.s * c.blocks_max + t) * kHeadDim, 4u * kHeadDim, bar);
-      }
-      __syncwarp();
-      for (int g = 0; g < n;) {
-        int run;
-        if (chan) {  // a block in the order of arrival: whole or partial runs of its epochs
-          const int i = t * kTile + g * kGroupTokens;
-          while (e + 1 < c.ep.n && i >= c.ep.start[e + 1]) e++;
-          const int m = i - c.ep.start[e], lg = c.ep.lg_ee[e], off = m & ((1 << lg) - 1);
-          tile = m >> lg;
-          grp = (c.ep.h[e] + off) >> 4;
-          run = min(n - g, ((1 << lg) - off) >> 4);
-        } else {
-          run = min(n - g, groups - grp);
-        }
-        if (elect_one()) {
-          bulk_g2s(st + g * gb, sbase + (size_t)tile * kTileBytes + (size_t)(grp * gb), (uint32_t)(run * gb), bar);
-          bulk_g2s(st + kTileGroups * gb + g * 128, mbase + ((size_t)tile * c.pf + (size_t)(grp * kGroupTokens)) * 2,
-                   (uint32_t)run * 128u, bar);
-        }
-        __syncwarp();
-        g += run;
-        if (!chan) {
-          grp += run;
-          if (grp == groups) {  // the next tile: full, the partial tile k, or half full
-            tile++;
-            grp = 0;
-            groups = tile < f.k ? f.gpt : tile == f.k ? f.gk : f.gh;
-          }
-        }
-      }
-      if (second)
-        odd.step(p.stages);
-      else
-        even.step(p.stages);
-    }
-  }
-out:
-  if (sm.abort) {  // copies in flight land before the CTA ends: of each slot the last use, if any
-    for (int i = 0; i < p.stages; i++) {
-      const Slot& r = i & 1 ? odd : even;
-      const uint32_t uses_phase = i < r.i ? r.phase : r.phase ^ 1;  // of the slot's last use; the phase before the first reads as done
-      drain_wait(KVQ_BAR(ring_full, i), uses_phase);
-    }
-  }
-}
-
-// Group gi (0..7) of window tile t; null if it does not exist.
-struct WindowGroup {
-  const uint8_t* code;
-  const uint32_t* meta;
-};
-__device__ __forceinline__ WindowGroup window_group(const TreePlan& p, int s, int t, int gi) {
-  const int wg = (t - p.tp) * kTileGroups + gi;
-  if (wg * kGroupTokens >= p.a.c.n_win) return WindowGroup{nullptr, nullptr};
-  constexpr int kPer = slots_per_tile(16) / kGroupTokens;
-  const size_t tile = (size_t)s * kWindowTiles + wg / kPer;
-  return WindowGroup{p.a.c.wcodes + tile * kTileBytes + (size_t)(wg % kPer) * group_bytes(16),
-                     p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
-}
-
-// Drafted Keys of a group, as k g / lambda.
-__device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, float scale, uint32_t taddr, int lane) {
-  const TreeArgs& a = p.a;
-  const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
-  for (int hf = 0; hf < 2; hf++) {
-    uint32_t r[16];
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const int j = j0 + g + 8 * x;
-      const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 64 * hf + 4 * t;
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < a.n) {
-          if (a.f32) {
-            k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at + 16 * q));
-          } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q));
-            k = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                            __uint_as_float(w.y & 0xffff0000u));
-          }
-        }
-        float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (a.c.lam_inv)
-          l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 64 * hf + 16 * q + 4 * t));
-        r[4 * q + 2 * x] = sat_h2(scale * k.x * l.x, scale * k.z * l.z);
-        r[4 * q + 2 * x + 1] = sat_h2(scale * k.y * l.y, scale * k.w * l.w);
-      }
-    }
-    tc_st_16x256_x4(taddr + 32 * hf, r);
-  }
-}
-// Drafted Values of a group for this warp's channels (widen_values' layout), times g.
-__device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, float scale, int w, int lane,
-                                             uint32_t (&out)[2][4]) {
-  const TreeArgs& a = p.a;
-  const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int u = 0; u < 2; u++) {
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-      float2 v[2];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const int j = j0 + 8 * u + 2 * t + e;
-        const long long at = b * a.v_b + j * a.v_t + h * a.v_h + 16 * g + 8 * r + 2 * w;
-        v[e] = make_float2(0.f, 0.f);
-        if (j < a.n) {
-          if (a.f32) {
-            v[e] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.v) + at));
-          } else {
-            const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.v) + at));
-            v[e] = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-          }
-        }
-      }
-      out[0][2 * u + r] = sat_h2(scale * v[0].x, scale * v[1].x);
-      out[1][2 * u + r] = sat_h2(scale * v[0].y, scale * v[1].y);
-    }
-  }
-}
-
-// Values of a packed tile in the ring.  CHECK: some of its tokens do not exist
-// (n groups do; group part only its first valid tokens): they become zeros, as
-// P is zero there and stale codes with a stale range may be anything.
-template <int BITS, bool CHECK, int GROUPS>
-__device__ __forceinline__ void value_tile(FromRing st, uint32_t ta, int g0, int n, int part, int valid, int w, int lane) {
-  constexpr int gb = group_bytes(BITS);
-  const int t = lane & 3;
-#pragma unroll 2
-  for (int g2 = g0; g2 < g0 + GROUPS; g2 += 2) {
-    uint32_t o0[8], o1[8];  // rows 0-15 and 16-31, columns 8 g2 .. 8 g2 + 15
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int gi = g2 + i;
-      uint32_t rc[2], zc[2], out[2][4];
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        uint4 m = (st + (kTileGroups * gb + gi * 128 + 8 * (8 * u + 2 * t))).u128();  // K, V of tokens 2t, 2t + 1 (+ 8u)
-        if constexpr (CHECK) {
-          const int first = 8 * u + 2 * t, have = gi >= n ? 0 : gi == part ? valid : kGroupTokens;
-          if (first >= have) m.y = 0u;
-          if (first + 1 >= have) m.w = 0u;
-        }
-        group_factors<BITS>(m.y, m.w, rc[u], zc[u]);
-      }
-      widen_values<BITS>(st + (gi * gb + part_bytes(BITS)), rc, zc, w, lane, out);
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        o0[4 * i + e] = out[0][e];
-        o1[4 * i + e] = out[1][e];
-      }
-    }
-    tc_st_16x128_x4(ta + 8 * g2, o0);
-    tc_st_16x128_x4(ta + 8 * g2 + (16u << 16), o1);
-  }
-}
-
-// Which rows see drafted tokens 32 w .. + 31 of tile t: one word per row.
-__device__ __forceinline__ void draft_seen(const TreePlan& p, uint32_t (*seen)[4], int s, int block, int t, int w, int lane) {
-  const TreeArgs& a = p.a;
-  const int b = s / a.c.kv_heads, j = (t - p.tp - p.tw) * kTile + 32 * w + lane;
-  const int r0 = block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
-  const unsigned char* m = a.mask ? a.mask + b * a.mask_b + j : nullptr;
-  constexpr int kBatch = 8;  // mask bytes in flight
-  for (int n0 = r0 / a.group; n0 * a.group < r1; n0 += kBatch) {
-    bool see[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; i++) {
-      const int node = n0 + i;
-      see[i] = j < a.n && node < a.n;
-      if (see[i]) see[i] = m ? m[(long long)node * a.n] != 0 : j <= node;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; i++) {
-      const uint32_t word = __ballot_sync(0xffffffffu, see[i]);
-      const int row = (n0 + i) * a.group + lane - r0;
-      if (lane < a.group && row >= 0 && row < r1 - r0) seen[row][w] = word;
-    }
-  }
-}
-
-// Widening: Keys, then Values of buffer buf's tiles (every second one), and for
-// drafted tiles which rows see them.  Warp w of a group writes tensor-memory rows
-// 32 w .. + 31: Keys of tokens 32 w .. + 31, Values of the channels of lane units
-// 2 w and 2 w + 1; of two groups that share a tile each takes one of the two Key
-// groups and half of the Value groups (part).
-template <int BITS, int COLS>
-__device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int buf, int part,
-                                           int w, int lane) {
-  using S = Split<COLS>;
-  constexpr int kKeys = 2 / S::kShare, kValues = kTileGroups / S::kShare;
-  const int i0 = part * kKeys, v0 = part * kValues;
-  const CacheView& c = p.a.c;
-  constexpr int gb = group_bytes(BITS);
-  const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t tk = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColK + 64 * buf;
-  const uint32_t tv = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColV + 64 * buf;
-  uint32_t phase = 1;  // of k_free and v_free
-  uint32_t ct = 0;
-  Slot sl(buf);
-  while (wk.next(p)) {
-    for (int t = wk.t0; t < wk.t1; t++, ct++) {
-      if ((ct & 1) == (uint32_t)buf) {
-        const bool packed = t < p.tp;
-        const FromRing st{ring + (uint32_t)(sl.i * p.stage_bytes)};
-        if (packed) tree_wait(KVQ_BAR(ring_full, sl.i), sl.phase, p.a.err, &sm.abort);
-        tree_wait(KVQ_BAR(k_free, buf), phase, p.a.err, &sm.abort);
-        tc_after();
-        // ---- Keys ----
-        if (packed) {
-          // groups that do not exist are read as whatever the stage holds: those rows of S are not used
-#pragma unroll 1
-          for (int i = i0; i < i0 + kKeys; i++) {
-            const uint32_t ti = tk + ((uint32_t)(16 * i) << 16);
-            const FromRing codes = st + (2 * w + i) * gb;
-            uint32_t rc[2] = {0u, 0u}, zc[2] = {0u, 0u};
-            if (c.kmc) {
-              widen_keys<BITS, true>(codes, rc, zc, st + kTileGroups * (gb + 128), ti, lane);
-            } else {
-              const FromRing meta = st + (kTileGroups * gb + (2 * w + i) * 128 + 8 * g);
-              const uint32_t m0 = meta.u32(), m1 = (meta + 64).u32();
-              group_factors<BITS>(m0, m0, rc[0], zc[0]);
-              group_factors<BITS>(m1, m1, rc[1], zc[1]);
-              widen_keys<BITS, false>(codes, rc, zc, st, ti, lane);
-            }
-          }
-        } else if (t < p.tp + p.tw) {
-#pragma unroll 1
-          for (int i = i0; i < i0 + kKeys; i++) {
-            const WindowGroup wg = window_group(p, wk.s, t, 2 * w + i);
-            if (wg.code) {
-              uint32_t rc[2], zc[2];
-              const uint32_t m0 = wg.meta[2 * g], m1 = wg.meta[2 * g + 16];
-              window_factors<BITS>(m0, m0, rc[0], zc[0]);
-              window_factors<BITS>(m1, m1, rc[1], zc[1]);
-              widen_keys<16, false>(FromGlobal{wg.code}, rc, zc, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
-            }
-          }
-        } else {
-          const int j0 = (t - p.tp - p.tw) * kTile + 32 * w;
-#pragma unroll 1
-          for (int i = i0; i < i0 + kKeys; i++)
-            if (j0 + 16 * i < p.a.n)
-              draft_keys(p, wk.s, j0 + 16 * i, value_scale<BITS>(), tk + ((uint32_t)(16 * i) << 16), lane);
-          if (part == 0) draft_seen(p, sm.seen[ct & 3], wk.s, wk.block, t, w, lane);
-        }
-        tc_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(KVQ_BAR(k_full, buf));
-        // ---- Values ----
-        tree_wait(KVQ_BAR(v_free, buf), phase, p.a.err, &sm.abort);
-        tc_after();
-        if (packed) {
-          const int n = min(kTileGroups, p.groups - t * kTileGroups);
-          const int pg = p.part_group - t * kTileGroups;
-          if (n == kTileGroups && (unsigned)pg >= (unsigned)kTileGroups)
-            value_tile<BITS, false, kValues>(st, tv, v0, n, pg, p.part_valid, w, lane);
-          else
-            value_tile<BITS, true, kValues>(st, tv, v0, n, pg, p.part_valid, w, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(KVQ_BAR(ring_free, sl.i));
-        } else {
-#pragma unroll 1
-          for (int g2 = v0; g2 < v0 + kValues; g2 += 2) {
-            uint32_t o0[8], o1[8];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-              uint32_t out[2][4] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-              if (t < p.tp + p.tw) {
-                const WindowGroup wg = window_group(p, wk.s, t, g2 + i);
-                if (wg.code) {
-                  uint32_t rc[2], zc[2];
-#pragma unroll
-                  for (int u = 0; u < 2; u++) {
-                    const uint4 m = *reinterpret_cast<const uint4*>(wg.meta + 2 * (8 * u + 2 * t4));
-                    const bool ok0 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4);
-                    const bool ok1 = token_valid(p, t, 16 * (g2 + i) + 8 * u + 2 * t4 + 1);
-                    window_factors<BITS>(ok0 ? m.y : 0u, ok1 ? m.w : 0u, rc[u], zc[u]);
-                  }
-                  widen_values<16>(FromGlobal{wg.code + part_bytes(16)}, rc, zc, w, lane, out);
-                }
-              } else {
-                const int j0 = (t - p.tp - p.tw) * kTile + 16 * (g2 + i);
-                if (j0 < p.a.n) draft_values(p, wk.s, j0, value_scale<BITS>(), w, lane, out);
-              }
-#pragma unroll
-              for (int e = 0; e < 4; e++) {
-                o0[4 * i + e] = out[0][e];
-                o1[4 * i + e] = out[1][e];
-              }
-            }
-            tc_st_16x128_x4(tv + 8 * g2, o0);
-            tc_st_16x128_x4(tv + 8 * g2 + (16u << 16), o1);
-          }
-        }
-        tc_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(KVQ_BAR(v_full, buf));
-        phase ^= 1;
-        if (packed) sl.step(p.stages);
-      }
-    }
-  }
-}
-
-// One warp per half: the MMAs of the half's tiles.  at: shared address of the CTA's data.
-template <int COLS, bool DUAL>
-__device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t at, Walk wk, int half) {
-  using S = Split<COLS>;
-  constexpr uint32_t kDescQk = mma_desc(COLS, false), kDescPv = mma_desc(COLS, true);
-  const uint32_t ts = sm.tmem + S::kColS + S::kStep * half, to = sm.tmem + S::kColO + S::kStep * half;
-  const uint32_t tk = sm.tmem + S::kColK, tv = sm.tmem + S::kColV;
-  const uint64_t q_desc = smem_desc(at + half * kQBytes), p_desc = smem_desc(at + 2 * kQBytes + half * kPBytes);
-  const uint64_t ones_desc = narrow_desc(at + 2 * kQBytes + 2 * kPBytes);
-  const uint64_t neg_desc = narrow_desc(at + 2 * kQBytes + 2 * kPBytes + kOnesBytes + half * kNegBytes);
-  uint32_t ct = 0, n = 0, seg = 0;  // tiles of the CTA, tiles of this half, segments with tiles of this half
-  auto pv = [&](uint32_t tile, uint32_t i, bool first) {
-    const int buf = tile & 1;
-    tree_wait(KVQ_BAR(v_full, buf), (tile >> 1) & 1, p.a.err, &sm.abort);
-    tree_wait(KVQ_BAR(p_full, half), i & 1, p.a.err, &sm.abort);
-    tc_after();
-    if (elect_one()) {
-#pragma unroll
-      for (int k = 0; k < 8; k++)
-        tc_mma(to, tv + 64 * buf + 8 * k, p_desc + (2048 >> 4) * k, kDescPv, !(first && k == 0));
-      tc_commit(KVQ_BAR(v_free, buf));
-      tc_commit(KVQ_BAR(pv_done, half));
-    }
-    __syncwarp();
-  };
-  while (wk.next(p)) {
-    bool any = false, prev_first = false;
-    uint32_t prev = 0;
-    for (int t = wk.t0; t < wk.t1; t++, ct++) {
-      const int buf = ct & 1;
-      if (!DUAL && buf != half) continue;
-      if (!any) tree_wait(KVQ_BAR(q_full, half), seg & 1, p.a.err, &sm.abort);
-      tree_wait(KVQ_BAR(k_full, buf), (ct >> 1) & 1, p.a.err, &sm.abort);
-      tree_wait(KVQ_BAR(s_free, half), (n & 1) ^ 1, p.a.err, &sm.abort);
-      tc_after();
-      if (elect_one()) {
-        tc_mma_ss(ts, ones_desc, neg_desc, kDescQk, false);  // - m
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-          tc_mma(ts, tk + 64 * buf + 8 * k, q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, true);
-        tc_commit(KVQ_BAR(k_free, buf));
-        tc_commit(KVQ_BAR(s_full, half));
-      }
-      __syncwarp();
-      if (any) pv(prev, n - 1, prev_first);
-      prev = ct;
-      prev_first = !any;
-      any = true;
-      n++;
-    }
-    if (any) {
-      pv(prev, n - 1, prev_first);
-      seg++;
-    }
-  }
-  if (elect_one()) tc_commit(KVQ_BAR(drain, half));
-  __syncwarp();
-  drain_wait(KVQ_BAR(drain, half), 0);
-}
-
-// Sum or maximum over the warp's lanes of N values a lane: every exchange halves
-// the values a lane carries.  N >= 32: lane L ends with values 0 .. N/32 - 1 of
-// columns L N/32 ...; N = 16: with column L / 2.
-template <int N, bool MAX>
-__device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
-  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
-#pragma unroll
-  for (int o = 16, len = N; o; o >>= 1) {
-    if (len > 1) {
-      len /= 2;
-#pragma unroll
-      for (int i = 0; i < N / 2; i++) {
-        if (i < len) {
-          const float keep = (lane & o) ? v[i + len] : v[i], send = (lane & o) ? v[i] : v[i + len];
-          v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-      }
-    } else {
-      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    }
-  }
-}
-
-// A warpgroup: softmax of C of the half's columns (from column cb on) in the
-// half's tiles, and the segment's results for them.
-template <int COLS, bool DUAL>
-__device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint32_t sb, uint8_t* base, Walk wk, int wg, int tl) {
-  using S = Split<COLS>;
-  constexpr int C = S::kCols;
-  static_assert(C == 16 || C == 32);
-  constexpr int kSoftThreads = 32 * S::kSoft;
-  const TreeArgs& a = p.a;
-  const int half = wg / S::kSubs, cb = (wg % S::kSubs) * C;
-  const int w = tl >> 5, lane = tl & 31;
-  const uint32_t lanes = (uint32_t)(32 * w) << 16;
-  const uint32_t ts = sm.tmem + S::kColS + S::kStep * half + cb + lanes, to = sm.tmem + S::kColO + S::kStep * half + cb + lanes;
-  uint8_t* q_smem = base + half * kQBytes;
-  uint8_t* p_all = base + 2 * kQBytes;
-  uint8_t* p_smem = p_all + half * kPBytes;
-  uint8_t* neg_smem = p_all + 2 * kPBytes + kOnesBytes + half * kNegBytes;
-  const int id = 1 + wg;  // barriers 1 .. 4: one warpgroup; 5: every softmax thread; 6, 7: one half
-  uint32_t ct = 0, n = 0;
-  const float out_scale = 1.0f / value_scale_of(a.c.bits), q_scale = a.qscale * out_scale;
-  while (wk.next(p)) {
-    const int b = wk.s / a.c.kv_heads, j = wk.s - b * a.c.kv_heads;
-    const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0) + cb;  // first row of these columns
-    const int nr = min(C, min(p.rows, (wk.block + 1) * p.block_rows) - r0);       // rows that exist (may be <= 0)
-    // tiles of this half in the segment
-    const int mine = DUAL ? wk.t1 - wk.t0 : (wk.t1 - wk.t0 + ((ct & 1) == (uint32_t)half ? 1 : 0)) >> 1;
-    float2 l2[C / 2];
-#pragma unroll
-    for (int i = 0; i < C / 2; i++) l2[i] = make_float2(0.f, 0.f);
-    if (mine > 0) {
-      // ---- q' = q lambda sm_scale log2(e) / g as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
-      const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
-                                 : make_float4(1.f, 1.f, 1.f, 1.f);
-      uint2 raw[C / 4];
-#pragma unroll
-      for (int i = 0; i < C / 4; i++) {
-        const int r = w + 4 * i;
-        raw[i] = make_uint2(0u, 0u);
-        if (r < nr) {
-          const int row = r0 + r, node = row / a.group, g = row - node * a.group;
-          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t +
-                                                   (long long)(j * a.group + g) * a.q_h + 4 * lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < C / 4; i++) {
-        const int rs = cb + w + 4 * i;  // row of the half's Q
-        const float x0 = __uint_as_float(raw[i].x << 16) * q_scale * lam.x;
-        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * q_scale * lam.y;
-        const float x2 = __uint_as_float(raw[i].y << 16) * q_scale * lam.z;
-        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * q_scale * lam.w;
-        const int chunk = (lane & 15) >> 1;
-        *reinterpret_cast<uint2*>(q_smem + (lane >> 4) * (kQBytes / 2) + rs * 128 + ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) =
-            make_uint2(sat_h2(x0, x2), sat_h2(x1, x3));
-      }
-      if (tl < C) {  // no maximum yet
-        sm.neg[half][cb + tl] = kUnset;
-        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl)) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl) + 128) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(q_full, half));
-    }
-    int done = 0;
-    for (int t = wk.t0; t < wk.t1; t++, ct++) {
-      if (!DUAL && (ct & 1) != (uint32_t)half) continue;
-      // which columns' rows do not see this thread's token
-      uint32_t hide = 0u;
-      if (t >= p.tp || t * kTileGroups + kTileGroups > p.groups || (unsigned)(p.part_group - t * kTileGroups) < (unsigned)kTileGroups)
-        hide = token_valid(p, t, tl) ? 0u : 0xffffffffu;
-      tree_wait(KVQ_BAR(s_full, half), n & 1, a.err, &sm.abort);
-      tc_after();
-      if (t >= p.tp + p.tw && hide == 0u) {
-        const uint32_t(*seen)[4] = sm.seen[ct & 3] + (DUAL ? half * kHalfRows : 0) + cb;
-#pragma unroll
-        for (int i = 0; i < C; i++) hide |= (seen[i][w] >> lane & 1u) ? 0u : 1u << i;
-      }
-      uint32_t xb[C];  // scores less the running maxima, as bits
-      tc_ld(xb, ts);
-      if (hide) {
-#pragma unroll
-        for (int i = 0; i < C; i++)
-          if (hide >> i & 1u) xb[i] = 0xff800000u;  // - infinity
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < C; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(xb[i]), __uint_as_float(xb[i + 1])));
-      // A segment's first tile has no maxima: its scores come out as they are.  So
-      // do those of a row that has seen nothing yet, which only drafted tiles leave.
-      if (bar_or(id, 128, done == 0 || t >= p.tp + p.tw || fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
-        {
-          float v[C];
-#pragma unroll
-          for (int i = 0; i < C; i++) v[i] = __uint_as_float(xb[i]);
-          warp_columns<C, true>(v, lane);
-          sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
-        }
-        bar_sync(id, 128);
-        if (tl < C) {
-          const int c = cb + tl;
-          const float old = sm.neg[half][c];
-          const float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
-          float shift = 0.f, f = 1.f;
-          if (old == kUnset ? m > -INFINITY : m > 0.f) {  // a row that has seen nothing stays unset
-            const float base_neg = old == kUnset ? 0.f : old;
-            const float want = (base_neg - m) * (1.0f / kNegScale);
-            const float hi = __half2float(__float2half_rn(want)), lo = __half2float(__float2half_rn(want - hi));
-            const float neg = (hi + lo) * kNegScale;  // what the MMA will add
-            shift = neg - base_neg;
-            f = old == kUnset ? 0.f : ex2(shift);
-            sm.neg[half][c] = neg;
-            *reinterpret_cast<uint32_t*>(neg_smem + narrow_at(c)) = pack_h2(hi, lo);
-            fence_async_smem();
-          }
-          sm.alpha[half][c] = f;
-          sm.shift[half][c] = shift;
-        }
-        bar_sync(id, 128);
-        if (done > 0) {  // O so far, once the last product is in
-          const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
-          tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);
-          tc_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            uint32_t o[16];
-            tc_ld(o, to + c0);
-#pragma unroll
-            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.alpha[half][cb + c0 + i]);
-            tc_st(to + c0, o);
-          }
-#pragma unroll
-          for (int i = 0; i < C / 2; i++) l2[i] = mul2(l2[i], al[i]);
-          tc_wait_st();
-        }
-#pragma unroll
-        for (int i = 0; i < C; i++) xb[i] = __float_as_uint(__uint_as_float(xb[i]) + sm.shift[half][cb + i]);
-      }
-      tc_before();  // S is in registers: the next tile's product may start
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(s_free, half));
-      if (done > 0) tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);  // P is free again
-#pragma unroll
-      for (int q = 0; q < C / 8; q++) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int i = 4 * q + e;
-          const float2 pr = make_float2(ex2(__uint_as_float(xb[2 * i])), ex2(__uint_as_float(xb[2 * i + 1])));
-          l2[i] = add2(l2[i], pr);
-          h[e] = pack_h2(pr.x, pr.y);
-        }
-        *reinterpret_cast<uint4*>(p_smem + tl * 128 + (((cb / 8 + q) ^ (tl & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      fence_async_smem();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(p_full, half));
-      n++;
-      done++;
-    }
-    // ---- the segment's results ----
-    {
-      float v[C];
-#pragma unroll
-      for (int i = 0; i < C / 2; i++) { v[2 * i] = l2[i].x; v[2 * i + 1] = l2[i].y; }
-      warp_columns<C, false>(v, lane);
-      sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
-    }
-    bar_sync(id, 128);
-    if (tl < C) {
-      const float* r = &sm.red[half][0][cb + tl];
-      const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
-      const float neg = mine > 0 ? sm.neg[half][cb + tl] : kUnset;
-      sm.ml[half][cb + tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
-    }
-    if (mine > 0) {
-      tree_wait(KVQ_BAR(pv_done, half), (n - 1) & 1, a.err, &sm.abort);
-      tc_after();
-    }
-    const bool whole = wk.t0 == 0 && wk.t1 == p.tiles;
-    // this CTA's records: 0 for the segment its share begins in, else 1
-    const int xi = wk.s * p.blocks + wk.block, begin = cta_begin(p.units, p.grid, blockIdx.x);
-    float* rec = p.parts + ((size_t)blockIdx.x * 2 + (xi * p.tiles + wk.t0 == begin ? 0 : 1)) * p.rec;
-    const int rr = (DUAL ? half * kHalfRows : 0) + cb;  // first row within the block
-    // C rows of bf16 leave from shared memory, 16 bytes a thread
-    auto flush = [&](const uint8_t* sh) {
-      for (int i = tl; i < C * 16; i += 128) {
-        const int r = i >> 4, q = i & 15;
-        if (r < nr) {
-          const int row = r0 + r, node = row / a.group, g = row - node * a.group;
-          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                   (((long long)b * a.n + node) * a.q_heads + j * a.group + g) * kHeadDim)[q] =
-              *reinterpret_cast<const uint4*>(sh + r * 256 + 16 * q);
-        }
-      }
-    };
-    const int ch = channel_of(tl);
-    if constexpr (DUAL) {
-      bar_sync(id, 128);  // ml
-      uint32_t o[C];
-      tc_ld(o, to);
-      tc_before();
-      if (whole) {
-        uint8_t* sh = p_smem + (wg % S::kSubs) * (C * 256);
-#pragma unroll
-        for (int i = 0; i < C; i++) {
-          const float l = sm.ml[half][cb + i].y;
-          reinterpret_cast<__nv_bfloat16*>(sh)[i * kHeadDim + ch] =
-              __float2bfloat16_rn(l != 0.f ? __uint_as_float(o[i]) * out_scale / l : 0.f);
-        }
-        bar_sync(id, 128);
-        flush(sh);
-        bar_sync(6 + half, kSoftThreads / 2);  // P is written again
-      } else {
-#pragma unroll
-        for (int i = 0; i < C; i++)
-          if (i < nr) rec[2 * p.block_rows + (rr + i) * kHeadDim + tl] = __uint_as_float(o[i]);
-        if (tl < nr) {
-          rec[rr + tl] = sm.ml[half][cb + tl].x;
-          rec[p.block_rows + rr + tl] = sm.ml[half][cb + tl].y;
-        }
-      }
-    } else {
-      // join the halves: half 1 hands its O over in shared memory (both P areas: [COLS][128] fp32)
-      bar_sync(5, kSoftThreads);  // ml of both; every product of both halves is in
-      float* other_o = reinterpret_cast<float*>(p_all) + cb * kTile;
-      if (half == 1 && mine > 0) {
-        uint32_t o[C];
-        tc_ld(o, to);
-#pragma unroll
-        for (int i = 0; i < C; i++) other_o[i * kTile + tl] = __uint_as_float(o[i]);
-      }
-      tc_before();
-      bar_sync(5, kSoftThreads);
-      if (half == 0) {
-        const int other = wk.t1 - wk.t0 - mine;
-        uint32_t o[C];
-        if (mine > 0) {
-          tc_ld(o, to);
-          tc_before();
-        }
-#pragma unroll
-        for (int i = 0; i < C; i++) {
-          const float2 m0 = sm.ml[0][cb + i], m1 = sm.ml[1][cb + i];
-          const float m = fmaxf(m0.x, m1.x);
-          const float f0 = m0.y != 0.f ? ex2(m0.x - m) : 0.f, f1 = m1.y != 0.f ? ex2(m1.x - m) : 0.f;
-          float v = mine > 0 ? __uint_as_float(o[i]) * f0 : 0.f;
-          if (other > 0) v = fmaf(other_o[i * kTile + tl], f1, v);
-          const float l = m0.y * f0 + m1.y * f1;
-          if (whole) {
-            o[i] = __float_as_uint(l != 0.f ? v * out_scale / l : 0.f);
-          } else if (i < nr) {
-            rec[2 * p.block_rows + (rr + i) * kHeadDim + tl] = v;
-            if (tl == i) {
-              rec[rr + i] = m;
-              rec[p.block_rows + rr + i] = l;
-            }
-          }
-        }
-        if (whole) {
-          bar_sync(id, 128);  // other_o is read
-          uint8_t* sh = reinterpret_cast<uint8_t*>(other_o);
-#pragma unroll
-          for (int i = 0; i < C; i++)
-            reinterpret_cast<__nv_bfloat16*>(sh)[i * kHeadDim + ch] = __float2bfloat16_rn(__uint_as_float(o[i]));
-          bar_sync(id, 128);
-          flush(sh);
-        }
-      }
-      bar_sync(5, kSoftThreads);  // P and ml are written again
-    }
-  }
-}
-
-template <int REGS>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-
-template <int COLS, bool DUAL>
-__global__ void __launch_bounds__(Split<COLS>::kThreads, 1) tree_kernel(const __grid_constant__ TreePlan p) {
-  using S = Split<COLS>;
-  constexpr int kWiden0 = S::kSoft, kCtl0 = kWiden0 + S::kWiden;
-  extern __shared__ uint8_t raw[];
-  const uint32_t raw_at = smem_u32(raw), smem_at = (raw_at + 1023u) & ~1023u;
-  const uint32_t sb = smem_at + kSmallAt, ring_at = smem_at + kFixedBytes;
-  uint8_t* base = raw + (smem_at - raw_at);
-  Small& sm = *reinterpret_cast<Small*>(base + kSmallAt);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == kCtl0 + 3) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  if (threadIdx.x == 0) {
-    sm.abort = 0;
-    for (int i = 0; i < kMaxStages; i++) {
-      mbar_init(KVQ_BAR(ring_full, i), 1);
-      mbar_init(KVQ_BAR(ring_free, i), 4 * S::kShare);
-    }
-    for (int i = 0; i < 2; i++) {
-      mbar_init(KVQ_BAR(k_full, i), 4 * S::kShare);
-      mbar_init(KVQ_BAR(k_free, i), DUAL ? 2 : 1);
-      mbar_init(KVQ_BAR(v_full, i), 4 * S::kShare);
-      mbar_init(KVQ_BAR(v_free, i), DUAL ? 2 : 1);
-      mbar_init(KVQ_BAR(q_full, i), S::kSoft / 2);
-      mbar_init(KVQ_BAR(s_full, i), 1);
-      mbar_init(KVQ_BAR(s_free, i), S::kSoft / 2);
-      mbar_init(KVQ_BAR(p_full, i), S::kSoft / 2);
-      mbar_init(KVQ_BAR(pv_done, i), 1);
-      mbar_init(KVQ_BAR(drain, i), 1);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (threadIdx.x < kTile) {  // the constant operand of the extra k-step
-    uint8_t* ones = base + 2 * kQBytes + 2 * kPBytes + narrow_at(threadIdx.x);
-    *reinterpret_cast<uint4*>(ones) = make_uint4(splat_h(pow2_h(8)), 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(ones + 128) = make_uint4(0u, 0u, 0u, 0u);
-    fence_async_smem();
-  }
-  tc_before();
-  __syncthreads();
-  tc_after();
-  pdl_wait();  // the cache, q, k, v and the mask may be written by earlier kernels
-  const Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
-  if (warp < kWiden0) {
-    regs_up<S::kSoftRegs>();
-    softmax_role<COLS, DUAL>(p, sm, sb, base, wk, warp >> 2, threadIdx.x & 127);
-  } else if (warp < kCtl0) {
-    if constexpr (S::kWidenRegs > S::kRegs) regs_up<S::kWidenRegs>();
-    if constexpr (S::kWidenRegs < S::kRegs) regs_down<S::kWidenRegs>();
-    const int group = (warp - kWiden0) >> 2, buf = group & 1, part = group >> 1, w = warp & 3;
-    switch (p.a.c.bits) {
-      case 2: widen_role<2, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
-      case 4: widen_role<4, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
-      case 8: widen_role<8, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
-      default: widen_role<16, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane); break;
-    }
-  } else {
-    regs_down<S::kCtlRegs>();
-    if (warp == kCtl0)
-      produce(p, sm, sb, ring_at, wk);
-    else if (warp < kCtl0 + 3)
-      mma_role<COLS, DUAL>(p, sm, sb, smem_at, wk, warp - kCtl0 - 1);
-    __syncwarp();
-  }
-  tc_before();
-  __syncthreads();
-  pdl_launch_dependents();
-  tc_after();
-  if (warp == kCtl0 + 3) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
-}
 
 // Joins the partial records of one block of rows: a CTA per (stream, block of
 // rows, 4 rows), a thread per tensor-memory row (channel).  Every record's max
@@ -1379,22 +81,6 @@ __global__ void __launch_bounds__(kHeadDim) tree_merge_kernel(const __grid_const
 }
 static_assert(kMergeRows * 32 == kHeadDim, "a warp per row");
 
-template <int COLS, bool DUAL>
-cudaError_t launch_cols(const TreePlan& p, cudaStream_t s) {
-  const size_t smem = kFixedBytes + (size_t)p.stages * p.stage_bytes + 1024;
-  // once per device: the attribute is the kernel's on that device
-  static std::atomic<unsigned long long> set{0};
-  int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev)) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (dev > 63 || !(set.load(std::memory_order_relaxed) & bit)) {
-    if (cudaError_t e = cudaFuncSetAttribute(tree_kernel<COLS, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024))
-      return e;
-    set.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return launch_pdl(tree_kernel<COLS, DUAL>, dim3(p.grid), dim3(Split<COLS>::kThreads), smem, s, p);
-}
-
 }  // namespace
 
 size_t tree_workspace(int num_sms, int rows) {
@@ -1425,18 +111,15 @@ cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
   if (units > 0x7fffffffLL || a.num_sms < 1) return cudaErrorInvalidValue;
   p.units = (int)units;
   p.grid = (int)std::min<long long>(units, std::min(a.num_sms, kMergeRecords));
-  p.stage_bytes = kTileGroups * (group_bytes(a.c.bits) + 128) + 4 * kHeadDim;
-  p.stages = (kSmemMax - kFixedBytes) / p.stage_bytes;
-  p.stages = std::min(p.stages, kMaxStages) & ~1;  // one ring per buffer
-  if (p.stages < 2) return cudaErrorInvalidValue;
   p.rec = p.block_rows * (2 + kHeadDim);
   p.parts = static_cast<float*>(a.ws);
   cudaError_t e;
-  switch (p.block_rows) {
-    case 16: e = launch_cols<16, false>(p, s); break;
-    case 32: e = launch_cols<32, false>(p, s); break;
-    case 64: e = launch_cols<64, false>(p, s); break;
-    default: e = launch_cols<64, true>(p, s); break;
+  switch (a.c.bits) {
+    case 2: e = launch_tree_bits<2>(p, s); break;
+    case 4: e = launch_tree_bits<4>(p, s); break;
+    case 8: e = launch_tree_bits<8>(p, s); break;
+    case 16: e = launch_tree_bits<16>(p, s); break;
+    default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || p.units % p.grid == 0 && (p.units / p.grid) % p.tiles == 0) return e;  // every share whole blocks of rows
   return launch_pdl(tree_merge_kernel, dim3((unsigned)(p.units / p.tiles), (unsigned)((p.block_rows + kMergeRows - 1) / kMergeRows)),

@@ -323,8 +323,16 @@ struct AppendOne {
   int dtype = 0;
 };
 
+// The output of a tree of few rows (kvq_tree_attn), with ticket counters of the call's own.
+struct TreeOut {
+  void* out = nullptr;
+  int nodes = 0, heads = 0, group = 0;
+  int* counters = nullptr;
+};
+
 cudaError_t enqueue_decode(kvq_cache* c, int layer, const DecodePlan& d, const void* q, int q_heads, float sm_scale,
-                           float* out, float* parts, cudaStream_t s, const AppendOne& app = AppendOne()) {
+                           float* out, float* parts, cudaStream_t s, const AppendOne& app = AppendOne(),
+                           const TreeOut& tree = TreeOut()) {
   const LayerState& L = c->L[layer];
   DecodeArgs a{};
   a.app_group = -1;
@@ -340,6 +348,13 @@ cudaError_t enqueue_decode(kvq_cache* c, int layer, const DecodePlan& d, const v
   a.group = q_heads / c->kv_heads;
   a.qscale = sm_scale * 1.4426950408889634f;
   a.nparts = d.nparts;
+  if (tree.out) {
+    a.tree_out = tree.out;
+    a.tree_nodes = tree.nodes;
+    a.tree_heads = tree.heads;
+    a.tree_group = tree.group;
+    a.counters = tree.counters;
+  }
   // The progressive cache first; the window launch follows it.  The first
   // launch triggers its dependents only after its own dependency wait, so
   // the window launch needs none: it runs in the shadow of the first one's
@@ -1004,7 +1019,10 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
 size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_nodes) {
   if (!c || layer < 0 || layer >= c->layers || q_heads <= 0 || q_heads % c->kv_heads || q_heads / c->kv_heads > 8) return 0;
   if (n_nodes < 1 || n_nodes > kTreeMaxNodes) return 0;
-  return tree_workspace(const_cast<kvq_cache*>(c)->sms(), n_nodes * (q_heads / c->kv_heads));
+  const int rows = n_nodes * (q_heads / c->kv_heads), n_streams = c->batch * c->kv_heads;
+  const size_t wide = tree_workspace(const_cast<kvq_cache*>(c)->sms(), rows);
+  if (rows > kTreeNarrowRows) return wide;
+  return std::max(wide, decode_parts_bytes(n_streams, rows) + tree_narrow_bytes(n_streams, rows));
 }
 
 kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads, int n_nodes, const kvq_rows* k,
@@ -1051,6 +1069,32 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   a.ws = workspace;
   a.num_sms = c->sms();
   const LayerState& L = c->L[layer];
+  const int rows = n_nodes * G;
+  // Few rows over a cache that holds tokens: the decode kernel reads it (one of
+  // its eight query columns a row), with the drafted tokens as one more partial
+  // of each stream.  One node of 7 heads over 32K 4-bit tokens takes 58 us so and
+  // 120 us through the tree kernel, whose tiles cost the same for 1 to 16 rows.
+  if (rows <= kTreeNarrowRows && a.c.n_prog + a.c.n_win > 0) {
+    const int n_streams = c->batch * c->kv_heads;
+    DecodePlan d = plan_decode(c, L);
+    d.splits = std::min(d.splits, kMaxSplits - 1 - d.wsplits);
+    d.nparts = d.splits + d.wsplits + 1;
+    TreeNarrow t{};
+    t.parts = static_cast<float*>(workspace);
+    t.q = static_cast<uint8_t*>(workspace) + decode_parts_bytes(n_streams, rows);
+    t.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(t.q) + (size_t)n_streams * rows * kHeadDim * 2);
+    t.nparts = d.nparts;
+    TreeOut o;
+    o.out = out;
+    o.nodes = n_nodes;
+    o.heads = q_heads;
+    o.group = G;
+    o.counters = t.counters;
+    if (cudaError_t e = launch_tree_draft(a, t, s)) return cuda_fail(e, "tree attention launch");
+    if (cudaError_t e = enqueue_decode(c, layer, d, t.q, c->kv_heads * rows, sm_scale, nullptr, t.parts, s, AppendOne(), o))
+      return cuda_fail(e, "tree attention launch");
+    return KVQ_OK;
+  }
   if (cudaError_t e = launch_tree(a, make_fill(L.bits, L.nt, L.pf, L.n_shrinks, L.n), s)) return cuda_fail(e, "tree attention launch");
   return KVQ_OK;
 }

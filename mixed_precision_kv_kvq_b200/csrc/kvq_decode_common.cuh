@@ -335,6 +335,17 @@ __device__ __forceinline__ void finish_stream(const DecodeArgs& a, int s, int sp
     add(k, v0, v1);
   }
   __syncthreads();  // the sums of w L
+  if (a.tree_out) {
+    for (int h = 0; h < G; h++) {
+      const int node = h / a.tree_group, g = h - node * a.tree_group;
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMaxGroup; i++) v = i == h ? acc[i] / mxs[kMaxGroup + i] : v;
+      static_cast<__nv_bfloat16*>(a.tree_out)[(((size_t)b * a.tree_nodes + node) * a.tree_heads + j * a.tree_group + g) * kHeadDim + c] =
+          __float2bfloat16_rn(v);
+    }
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < kMaxGroup; h++)
     if (h < G) outp[h * kHeadDim + c] = acc[h] / mxs[kMaxGroup + h];

@@ -258,6 +258,12 @@ struct DecodeArgs {
   const uint32_t* kmc;   // [streams][blocks_max][128]
   int blocks_max;
   Epochs ep;
+  // a tree of few rows (kvq_tree_attn): the `group` query rows of a stream are
+  // node r / tree_group, head r % tree_group of its KV head, and the merged rows
+  // go to tree_out, bf16 [batch][tree_nodes][tree_heads][128], instead of out.
+  // The drafted tokens' partial is among nparts already.
+  void* tree_out;
+  int tree_nodes, tree_heads, tree_group;
 };
 
 // CTAs per stream for a launch over n_streams streams on num_sms SMs.

@@ -81,7 +81,92 @@ __global__ void __launch_bounds__(kHeadDim) tree_merge_kernel(const __grid_const
 }
 static_assert(kMergeRows * 32 == kHeadDim, "a warp per row");
 
+// Few rows: the drafted tokens' share of a stream, and its queries for the decode
+// kernel.  One CTA per stream: the n R <= 64 scores by warps (a lane four
+// channels), then a thread per channel for the output.
+__global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_constant__ TreeArgs a, const TreeNarrow t) {
+  constexpr int kN = kTreeNarrowRows;  // rows, and nodes
+  __shared__ float sc[kN][kN];         // score, then weight, of row r and node i
+  __shared__ float ml[2][kN];
+  const int s = blockIdx.x, b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
+  const int R = a.n * a.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();  // the decode launch waits for this kernel before it touches what it writes
+  if (threadIdx.x == 0) t.counters[s] = 1;  // this partial's ticket
+  auto load4 = [&](const void* x, long long at, float (&y)[4], bool f32) {
+    if (f32) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+      y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x) + at);
+      y[0] = __uint_as_float(v.x << 16); y[1] = __uint_as_float(v.x & 0xffff0000u);
+      y[2] = __uint_as_float(v.y << 16); y[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+  };
+  for (int r = warp; r < R; r += 4) {
+    const int node = r / a.group, g = r - node * a.group;
+    const long long at = b * a.q_b + node * a.q_t + (long long)(j * a.group + g) * a.q_h + 4 * lane;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(t.q) + ((size_t)s * R + r) * kHeadDim)[lane] =
+        *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+    float q[4];
+    load4(a.q, at, q, false);
+    for (int i = 0; i < a.n; i++) {
+      const bool see = a.mask ? a.mask[b * a.mask_b + (long long)node * a.n + i] != 0 : i <= node;
+      float d = 0.f;
+      if (see) {
+        float k[4];
+        load4(a.k, b * a.k_b + i * a.k_t + j * a.k_h + 4 * lane, k, a.f32);
+        d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (lane == 0) sc[r][i] = see ? d * a.qscale : -INFINITY;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kN) {
+    const int r = threadIdx.x;
+    float m = -INFINITY, l = 0.f;
+    if (r < R) {
+      for (int i = 0; i < a.n; i++) m = fmaxf(m, sc[r][i]);
+      for (int i = 0; i < a.n; i++) {
+        const float w = m > -INFINITY ? ex2(sc[r][i] - m) : 0.f;
+        sc[r][i] = w;
+        l += w;
+      }
+    }
+    ml[0][r] = m;
+    ml[1][r] = l;
+  }
+  __syncthreads();
+  float o[kN] = {};
+  for (int i = 0; i < a.n; i++) {
+    const long long at = b * a.v_b + i * a.v_t + j * a.v_h + threadIdx.x;
+    const float v = a.f32 ? static_cast<const float*>(a.v)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[at]);
+#pragma unroll
+    for (int r = 0; r < kN; r++)
+      if (r < R && sc[r][i] != 0.f) o[r] = fmaf(sc[r][i], v, o[r]);  // what a row does not see may be anything
+  }
+  float* rec = t.parts + ((size_t)s * t.nparts + t.nparts - 1) * kPartFloats;
+  if (threadIdx.x < kN) {
+    rec[threadIdx.x] = ml[0][threadIdx.x];
+    rec[kMaxGroup + threadIdx.x] = ml[1][threadIdx.x];
+  }
+#pragma unroll
+  for (int r = 0; r < kN; r += 4)
+    *reinterpret_cast<float4*>(rec + 2 * kMaxGroup + threadIdx.x * kMaxGroup + r) = make_float4(o[r], o[r + 1], o[r + 2], o[r + 3]);
+}
+static_assert(kTreeNarrowRows == kMaxGroup, "a decode call's query heads per KV head");
+
 }  // namespace
+
+size_t tree_narrow_bytes(int n_streams, int rows) {
+  return (size_t)n_streams * rows * kHeadDim * 2 + ((size_t)n_streams * 4 + 15) / 16 * 16;
+}
+
+cudaError_t launch_tree_draft(const TreeArgs& a, const TreeNarrow& t, cudaStream_t s) {
+  return launch_pdl(tree_draft_kernel, dim3(a.c.batch * a.c.kv_heads), dim3(kHeadDim), 0, s, a, t);
+}
 
 size_t tree_workspace(int num_sms, int rows) {
   const int block = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;

@@ -70,6 +70,19 @@ struct TreeArgs {
   int num_sms;
 };
 size_t tree_workspace(int num_sms, int rows);
+// Few rows (n group <= kTreeNarrowRows) go through the decode kernel: this launch
+// lays their queries out as a decode call's, [batch][kv_heads][n group][128],
+// leaves the drafted tokens' partial as the last of each stream's nparts and
+// takes its ticket (so counters need no clearing before).
+constexpr int kTreeNarrowRows = 8;
+struct TreeNarrow {
+  void* q;        // bf16
+  float* parts;
+  int* counters;  // [streams]
+  int nparts;
+};
+size_t tree_narrow_bytes(int n_streams, int rows);  // queries and counters
+cudaError_t launch_tree_draft(const TreeArgs& a, const TreeNarrow& t, cudaStream_t s);
 cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s);
 
 }  // namespace kvq

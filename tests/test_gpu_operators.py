@@ -19,6 +19,11 @@ finfo(t).eps / 2 relative to the value (bf16 2^-8, fp16 2^-11, fp32 2^-24).
    delta = u sum_c |q'_c| (3 |k_c| + 2 |c|), c the centre of the Key's group (of
    its channel's block with per-channel groups), plus 2e-4 for the fp32 sums
    and the exponential; weights then change by at most e^(2 delta) - 1 relative.
+   Up to 8 rows (n G) go through the decode kernel: its 15-bit query is finer,
+   but its Value codes enter the MMA uncentred as subnormals, whose products are
+   off by up to 2^-12 of the sum of the terms' sizes, sum_t w_t R_t (the
+   decode kernel's measured bound is 1.8e-4 < 2^-12), p R is rounded once
+   (u |v - c| <= u (|v| + |c|)), and its p may exceed the largest by 2^8 less.
    The output is rounded once to bf16:
    |o - o*| <= u_bf16 |o*| 1.02 + 1.02 ((e^(2 delta) - 1) sum_t w_t |v_t| + the
    above) + 1e-6 (1.02: products of these, and second orders)."""
@@ -225,6 +230,7 @@ def held(kvq, cache, mode, B, H, T, scale, sample=None):
     ks, vs = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 128), np.float32)
 
     kcen, vcen = np.zeros((B, H, T, 128), np.float32), np.zeros((B, H, T, 1), np.float32)
+    vrange = np.zeros((B, H, T, 1), np.float32)
 
     def centre(r, z, b):
         return z + r * (2.0 ** (b - 1) / (2.0 ** b - 1))
@@ -247,6 +253,7 @@ def held(kvq, cache, mode, B, H, T, scale, sample=None):
             vs[b, j, off:off + n] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
             kcen[b, j, off:off + n] = centre(kr, kz, bits)
             vcen[b, j, off:off + n] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], bits)
+            vrange[b, j, off:off + n] = half(vm[:, 0])[:, None]
         if mode != "plain":
             kc, vc, km, vm = cache.export_window(0, sb, sj)
             m = len(kc)
@@ -255,11 +262,12 @@ def held(kvq, cache, mode, B, H, T, scale, sample=None):
             vs[b, j, at] = values(vc, half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
             kcen[b, j, at] = centre(half(km[:, 0])[:, None], half(km[:, 1])[:, None], 16)
             vcen[b, j, at] = centre(half(vm[:, 0])[:, None], half(vm[:, 1])[:, None], 16)
+            vrange[b, j, at] = half(vm[:, 0])[:, None]
     if scale is not None:
         ks = ks * scale.numpy()[None, :, None, :]
         kcen = kcen * scale.numpy()[None, :, None, :]
     ks, vs = torch.from_numpy(ks), torch.from_numpy(vs)
-    ks.centre, vs.centre = torch.from_numpy(kcen), torch.from_numpy(vcen)
+    ks.centre, vs.centre, vs.range = torch.from_numpy(kcen), torch.from_numpy(vcen), torch.from_numpy(vrange)
     return ks, vs
 
 
@@ -355,7 +363,7 @@ def tree_check(q, dk, dv, mask, ks, vs, got, sm_scale=128 ** -0.5):
     dev = "cuda"
     seen = torch.ones(n, n, dtype=torch.bool).tril() if mask is None else mask.bool().cpu()
     seen = seen.expand(B, n, n).to(dev)
-    kc, vc = ks.centre.to(dev).double().abs(), vs.centre.to(dev).double().abs()
+    kc, vc, vr = (x.to(dev).double().abs() for x in (ks.centre, vs.centre, vs.range))
     ks, vs = ks.to(dev).double(), vs.to(dev).double()
     T = ks.shape[2]
     bad = torch.full((), -math.inf, dtype=torch.float64, device=dev)
@@ -369,6 +377,8 @@ def tree_check(q, dk, dv, mask, ks, vs, got, sm_scale=128 ** -0.5):
             kerr[:T] += 2 * kc[b, j]
             verr = 4 * vv.abs()
             verr[:T] += 3 * vc[b, j]
+            if n * G <= 8 and T:
+                verr[:T] += 2.0 ** -12 / U16 * vr[b, j]
             for g in range(G):
                 qq = q[b, :, j * G + g].double()
                 s = torch.where(vis, sm_scale * (qq @ kk.T), bad)
@@ -486,11 +496,11 @@ def test_tree_rows_that_see_nothing(kvq, T):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T", [0, 200])
-def test_tree_padding_never_leaks(kvq, dtype, T):
+@pytest.mark.parametrize("n,real,G", [(14, 9, 5), (8, 3, 1), (7, 2, 1)])
+def test_tree_padding_never_leaks(kvq, dtype, T, n, real, G):
     """Padded nodes hold NaN, infinities and the type's extremes; no other node's output notices."""
     cache, _, ks, vs = make_cache(kvq, "plain", 1, 2, T, 4, 512)
-    n, real = 14, 9
-    q, dk, dv = tree_inputs(11, 1, n, 2, 5, dtype)
+    q, dk, dv = tree_inputs(11, 1, n, 2, G, dtype)
     mask = torch.zeros(n, n, dtype=torch.bool)
     mask[:real, :real] = tree_mask(3, n=real)
     want = cache.tree_attn(0, q, dk, dv, mask.cuda())
@@ -524,10 +534,11 @@ def test_tree_equals_decode_of_one_token(kvq):
     assert ((tree[:, 0].float() - dec).abs() <= 2 * UBF * dec.abs() + 0.01 * dec.abs().amax(-1, keepdim=True)).all()
 
 
-def test_tree_streams_and_graphs(kvq):
+@pytest.mark.parametrize("n,G", [(9, 7), (1, 7), (2, 4)])
+def test_tree_streams_and_graphs(kvq, n, G):
     """Two calls at once on two streams, and two captured graphs replayed in turn and together."""
     cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, 3000, 2, 4096)
-    a, b = tree_inputs(19, 2, 9, 2, 7), tree_inputs(23, 2, 9, 2, 7)
+    a, b = tree_inputs(19, 2, n, 2, G), tree_inputs(23, 2, n, 2, G)
     wa, wb = cache.tree_attn(0, *a), cache.tree_attn(0, *b)
     tree_check(*a, None, ks, vs, wa)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()

@@ -171,11 +171,19 @@ def _rows(t: Optional[torch.Tensor]):
     return _ROWS(t.data_ptr(), b, n, h)
 
 
-def _check_rows(name: str, t: torch.Tensor, dtype, shape=None) -> None:
-    if not t.is_cuda or t.dim() != 4 or t.shape[3] != HEAD_DIM or (t.stride(3) != 1 and t.numel()):
+def _is_rows(t: torch.Tensor, dtype, device) -> bool:
+    """A [batch][n][heads][128] CUDA tensor of this type and device whose channels are neighbours."""
+    return (t.dtype is dtype and t.device == device and t.dim() == 4 and t.shape[3] == HEAD_DIM
+            and (t.stride(3) == 1 or not t.numel()) and t.is_cuda)
+
+
+def _check_rows(name: str, t: torch.Tensor, dtype, shape=None, device=None) -> None:
+    if not _is_rows(t, dtype, t.device if device is None else device):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
         raise ValueError(f"{name} must be a CUDA tensor [batch][n][heads][128] with neighbouring channels")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
@@ -188,7 +196,7 @@ class _On:
 
     def __init__(self, device, stream):
         self.device = device
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self.guard = torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else None
         self.stream = None
         if stream is None:
             self.ptr = torch._C._cuda_getCurrentRawStream(device.index)
@@ -263,36 +271,35 @@ def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: 
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")
-    if first.dim() != 4:
-        raise ValueError("q and k must be [batch][n][heads][128]")
-    dtype, lead = _dtype_code(first), first.shape[:2]
+    dtype, dt, device = _dtype_code(first), first.dtype, first.device
+    _check_rows("q" if q is not None else "k", first, dt)
+    batch, n = first.shape[0], first.shape[1]
+    if q is not None and k is not None:
+        _check_rows("k", k, dt, device=device)
+        if k.shape[0] != batch or k.shape[1] != n:
+            raise ValueError(f"q and k must agree in batch and tokens, got {list(q.shape)} and {list(k.shape)}")
     for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out without {name}")
-            continue
-        _check_rows(name, x, first.dtype)
-        if x.shape[:2] != lead or x.device != first.device:
-            raise ValueError("q and k must agree in batch, tokens and device")
         if y is not None:
-            _check_rows(name + "_out", y, first.dtype, x.shape)
-            if y.device != first.device:
-                raise ValueError("inputs and outputs must be on one device")
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != first.device:
+            if x is None:
+                raise ValueError(f"{name}_out without {name}")
+            _check_rows(name + "_out", y, dt, x.shape, device)
+    pt = positions.dtype
+    if (pt is not torch.int64 and pt is not torch.int32) or positions.device != device:
         raise ValueError("positions must be an int32 or int64 tensor on the device of q and k")
-    if positions.shape == lead:
-        pb, pt = positions.stride()
-    elif positions.dim() == 1 and positions.shape[0] == lead[1]:
-        pb, pt = 0, positions.stride(0)
+    shape = positions.shape
+    if len(shape) == 2 and shape[0] == batch and shape[1] == n:
+        ps_b, ps_t = positions.stride()
+    elif len(shape) == 1 and shape[0] == n:
+        ps_b, ps_t = 0, positions.stride(0)
     else:
-        raise ValueError(f"positions must be {list(lead)} or [{lead[1]}], got {list(positions.shape)}")
-    with _On(first.device, stream) as on:
+        raise ValueError(f"positions must be [{batch}][{n}] or [{n}], got {list(shape)}")
+    with _On(device, stream) as on:
         if q is not None and q_out is None:
-            q_out = on.empty(q.shape, q.dtype)
+            q_out = on.empty(q.shape, dt)
         if k is not None and k_out is None:
-            k_out = on.empty(k.shape, k.dtype)
-        check(load().kvq_rope(rope.rot_dim, rope._code, rope._ptr, rope.magnitude, _dptr(positions),
-                              KVQ_POS_I64 if positions.dtype == torch.int64 else KVQ_POS_I32, pb, pt, lead[0], lead[1], dtype,
+            k_out = on.empty(k.shape, dt)
+        check(load().kvq_rope(rope.rot_dim, rope._code, rope._ptr, rope.magnitude, positions.data_ptr(),
+                              KVQ_POS_I64 if pt is torch.int64 else KVQ_POS_I32, ps_b, ps_t, batch, n, dtype,
                               _rows(q), _rows(q_out), q.shape[2] if q is not None else 0,
                               _rows(k), _rows(k_out), k.shape[2] if k is not None else 0, on.ptr))
     return q_out, k_out
@@ -307,26 +314,29 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     """q: device bf16 [batch][n][q_heads][128]; k, v: device [batch][n][kv_heads][128], bf16 or fp32 (strided views
     allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
     shaped like q."""
+    dtype, dt, device = _dtype_code(k), k.dtype, q.device
     _check_rows("q", q, torch.bfloat16)
-    dtype = _dtype_code(k)
-    b, n = q.shape[:2]
-    _check_rows("k", k, k.dtype, (b, n, k.shape[2], HEAD_DIM))
-    _check_rows("v", v, k.dtype, k.shape)
-    _check_rows("out", out, torch.bfloat16, q.shape)
-    if not out.is_contiguous() or not workspace.is_cuda:
-        raise ValueError("out must be contiguous and workspace a CUDA tensor")
-    mask_b = 0
+    b, n, q_heads, _ = q.shape
+    _check_rows("k", k, dt, device=device)
+    if k.shape[0] != b or k.shape[1] != n:
+        raise ValueError(f"k must be [{b}][{n}][kv_heads][128], got {list(k.shape)}")
+    _check_rows("v", v, dt, k.shape, device)
+    _check_rows("out", out, torch.bfloat16, q.shape, device)
+    if not out.is_contiguous() or workspace.device != device:
+        raise ValueError("out must be contiguous and workspace on its device")
+    mask_ptr, mask_b = None, 0
     if mask is not None:
-        if mask.dtype not in (torch.bool, torch.uint8) or not mask.is_cuda or not mask.is_contiguous():
-            raise ValueError("mask must be a contiguous bool or uint8 CUDA tensor")
-        if tuple(mask.shape) == (b, n, n):
+        mt, ms = mask.dtype, mask.shape
+        if (mt is not torch.bool and mt is not torch.uint8) or mask.device != device or not mask.is_contiguous():
+            raise ValueError("mask must be a contiguous bool or uint8 tensor on the device of q")
+        if len(ms) == 3 and ms[0] == b and ms[1] == n and ms[2] == n:
             mask_b = n * n
-        elif tuple(mask.shape) != (n, n):
-            raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(mask.shape)}")
-    ws_bytes = workspace.numel() * workspace.element_size()
-    check(load().kvq_tree_attn(cache, layer, _rows(q), q.shape[2], n, _rows(k), _rows(v), dtype,
-                               _dptr(mask) if mask is not None else None, mask_b, float(sm_scale), _dptr(out),
-                               _dptr(workspace), ws_bytes, _stream_ptr(stream)))
+        elif len(ms) != 2 or ms[0] != n or ms[1] != n:
+            raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(ms)}")
+        mask_ptr = mask.data_ptr()
+    check(load().kvq_tree_attn(cache, layer, _rows(q), q_heads, n, _rows(k), _rows(v), dtype, mask_ptr, mask_b, sm_scale,
+                               out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               stream if type(stream) is int else _stream_ptr(stream)))
 
 
 def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor],
@@ -336,12 +346,14 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
     first = k_out if k_out is not None else v_out
     if first is None:
         raise ValueError("k_out and v_out are both None")
-    for name, x in (("k_out", k_out), ("v_out", v_out)):
-        if x is not None:
-            _check_rows(name, x, first.dtype, first.shape)
+    dtype, dt = _dtype_code(first), first.dtype
+    _check_rows("k_out" if first is k_out else "v_out", first, dt)
+    if k_out is not None and v_out is not None:
+        _check_rows("v_out", v_out, dt, k_out.shape, k_out.device)
     if first.shape[1] != count:
         raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
-    check(load().kvq_read(cache, layer, start, count, _dtype_code(first), _rows(k_out), _rows(v_out), _stream_ptr(stream)))
+    check(load().kvq_read(cache, layer, start, count, dtype, _rows(k_out), _rows(v_out),
+                          stream if type(stream) is int else _stream_ptr(stream)))
 
 
 def kvq_query(cache, layer: int) -> dict:
@@ -447,6 +459,7 @@ class KVQCache:
         self.pool = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self.handle = kvq_alloc_ex(layers, batch, kv_heads, head_dim, budget_bytes, fbit, self.pool, options)
         self._ws = {}
+        self._tree_ws = {}
         self._stage = {}
 
     # -- helpers
@@ -508,22 +521,23 @@ class KVQCache:
         q: bf16 [batch][n][q_heads][128]; k, v: the drafted tokens' Keys and Values [batch][n][kv_heads][128], bf16 or
         fp32; mask: bool or uint8 [batch][n][n] or [n][n], mask[i][j]: node i sees node j (None: a chain, j <= i).
         -> bf16, shaped like q.  The drafted tokens do not enter the cache."""
-        self._check_batch("q", q, None)
-        self._check_batch("k", k, self.kv_heads)
-        self._check_batch("v", v, self.kv_heads)
-        if mask is not None and mask.device != q.device:
-            raise ValueError("mask must be on the cache's device")
-        if out is not None and out.device != q.device:
-            raise ValueError("out must be on the cache's device")
-        if sm_scale is None:
-            sm_scale = HEAD_DIM ** -0.5
-        with _On(q.device, stream) as on:
+        device = self.pool.device
+        if q.dim() != 4 or q.shape[0] != self.batch or q.device != device:
+            raise ValueError(f"q must be [{self.batch}][n][q_heads][128] on {device}, got {list(q.shape)} on {q.device}")
+        if k.dim() != 4 or k.shape[2] != self.kv_heads:
+            raise ValueError(f"k must be [{self.batch}][n][{self.kv_heads}][128], got {list(k.shape)}")
+        with _On(device, stream) as on:
             # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
-            nbytes = kvq_tree_workspace(self.handle, layer, q.shape[2], q.shape[1])
+            size = (q.shape[2], q.shape[1])
+            nbytes = self._tree_ws.get(size)
+            if nbytes is None:
+                nbytes = kvq_tree_workspace(self.handle, layer, *size)
+                if nbytes:
+                    self._tree_ws[size] = nbytes
             if out is None:
                 out = on.empty(q.shape, torch.bfloat16)
-            ws = on.empty((nbytes,), torch.uint8)
-            kvq_tree_attn(self.handle, layer, q, k, v, mask, sm_scale, out, ws, on.ptr)
+            kvq_tree_attn(self.handle, layer, q, k, v, mask, HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out,
+                          on.empty((nbytes,), torch.uint8), on.ptr)
         return out
 
     def read(self, layer: int, start: int = 0, count: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -540,9 +554,10 @@ class KVQCache:
             if k_out is None and v_out is None:
                 shape = (self.batch, count, self.kv_heads, HEAD_DIM)
                 k_out, v_out = on.empty(shape, dtype), on.empty(shape, dtype)
-            for name, x in (("k_out", k_out), ("v_out", v_out)):
-                if x is not None:
-                    self._check_batch(name, x, self.kv_heads)
+            else:
+                for name, x in (("k_out", k_out), ("v_out", v_out)):
+                    if x is not None:
+                        self._check_batch(name, x, self.kv_heads)
             kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr)
         return k_out, v_out
 

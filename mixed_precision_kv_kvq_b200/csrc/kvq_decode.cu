@@ -465,7 +465,9 @@ struct WarpSmem {
   uint8_t meta[kStages][kStageMeta];
 };
 
-template <int BITS, bool CHAN>
+// TREE: the output of a tree of few rows (a template, so that the decode calls'
+// kernels stay as they are: as a branch it cost them 0.3-1.6 us of 45-81).
+template <int BITS, bool CHAN, bool TREE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   WarpSmem* ws = reinterpret_cast<WarpSmem*>(smem);
@@ -965,32 +967,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
   }
   // warp 0's two code stages (free now; the merge weights above are in registers)
   static_assert(kScratchFloats * 4 <= kStages * kStageCode, "the merge scratch fits");
-  finish_stream(a, s, split, Oc, Mh, Lh, flags, reinterpret_cast<float*>(ws[0].code[0]));
+  finish_stream<TREE>(a, s, split, Oc, Mh, Lh, flags, reinterpret_cast<float*>(ws[0].code[0]));
 }
 
-template <int BITS, bool CHAN>
+template <int BITS, bool CHAN, bool TREE>
 cudaError_t launch_bits(const DecodeArgs& a, cudaStream_t s) {
   constexpr int kBytes = kSmemBytes + (CHAN ? kChanSmem : 0);
   static bool attr_set = false;  // per process and kernel; set before the first launch
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN>, cudaFuncAttributePreferredSharedMemoryCarveout,
+      e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
   const unsigned grid = (unsigned)(a.batch * a.kv_heads) * (unsigned)a.splits;
-  return launch_pdl(decode_kernel<BITS, CHAN>, dim3(grid), dim3(kThreads), kBytes, s, a);
+  return launch_pdl(decode_kernel<BITS, CHAN, TREE>, dim3(grid), dim3(kThreads), kBytes, s, a);
 }
 
-template <bool CHAN>
+template <bool CHAN, bool TREE>
 cudaError_t launch_width(const DecodeArgs& a, cudaStream_t s) {
   switch (a.fill.bits) {
-    case 2: return launch_bits<2, CHAN>(a, s);
-    case 4: return launch_bits<4, CHAN>(a, s);
-    case 8: return launch_bits<8, CHAN>(a, s);
-    case 16: return launch_bits<16, CHAN>(a, s);
+    case 2: return launch_bits<2, CHAN, TREE>(a, s);
+    case 4: return launch_bits<4, CHAN, TREE>(a, s);
+    case 8: return launch_bits<8, CHAN, TREE>(a, s);
+    case 16: return launch_bits<16, CHAN, TREE>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1061,7 +1063,8 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
   const long long units = a.chan ? a.fill.gps / 8 : a.fill.gps;
   if ((long long)a.batch * a.kv_heads * a.splits > (long long)a.rank_sms * kCtasPerSm || units < 2LL * a.splits)
     b.rank_sms = 0;
-  return b.chan ? launch_width<true>(b, s) : launch_width<false>(b, s);
+  if (b.tree_out) return b.chan ? launch_width<true, true>(b, s) : launch_width<false, true>(b, s);
+  return b.chan ? launch_width<true, false>(b, s) : launch_width<false, false>(b, s);
 }
 
 }  // namespace kvq

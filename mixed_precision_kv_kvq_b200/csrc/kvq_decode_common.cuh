@@ -232,7 +232,9 @@ __device__ __forceinline__ uint32_t quad_reg(const uint32_t* u) {
 // and the CTA that takes the stream's last ticket (atomic, no waiting) merges
 // all partials with log-sum-exp weights.  flags[1]: CTA-shared scratch word;
 // scratch: kScratchFloats floats of free shared memory.
+// TREE: a tree of few rows (DecodeArgs::tree_out).
 constexpr int kScratchFloats = 2 * kMaxSplits * kMaxGroup + 2 * kMaxGroup;
+template <bool TREE>
 __device__ __forceinline__ void finish_stream(const DecodeArgs& a, int s, int split, const float (&Oc)[kMaxGroup],
                                               const float (&Mh)[kMaxGroup], const float (&Lh)[kMaxGroup],
                                               volatile int* flags, float* scratch) {
@@ -335,7 +337,7 @@ __device__ __forceinline__ void finish_stream(const DecodeArgs& a, int s, int sp
     add(k, v0, v1);
   }
   __syncthreads();  // the sums of w L
-  if (a.tree_out) {
+  if constexpr (TREE) {  // rows of a tree: bf16, to the call's own layout
     for (int h = 0; h < G; h++) {
       const int node = h / a.tree_group, g = h - node * a.tree_group;
       float v = 0.f;
@@ -344,12 +346,12 @@ __device__ __forceinline__ void finish_stream(const DecodeArgs& a, int s, int sp
       static_cast<__nv_bfloat16*>(a.tree_out)[(((size_t)b * a.tree_nodes + node) * a.tree_heads + j * a.tree_group + g) * kHeadDim + c] =
           __float2bfloat16_rn(v);
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int h = 0; h < kMaxGroup; h++)
-    if (h < G) outp[h * kHeadDim + c] = acc[h] / mxs[kMaxGroup + h];
-  if (threadIdx.x == 0) a.counters[s] = 0;
+    for (int h = 0; h < kMaxGroup; h++)
+      if (h < G) outp[h * kHeadDim + c] = acc[h] / mxs[kMaxGroup + h];
+    if (threadIdx.x == 0) a.counters[s] = 0;
+  }
 }
 
 }  // namespace

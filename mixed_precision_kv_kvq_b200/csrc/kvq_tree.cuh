@@ -18,23 +18,30 @@
 // (16x256b: rows lane / 4 and + 8, two columns a lane), and one channel of two
 // neighbouring tokens in each Value pair (16x128b, one column a lane), so
 // codes are widened in registers and stored once, with no transposition.
-// Codes become val = (c - 2^(b-1)) 2^(1-b) first, exact in fp16 at 8 bits and
-// fewer (rounded to 11 bits at 16), then one fma gives the value times
-// g = (1 - 2^-b) / 2: x g = val R/4 + (Z g + R/4).  With this g R/4 is exact,
-// the value is rounded twice (its centre Z g + R/4, then itself), and nothing
-// in binary16's range overflows.  1/g goes into the query and the output.
+// Codes become val = (c - 2^(b-1)) 2^(1-b), exact in fp16 at 8 bits and fewer
+// (rounded to 11 bits at 16).  With rk = R 2^(b-1) / (2^b - 1) a Key is
+// (Z + rk) + rk val, and the score
+//   s = rk (q' . val + a sum(q')) - m,   a = (Z + rk) / rk.
+// Keys go in as val, and a sum(q') by one more k-step (below); rk and -m are
+// applied in fp32 by the thread that owns the token.  (Keys rounded to fp16 as
+// whole values took the bf16 output from 0.17% to 0.28% off where outlier
+// channels dominate: their errors differ from token to token, while the
+// query's are common to the tokens that matter.)  Drafted Keys and those of
+// per-channel groups go in as fp16 values, rk a constant and a = 0.
+// Values go in as one fma from val: x g = val R/4 + (Z g + R/4), g = (1 - 2^-b) / 2:
+// with this g R/4 is exact, the value is rounded twice (its centre Z g + R/4,
+// then itself), and nothing in binary16's range overflows.
 // S has a token per tensor-memory lane: a thread owns one token and walks the
-// rows, so whether a token counts is a register, P is written row by row as the
-// K-slices that an MN-major operand wants (16-byte stores, 128-byte swizzle),
-// and row sums are per-thread partial sums until the end.  A row's running
-// maximum m_r is shared by the 128 threads and subtracted by the MMA itself:
-// one more k-step multiplies a constant left operand (256, 256, 0, ...) with
-// -m_r / 256 as an fp16 pair (high + low part), so a thread's score is ready for
-// the exponential as it comes out of tensor memory.  (Read from shared memory
-// instead, the per-row terms took 16 LDS.128 per 32 rows and thread, ~1000 cycles
-// of a tile's 3800.)  m_r moves only when some score exceeds it by more than
-// 2^8 (one vote per 32 rows), and only then are column maxima formed and O
-// rescaled in tensor memory.
+// rows, so a token's rk and whether it counts are registers, P is written row by
+// row as the K-slices that an MN-major operand wants (16-byte stores, 128-byte
+// swizzle), and row sums are per-thread partial sums until the end.  The extra
+// k-step of the scores multiplies (a, a, a's low part) with (sum(q'), its low
+// part, sum(q')), fp16 pairs of 22 bits, so that a row's only term at the softmax is
+// -m, four rows an LDS.128 (with sum(q') there too, the loads took ~1000 cycles
+// of a tile's 3800).  The running maximum m of a row is shared by the 128
+// threads; it moves only when some score exceeds it by more than 2^8 (one vote
+// per 32 rows), and only then are column maxima formed and O rescaled in
+// tensor memory.
 //
 // Roles (one CTA per SM, which holds all 512 tensor-memory columns): 8 or 16
 // softmax warps, groups of four widening warps, one warp streaming packed tiles
@@ -123,14 +130,15 @@ struct Split {
   static constexpr uint32_t kColS = 0, kColO = 2 * kStep, kColK = 4 * kStep, kColV = kColK + 128;
   static_assert(kColV + 128 <= 512);
 };
-constexpr int kOnesBytes = kTile * 32;             // constant left operand of the extra k-step: [128][16] fp16
-constexpr int kNegBytes = kHalfRows * 32;          // one half's -m / 256: [64][16] fp16
-constexpr float kNegScale = 256.0f;                // -m up to 1.6e7, to 22 bits
+constexpr int kCentreBytes = kTile * 32;           // a of one buffer's tokens: [128][16] fp16
+constexpr int kSumBytes = kHalfRows * 32;          // sum(q') of one half's rows: [64][16] fp16
+constexpr float kSumScale = 16.0f;                 // sum(q') / 16 and 16 a: up to 10^6 and 4000
+constexpr float kCentreMax = 4000.0f;
 
 struct Small {
-  float neg[2][kHalfRows];           // per half: -m as the MMA subtracts it (kUnset: no token yet, 0 there)
+  float rk[4][kTile];                // of the tokens of tile t, ring of 4
+  float neg[2][kHalfRows];           // per half: -m (kUnset: no token yet)
   float alpha[2][kHalfRows];         // factor of the last rescaling
-  float shift[2][kHalfRows];         // and what it added to the scores
   float red[2][4][kHalfRows];        // per warp: column maxima, then row sums
   float2 ml[2][kHalfRows];           // final (m, l)
   uint32_t seen[4][kTile][4];        // drafted tile t: bit i of word w: the row sees token 32 w + i
@@ -143,16 +151,16 @@ struct Small {
 constexpr int kSmallBytes = (sizeof(Small) + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024 - 1024;  // the base is aligned by hand
 
-// Shared memory: Q of both halves, P of both, the constant operand and -m of the
-// extra k-step, Small, the ring.  (A second P buffer a half, so that a tile's
+// Shared memory: Q of both halves, P of both, the operands of the extra k-step,
+// Small, the ring.  (A second P buffer a half, so that a tile's
 // probabilities need not wait for the product of the tile before, gained
 // nothing: 211 against 207 us for 112 rows over 32K 2-bit tokens.)
 template <int BITS>
 struct Layout {
   static constexpr int kP = 2 * kQBytes;
-  static constexpr int kOnes = kP + 2 * kPBytes;
-  static constexpr int kNeg = kOnes + kOnesBytes;
-  static constexpr int kSmall = kNeg + 2 * kNegBytes;
+  static constexpr int kCentre = kP + 2 * kPBytes;
+  static constexpr int kSum = kCentre + 2 * kCentreBytes;
+  static constexpr int kSmall = kSum + 2 * kSumBytes;
   static constexpr int kRing = kSmall + kSmallBytes;
   static constexpr int kStage = kTileGroups * (group_bytes(BITS) + 128) + 4 * kHeadDim;
   static constexpr int kFit = (kSmemMax - kRing) / kStage;
@@ -434,11 +442,10 @@ __device__ __forceinline__ void window_factors(uint32_t m0, uint32_t m1, uint32_
 }
 
 // Keys of one group into 16 tensor-memory rows, 64 channels at a time.  part:
-// the group's Key part; rc, zc: factors of tokens g and g + 8; CHAN:
-// per-channel groups, their (R, Z) words at kmc (the cache's width).
+// the group's Key part.  CHAN: per-channel groups, their (R, Z) words at kmc (the
+// cache's width): values times g; otherwise val.
 template <int BITS, bool CHAN, typename From>
-__device__ __forceinline__ void widen_keys(From part, const uint32_t (&rc)[2], const uint32_t (&zc)[2], FromRing kmc,
-                                           uint32_t taddr, int lane) {
+__device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t taddr, int lane) {
   constexpr int kHalfWords = BITS / 2;  // words of 4 quad positions of one token
   const From unit = part + lane * unit_bytes(BITS);
 #pragma unroll
@@ -470,10 +477,13 @@ __device__ __forceinline__ void widen_keys(From part, const uint32_t (&rc)[2], c
       }
 #pragma unroll
       for (int x = 0; x < 2; x++) {
-        uint32_t k0, k1;
+        uint32_t& k0 = r[4 * p + 2 * x];
+        uint32_t& k1 = r[4 * p + 2 * x + 1];
         key_pairs<BITS>(u[x], p, k0, k1);
-        r[4 * p + 2 * x] = hfma2_u(k0, CHAN ? ra[0] : rc[x], CHAN ? za[0] : zc[x]);
-        r[4 * p + 2 * x + 1] = hfma2_u(k1, CHAN ? ra[1] : rc[x], CHAN ? za[1] : zc[x]);
+        if constexpr (CHAN) {
+          k0 = hfma2_u(k0, ra[0], za[0]);
+          k1 = hfma2_u(k1, ra[1], za[1]);
+        }
       }
     }
     tc_st_16x256_x4(taddr + 32 * hf, r);
@@ -784,6 +794,18 @@ __device__ __forceinline__ void draft_seen(const TreePlan& p, uint32_t (*seen)[4
   }
 }
 
+// What a token's score needs beside val: rk for the softmax, a for the extra
+// k-step.  A range below |Z + rk| / 4000 (binary16 gives Z itself to 1 / 2048) is
+// taken as that, in a too, so that equal codes still give Z.
+__device__ __forceinline__ void key_terms(uint32_t m, float half_codes, float& rk, uint2& centre) {
+  const float r = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * half_codes;
+  const float z = __half2float(__ushort_as_half((unsigned short)(m >> 16)));
+  rk = fmaxf(r, fabsf(z) * (1.0f / (kCentreMax - 1.0f)));
+  const float a = rk > 0.f ? (z + rk) / rk * kSumScale : 0.f;
+  const float hi = __half2float(__float2half_rn(a));
+  centre = make_uint2(pack_h2(hi, hi), pack_h2(a - hi, 0.f));
+}
+
 // Widening: Keys, then Values of buffer buf's tiles (every second one), and for
 // drafted tiles which rows see them.  Warp w of a group writes tensor-memory rows
 // 32 w .. + 31: Keys of tokens 32 w .. + 31, Values of the channels of lane units
@@ -798,7 +820,8 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
   const int i0 = part * kKeys, v0 = part * kValues;
   const CacheView& c = p.a.c;
   constexpr int gb = group_bytes(BITS);
-  const int g = lane >> 2, t4 = lane & 3;
+  const int t4 = lane & 3;
+  const uint32_t centre_at = sb - Lay::kSmall + Lay::kCentre + buf * kCentreBytes;
   const uint32_t tk = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColK + 64 * buf;
   const uint32_t tv = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColV + 64 * buf;
   uint32_t phase = 1;  // of k_free and v_free
@@ -813,35 +836,31 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
         tree_wait(KVQ_BAR(k_free, buf), phase, p.a.err, &sm.abort);
         tc_after();
         // ---- Keys ----
+        const int tl = 32 * w + 16 * i0 + (kKeys == 2 ? lane : lane & 15);  // this lane's token (one group: twice)
+        float rk = 0.f;
+        uint2 centre = make_uint2(0u, 0u);
         if (packed) {
           // groups that do not exist are read as whatever the stage holds: those rows of S are not used
+          const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
+          if (c.kmc) {
 #pragma unroll 1
-          for (int i = i0; i < i0 + kKeys; i++) {
-            const uint32_t ti = tk + ((uint32_t)(16 * i) << 16);
-            const FromRing codes = st + (2 * w + i) * gb;
-            uint32_t rc[2] = {0u, 0u}, zc[2] = {0u, 0u};
-            if (c.kmc) {
-              widen_keys<BITS, true>(codes, rc, zc, st + kTileGroups * (gb + 128), ti, lane);
-            } else {
-              const FromRing meta = st + (kTileGroups * gb + (2 * w + i) * 128 + 8 * g);
-              const uint32_t m0 = meta.u32(), m1 = (meta + 64).u32();
-              group_factors<BITS>(m0, m0, rc[0], zc[0]);
-              group_factors<BITS>(m1, m1, rc[1], zc[1]);
-              widen_keys<BITS, false>(codes, rc, zc, st, ti, lane);
-            }
+            for (int i = i0; i < i0 + kKeys; i++)
+              widen_keys<BITS, true>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), tk + ((uint32_t)(16 * i) << 16), lane);
+            rk = 1.0f / value_scale<BITS>();
+          } else {
+#pragma unroll 1
+            for (int i = i0; i < i0 + kKeys; i++)
+              widen_keys<BITS, false>(st + (2 * w + i) * gb, st, tk + ((uint32_t)(16 * i) << 16), lane);
+            key_terms(m, (float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u), rk, centre);
           }
         } else if (t < p.tp + p.tw) {
 #pragma unroll 1
           for (int i = i0; i < i0 + kKeys; i++) {
             const WindowGroup wg = window_group(p, wk.s, t, 2 * w + i);
-            if (wg.code) {
-              uint32_t rc[2], zc[2];
-              const uint32_t m0 = wg.meta[2 * g], m1 = wg.meta[2 * g + 16];
-              window_factors<BITS>(m0, m0, rc[0], zc[0]);
-              window_factors<BITS>(m1, m1, rc[1], zc[1]);
-              widen_keys<16, false>(FromGlobal{wg.code}, rc, zc, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
-            }
+            if (wg.code) widen_keys<16, false>(FromGlobal{wg.code}, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
           }
+          const WindowGroup wg = window_group(p, wk.s, t, tl >> 4);
+          if (wg.meta) key_terms(wg.meta[2 * (tl & 15)], 32768.0f / 65535.0f, rk, centre);
         } else {
           const int j0 = (t - p.tp - p.tw) * kTile + 32 * w;
 #pragma unroll 1
@@ -849,7 +868,11 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
             if (j0 + 16 * i < p.a.n)
               draft_keys(p, wk.s, j0 + 16 * i, value_scale<BITS>(), tk + ((uint32_t)(16 * i) << 16), lane);
           if (part == 0) draft_seen(p, sm.seen[ct & 3], wk.s, wk.block, t, w, lane);
+          rk = 1.0f / value_scale<BITS>();
         }
+        sm.rk[ct & 3][tl] = rk;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(centre_at + narrow_at(tl)), "r"(centre.x), "r"(centre.y) : "memory");
+        fence_async_smem();
         tc_wait_st();
         tc_before();
         __syncwarp();
@@ -921,7 +944,7 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
   using Lay = Layout<BITS>;
   const uint64_t q_desc = smem_desc(at + half * kQBytes);
   const uint64_t p_desc = smem_desc(at + Lay::kP + half * kPBytes);
-  const uint64_t ones_desc = narrow_desc(at + Lay::kOnes), neg_desc = narrow_desc(at + Lay::kNeg + half * kNegBytes);
+  const uint64_t centre_desc = narrow_desc(at + Lay::kCentre), sum_desc = narrow_desc(at + Lay::kSum + half * kSumBytes);
   // The two products of a tile are issued each as soon as it is ready: the next
   // tile's scores first where the Keys are early, the output first where they are
   // late (it frees the Values' buffer).
@@ -972,7 +995,7 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
           (!q.first || mbar_test(KVQ_BAR(q_full, half), (q.segs - 1) & 1))) {
         tc_after();
         if (elect_one()) {
-          tc_mma_ss(ts, ones_desc, neg_desc, kDescQk, false);  // - m
+          tc_mma_ss(ts, centre_desc + (kCentreBytes >> 4) * buf, sum_desc, kDescQk, false);  // a sum(q')
 #pragma unroll
           for (int k = 0; k < 8; k++)
             tc_mma(ts, tk + 64 * buf + 8 * k, q_desc + (((k >> 2) * (kQBytes / 2) + 32 * (k & 3)) >> 4), kDescQk, true);
@@ -1059,13 +1082,12 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
   using Lay = Layout<BITS>;
   uint8_t* p_all = base + Lay::kP;
   uint8_t* p_smem = p_all + half * kPBytes;
-  uint8_t* neg_smem = base + Lay::kNeg + half * kNegBytes;
+  uint8_t* sum_smem = base + Lay::kSum + half * kSumBytes;
   // the product of this half's tile i is in
   auto wait_pv = [&](uint32_t i) { tree_wait(KVQ_BAR(pv_done, half), i & 1, p.a.err, &sm.abort); };
   const int id = 1 + wg;  // barriers 1 .. 4: one warpgroup; 5: every softmax thread; 6, 7: one half
   uint32_t ct = 0, n = 0;
   constexpr float out_scale = 1.0f / value_scale<BITS>();
-  const float q_scale = a.qscale * out_scale;
   while (wk.next(p)) {
     const int b = wk.s / a.c.kv_heads, j = wk.s - b * a.c.kv_heads;
     const int r0 = wk.block * p.block_rows + (DUAL ? half * kHalfRows : 0) + cb;  // first row of these columns
@@ -1076,7 +1098,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
     for (int i = 0; i < C / 2; i++) l2[i] = make_float2(0.f, 0.f);
     if (mine > 0) {
-      // ---- q' = q lambda sm_scale log2(e) / g as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
+      // ---- q' = q lambda sm_scale log2(e) as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
       const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
                                  : make_float4(1.f, 1.f, 1.f, 1.f);
       uint2 raw[C / 4];
@@ -1093,22 +1115,31 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
       for (int i = 0; i < C / 4; i++) {
         const int rs = cb + w + 4 * i;  // row of the half's Q
-        const float x0 = __uint_as_float(raw[i].x << 16) * q_scale * lam.x;
-        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * q_scale * lam.y;
-        const float x2 = __uint_as_float(raw[i].y << 16) * q_scale * lam.z;
-        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * q_scale * lam.w;
+        const float x0 = __uint_as_float(raw[i].x << 16) * a.qscale * lam.x;
+        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * a.qscale * lam.y;
+        const float x2 = __uint_as_float(raw[i].y << 16) * a.qscale * lam.z;
+        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * a.qscale * lam.w;
+        const uint32_t h02 = sat_h2(x0, x2), h13 = sat_h2(x1, x3);
+        const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02));
+        const float2 f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
+        float sum = (f02.x + f02.y) + (f13.x + f13.y);  // of the rounded q', as the products see it
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int chunk = (lane & 15) >> 1;
         *reinterpret_cast<uint2*>(q_smem + (lane >> 4) * (kQBytes / 2) + rs * 128 + ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) =
-            make_uint2(sat_h2(x0, x2), sat_h2(x1, x3));
-      }
-      if (tl < C) {  // no maximum yet
-        sm.neg[half][cb + tl] = kUnset;
-        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl)) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(neg_smem + narrow_at(cb + tl) + 128) = make_uint4(0u, 0u, 0u, 0u);
+            make_uint2(h02, h13);
+        if (lane == 0) {
+          const float sc = fminf(fmaxf(sum * (1.0f / kSumScale), -65504.f), 65504.f);
+          const float hi = __half2float(__float2half_rn(sc));
+          *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs)) = make_uint4(pack_h2(hi, sc - hi), pack_h2(hi, 0.f), 0u, 0u);
+          *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs) + 128) = make_uint4(0u, 0u, 0u, 0u);
+          sm.neg[half][rs] = kUnset;  // no maximum yet
+        }
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(KVQ_BAR(q_full, half));
+      bar_sync(id, 128);  // neg
     }
     int done = 0;
     for (int t = wk.t0; t < wk.t1; t++, ct++) {
@@ -1124,23 +1155,38 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
         for (int i = 0; i < C; i++) hide |= (seen[i][w] >> lane & 1u) ? 0u : 1u << i;
       }
-      uint32_t xb[C];  // scores less the running maxima, as bits
-      tc_ld(xb, ts);
-      if (hide) {
+      const float rk = sm.rk[ct & 3][tl];
+      float2 x[C / 2];
+      auto scores = [&]() {  // less the running maxima (a row that has none: relative to -kUnset)
+        uint32_t d[C];
+        tc_ld(d, ts);
 #pragma unroll
-        for (int i = 0; i < C; i++)
-          if (hide >> i & 1u) xb[i] = 0xff800000u;  // - infinity
-      }
+        for (int i = 0; i < C; i += 4) {
+          const float4 neg = *reinterpret_cast<const float4*>(&sm.neg[half][cb + i]);
+          x[i / 2] = fma2(splat2(rk), make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), make_float2(neg.x, neg.y));
+          x[i / 2 + 1] = fma2(splat2(rk), make_float2(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), make_float2(neg.z, neg.w));
+        }
+        if (hide) {
+#pragma unroll
+          for (int i = 0; i < C / 2; i++) {
+            if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
+            if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
+          }
+        }
+      };
+      scores();
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < C; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(xb[i]), __uint_as_float(xb[i + 1])));
-      // A segment's first tile has no maxima: its scores come out as they are.  So
-      // do those of a row that has seen nothing yet, which only drafted tiles leave.
-      if (bar_or(id, 128, done == 0 || t >= p.tp + p.tw || fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
+      for (int i = 0; i < C / 2; i++) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(x[i].x, x[i].y));
+      if (bar_or(id, 128, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
+        // Column maxima from the scores themselves: a row's first ones were taken
+        // against no maximum.
         {
+          uint32_t d[C];
           float v[C];
+          tc_ld(d, ts);
 #pragma unroll
-          for (int i = 0; i < C; i++) v[i] = __uint_as_float(xb[i]);
+          for (int i = 0; i < C; i++) v[i] = (hide >> i & 1u) ? -INFINITY : rk * __uint_as_float(d[i]);
           warp_columns<C, true>(v, lane);
           sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
         }
@@ -1148,21 +1194,14 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
         if (tl < C) {
           const int c = cb + tl;
           const float old = sm.neg[half][c];
-          const float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
-          float shift = 0.f, f = 1.f;
-          if (old == kUnset ? m > -INFINITY : m > 0.f) {  // a row that has seen nothing stays unset
-            const float base_neg = old == kUnset ? 0.f : old;
-            const float want = (base_neg - m) * (1.0f / kNegScale);
-            const float hi = __half2float(__float2half_rn(want)), lo = __half2float(__float2half_rn(want - hi));
-            const float neg = (hi + lo) * kNegScale;  // what the MMA will add
-            shift = neg - base_neg;
-            f = old == kUnset ? 0.f : ex2(shift);
-            sm.neg[half][c] = neg;
-            *reinterpret_cast<uint32_t*>(neg_smem + narrow_at(c)) = pack_h2(hi, lo);
-            fence_async_smem();
+          float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
+          float f = 0.f;
+          if (old != kUnset) {
+            m = fmaxf(m, -old);
+            f = ex2(-old - m);
           }
           sm.alpha[half][c] = f;
-          sm.shift[half][c] = shift;
+          if (m > -INFINITY) sm.neg[half][c] = -m;  // a row that has seen nothing stays unset
         }
         bar_sync(id, 128);
         if (done > 0) {  // O so far, once the last product is in
@@ -1181,8 +1220,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
           for (int i = 0; i < C / 2; i++) l2[i] = mul2(l2[i], al[i]);
           tc_wait_st();
         }
-#pragma unroll
-        for (int i = 0; i < C; i++) xb[i] = __float_as_uint(__uint_as_float(xb[i]) + sm.shift[half][cb + i]);
+        scores();
       }
       tc_before();  // S is in registers: the next tile's product may start
       __syncwarp();
@@ -1195,7 +1233,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           const int i = 4 * q + e;
-          const float2 pr = make_float2(ex2(__uint_as_float(xb[2 * i])), ex2(__uint_as_float(xb[2 * i + 1])));
+          const float2 pr = make_float2(ex2(x[i].x), ex2(x[i].y));
           l2[i] = add2(l2[i], pr);
           h[e] = pack_h2(pr.x, pr.y);
         }
@@ -1366,10 +1404,10 @@ __global__ void __launch_bounds__(Split<COLS>::kThreads, 1) tree_kernel(const __
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x < kTile) {  // the constant operand of the extra k-step
-    uint8_t* ones = base + Lay::kOnes + narrow_at(threadIdx.x);
-    *reinterpret_cast<uint4*>(ones) = make_uint4(splat_h(pow2_h(8)), 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(ones + 128) = make_uint4(0u, 0u, 0u, 0u);
+  if (threadIdx.x < 2 * kTile) {  // the widening warps write the first 8 bytes of a token's row
+    uint8_t* centre = base + Lay::kCentre + (threadIdx.x / kTile) * kCentreBytes + narrow_at(threadIdx.x % kTile);
+    *reinterpret_cast<uint4*>(centre) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(centre + 128) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
   tc_before();

@@ -153,20 +153,20 @@ __device__ __forceinline__ void read_group(const ReadArgs& a, const uint8_t* gba
   }
 }
 
-// Groups [g0, g0 + pg) of every stream's progressive cache (in the order of
-// arrival), then wg groups of the window or the staged block.
-template <int BITS, typename T>
-__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a, int g0, int pg, int wg) {
+// Groups [g0, g0 + n) of every stream's progressive cache (in the order of
+// arrival), or (WIN) of the window or the staged block.  Heads run fastest over
+// the warps: neighbouring warps write neighbouring rows of the output.
+template <int BITS, typename T, bool WIN>
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a, int g0, int n) {
   __shared__ __align__(16) uint8_t smem[kReadWarps][kGroupTokens * row_pitch<T>()];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kReadWarps + warp;
-  const int per = pg + wg;
-  const long long streams = (long long)a.c.batch * a.c.kv_heads;
-  if (unit >= streams * per) return;
-  const int s = (int)(unit / per), u = (int)(unit - (long long)s * per);
-  const int b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
+  const int per = n * a.c.kv_heads;
+  if (unit >= (long long)a.c.batch * per) return;
+  const int b = (int)(unit / per), rest = (int)(unit - (long long)b * per), u = rest / a.c.kv_heads, j = rest - u * a.c.kv_heads;
+  const int s = b * a.c.kv_heads + j;
   const long long shift = a.c.window ? 1 : 0;  // progressive token i is token i + 1 after the sink
-  if (u < pg) {
+  if constexpr (!WIN) {
     const int i0 = kGroupTokens * (g0 + u);
     const Place pl = place_of(a.c.ep, i0);
     const size_t tile = (size_t)s * a.c.nt + pl.tile;
@@ -178,26 +178,26 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadArgs a,
                         a.c.meta + (tile * a.c.pf + pl.slot) * 2, kmc, b, j, rel, smem[warp], lane);
   } else {
     constexpr int kGroups = slots_per_tile(16) / kGroupTokens;  // groups of a 16-bit tile
-    const int wgi = u - pg, slot = kGroupTokens * wgi + lane;
-    const size_t tile = (size_t)s * kWindowTiles + wgi / kGroups;
-    const int first = kGroupTokens * (wgi % kGroups);
+    const int slot = kGroupTokens * u + lane;
+    const size_t tile = (size_t)s * kWindowTiles + u / kGroups;
+    const int first = kGroupTokens * (u % kGroups);
     const long long tok = a.c.window ? window_token(a.c.n_all, slot) : a.c.n_prog + slot;
     const long long rel = lane < kGroupTokens && slot < a.c.n_win ? tok - a.start : -1;
-    read_group<16, T>(a, a.c.wcodes + tile * kTileBytes + (size_t)(wgi % kGroups) * group_bytes(16),
+    read_group<16, T>(a, a.c.wcodes + tile * kTileBytes + (size_t)(u % kGroups) * group_bytes(16),
                       a.c.wmeta + (tile * slots_per_tile(16) + first) * 2, nullptr, b, j, rel, smem[warp], lane);
   }
 }
 
-template <int BITS>
-cudaError_t launch_bits(const ReadArgs& a, int g0, int pg, int wg, cudaStream_t s) {
-  const long long units = (long long)a.c.batch * a.c.kv_heads * (pg + wg);
+template <int BITS, bool WIN>
+cudaError_t launch_bits(const ReadArgs& a, int g0, int n, cudaStream_t s) {
+  const long long units = (long long)a.c.batch * a.c.kv_heads * n;
   if (units == 0) return cudaSuccess;
   const long long ctas = (units + kReadWarps - 1) / kReadWarps;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (a.f32)
-    read_kernel<BITS, float><<<(unsigned)ctas, kReadWarps * 32, 0, s>>>(a, g0, pg, wg);
+    read_kernel<BITS, float, WIN><<<(unsigned)ctas, kReadWarps * 32, 0, s>>>(a, g0, n);
   else
-    read_kernel<BITS, __nv_bfloat16><<<(unsigned)ctas, kReadWarps * 32, 0, s>>>(a, g0, pg, wg);
+    read_kernel<BITS, __nv_bfloat16, WIN><<<(unsigned)ctas, kReadWarps * 32, 0, s>>>(a, g0, n);
   return cudaGetLastError();
 }
 
@@ -217,11 +217,12 @@ cudaError_t launch_read(const ReadArgs& a, cudaStream_t s) {
   // the window holds token 0 and the latest ones; staged tokens follow the progressive ones
   const bool tail = a.c.n_win > 0 && (a.start + a.n > a.c.n_prog + shift || (a.c.window && a.start == 0));
   const int wg = tail ? (a.c.n_win + kGroupTokens - 1) / kGroupTokens : 0;
+  if (cudaError_t e = launch_bits<16, true>(a, 0, wg, s)) return e;
   switch (a.c.bits) {
-    case 2: return launch_bits<2>(a, g0, pg, wg, s);
-    case 4: return launch_bits<4>(a, g0, pg, wg, s);
-    case 8: return launch_bits<8>(a, g0, pg, wg, s);
-    case 16: return launch_bits<16>(a, g0, pg, wg, s);
+    case 2: return launch_bits<2, false>(a, g0, pg, s);
+    case 4: return launch_bits<4, false>(a, g0, pg, s);
+    case 8: return launch_bits<8, false>(a, g0, pg, s);
+    case 16: return launch_bits<16, false>(a, g0, pg, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -21,9 +21,9 @@ __global__ void __launch_bounds__(kHeadDim) tree_merge_kernel(const __grid_const
   __shared__ __align__(16) __nv_bfloat16 sh[kMergeRows][kHeadDim];
   const TreeArgs& a = p.a;
   const int x = blockIdx.x, s = x / p.blocks, block = x - s * p.blocks;
-  const int c0 = cta_of(p.units, p.grid, x * p.tiles), c1 = cta_of(p.units, p.grid, x * p.tiles + p.tiles - 1);
+  const int c0 = cta_of(p, x, 0), c1 = cta_of(p, x, p.tiles - 1);
   const int b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
-  const int first = cta_begin(p.units, p.grid, c0) == x * p.tiles ? 0 : 1;  // the record of CTA c0
+  const int first = cta_begin(p, c0) == x * p.tiles ? 0 : 1;  // the record of CTA c0
   const float* p0 = p.parts + ((size_t)c0 * 2 + first) * p.rec;
   const float* p1 = p.parts + (size_t)(c0 + 1) * 2 * p.rec;  // record k >= 1 at p1 + (k - 1) 2 rec
   const int nrec = c1 - c0 + 1, rb = blockIdx.y * kMergeRows;
@@ -192,7 +192,8 @@ cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
   p.tw = (a.c.n_win + kTile - 1) / kTile;
   p.td = (a.n + kTile - 1) / kTile;
   p.tiles = p.tp + p.tw + p.td;
-  const long long units = (long long)a.c.batch * a.c.kv_heads * p.blocks * p.tiles;
+  p.extra = kDraftExtra * p.td;
+  const long long units = (long long)a.c.batch * a.c.kv_heads * p.blocks * (p.tiles + p.extra);
   if (units > 0x7fffffffLL || a.num_sms < 1) return cudaErrorInvalidValue;
   p.units = (int)units;
   p.grid = (int)std::min<long long>(units, std::min(a.num_sms, kMergeRecords));
@@ -206,8 +207,8 @@ cudaError_t launch_tree(const TreeArgs& a, const Fill& f, cudaStream_t s) {
     case 16: e = launch_tree_bits<16>(p, s); break;
     default: return cudaErrorInvalidValue;
   }
-  if (e != cudaSuccess || p.units % p.grid == 0 && (p.units / p.grid) % p.tiles == 0) return e;  // every share whole blocks of rows
-  return launch_pdl(tree_merge_kernel, dim3((unsigned)(p.units / p.tiles), (unsigned)((p.block_rows + kMergeRows - 1) / kMergeRows)),
+  if (e != cudaSuccess || p.units % p.grid == 0 && (p.units / p.grid) % (p.tiles + p.extra) == 0) return e;  // every share whole blocks of rows
+  return launch_pdl(tree_merge_kernel, dim3((unsigned)(p.units / (p.tiles + p.extra)), (unsigned)((p.block_rows + kMergeRows - 1) / kMergeRows)),
                     dim3(kHeadDim), 0, s, p);
 }
 

@@ -83,14 +83,24 @@ struct TreePlan {
   int part_group, part_valid;  // the one group that may be partial, and its tokens
   int rows, block_rows, blocks;  // query rows of a stream, rows per block, blocks
   int tp, tw, td, tiles;         // progressive, window and drafted tiles of a stream
-  int units, grid;
+  int extra, units, grid;
   int rec;              // floats of one partial record
   float* parts;         // [grid][2][rec]: m[block_rows], l[block_rows], O[block_rows][128]
 };
 
-__host__ __device__ __forceinline__ int cta_begin(int units, int grid, int i) { return (int)((long long)units * i / grid); }
-__host__ __device__ __forceinline__ int cta_of(int units, int grid, int u) {
-  return (int)((((long long)u + 1) * grid - 1) / units);
+// A CTA's share.  The line's units are the tiles of every (stream, block of rows),
+// drafted tiles counting 1 + kDraftExtra each (at the end of their block): units
+// are cut evenly, a cut inside a drafted tile moves to the block's end, and
+// tile_at gives it as a tile of the line, block * tiles + tile.
+constexpr int kDraftExtra = 3;
+__host__ __device__ __forceinline__ int cta_begin(const TreePlan& p, int i) {
+  const int per = p.tiles + p.extra, v = (int)((long long)p.units * i / p.grid), x = v / per;
+  const int t = v - x * per;
+  return x * p.tiles + (t < p.tiles ? t : p.tiles);
+}
+__host__ __device__ __forceinline__ int cta_of(const TreePlan& p, int block, int tile) {
+  const long long v = (long long)block * (p.tiles + p.extra) + tile;
+  return (int)(((v + 1) * p.grid - 1) / p.units);
 }
 
 // The kernel for caches of BITS bits (kvq_tree_<BITS>.cu).
@@ -669,40 +679,53 @@ __device__ __forceinline__ WindowGroup window_group(const TreePlan& p, int s, in
                      p.a.c.wmeta + (tile * slots_per_tile(16) + kGroupTokens * (wg % kPer)) * 2};
 }
 
-// Drafted Keys of a group, as k g / lambda.
-__device__ __forceinline__ void draft_keys(const TreePlan& p, int s, int j0, float scale, uint32_t taddr, int lane) {
-  const TreeArgs& a = p.a;
-  const int b = s / a.c.kv_heads, h = s - b * a.c.kv_heads;
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
-  for (int hf = 0; hf < 2; hf++) {
-    uint32_t r[16];
+// Drafted Keys of a group: a lane's part of tokens g and g + 8 as it is in memory
+// (bf16: channels 16 q + 4 t .. + 3 of both halves; fp32: of half hf), so that
+// the loads are in flight while something else is done, and into tensor memory
+// as k g / lambda.
+struct DraftKeys {
+  uint4 raw[2][4];
+  __device__ __forceinline__ void load(const TreeArgs& a, int b, int h, int j0, int hf, int lane) {
 #pragma unroll
     for (int x = 0; x < 2; x++) {
-      const int j = j0 + g + 8 * x;
-      const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 64 * hf + 4 * t;
+      const int j = j0 + (lane >> 2) + 8 * x;
+      const long long at = b * a.k_b + j * a.k_t + h * a.k_h + 4 * (lane & 3);
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+        raw[x][q] = make_uint4(0u, 0u, 0u, 0u);
         if (j < a.n) {
           if (a.f32) {
-            k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k) + at + 16 * q));
+            raw[x][q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.k) + at + 64 * hf + 16 * q));
           } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q));
-            k = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                            __uint_as_float(w.y & 0xffff0000u));
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + at + 16 * q;
+            const uint2 lo = __ldg(reinterpret_cast<const uint2*>(k)), hi = __ldg(reinterpret_cast<const uint2*>(k + 64));
+            raw[x][q] = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
         }
-        float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (a.c.lam_inv)
-          l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 64 * hf + 16 * q + 4 * t));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const TreeArgs& a, int h, int hf, float scale, uint32_t taddr, int lane) const {
+    uint32_t r[16];
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      float4 l = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (a.c.lam_inv)
+        l = __ldg(reinterpret_cast<const float4*>(a.c.lam_inv + (size_t)h * kHeadDim + 64 * hf + 16 * q + 4 * (lane & 3)));
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const uint4 w = raw[x][q];
+        const uint32_t u0 = hf ? w.z : w.x, u1 = hf ? w.w : w.y;
+        const float4 k = a.f32 ? make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w))
+                               : make_float4(__uint_as_float(u0 << 16), __uint_as_float(u0 & 0xffff0000u),
+                                             __uint_as_float(u1 << 16), __uint_as_float(u1 & 0xffff0000u));
         r[4 * q + 2 * x] = sat_h2(scale * k.x * l.x, scale * k.z * l.z);
         r[4 * q + 2 * x + 1] = sat_h2(scale * k.y * l.y, scale * k.w * l.w);
       }
     }
     tc_st_16x256_x4(taddr + 32 * hf, r);
   }
-}
+};
 // Drafted Values of a group for this warp's channels (widen_values' layout), times g.
 __device__ __forceinline__ void draft_values(const TreePlan& p, int s, int j0, float scale, int w, int lane,
                                              uint32_t (&out)[2][4]) {
@@ -776,7 +799,7 @@ __device__ __forceinline__ void draft_seen(const TreePlan& p, uint32_t (*seen)[4
   const int b = s / a.c.kv_heads, j = (t - p.tp - p.tw) * kTile + 32 * w + lane;
   const int r0 = block * p.block_rows, r1 = min(p.rows, r0 + p.block_rows);
   const unsigned char* m = a.mask ? a.mask + b * a.mask_b + j : nullptr;
-  constexpr int kBatch = 8;  // mask bytes in flight
+  constexpr int kBatch = 16;  // mask bytes in flight
   for (int n0 = r0 / a.group; n0 * a.group < r1; n0 += kBatch) {
     bool see[kBatch];
 #pragma unroll
@@ -862,12 +885,28 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
           const WindowGroup wg = window_group(p, wk.s, t, tl >> 4);
           if (wg.meta) key_terms(wg.meta[2 * (tl & 15)], 32768.0f / 65535.0f, rk, centre);
         } else {
-          const int j0 = (t - p.tp - p.tw) * kTile + 32 * w;
+          const int j0 = (t - p.tp - p.tw) * kTile + 32 * w, sb_ = wk.s / c.kv_heads, sh = wk.s - sb_ * c.kv_heads;
+          if (c.lam_inv && lane < 4) asm volatile("prefetch.global.L1 [%0];" ::"l"(c.lam_inv + (size_t)sh * kHeadDim + 32 * lane));
+          bool told = part != 0;
 #pragma unroll 1
-          for (int i = i0; i < i0 + kKeys; i++)
-            if (j0 + 16 * i < p.a.n)
-              draft_keys(p, wk.s, j0 + 16 * i, value_scale<BITS>(), tk + ((uint32_t)(16 * i) << 16), lane);
-          if (part == 0) draft_seen(p, sm.seen[ct & 3], wk.s, wk.block, t, w, lane);
+          for (int i = i0; i < i0 + kKeys || !told; i++) {
+            const bool any = i < i0 + kKeys && j0 + 16 * i < p.a.n;
+            const int passes = p.a.f32 ? 2 : 1;
+#pragma unroll 1
+            for (int ps = 0; ps < passes; ps++) {
+              DraftKeys dk;
+              if (any) dk.load(p.a, sb_, sh, j0 + 16 * i, ps, lane);
+              if (!told) {
+                draft_seen(p, sm.seen[ct & 3], wk.s, wk.block, t, w, lane);
+                told = true;
+              }
+              if (any) {
+                const uint32_t ti = tk + ((uint32_t)(16 * i) << 16);
+                dk.store(p.a, sh, ps, value_scale<BITS>(), ti, lane);
+                if (passes == 1) dk.store(p.a, sh, 1, value_scale<BITS>(), ti, lane);
+              }
+            }
+          }
           rk = 1.0f / value_scale<BITS>();
         }
         sm.rk[ct & 3][tl] = rk;
@@ -1267,7 +1306,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
     }
     const bool whole = wk.t0 == 0 && wk.t1 == p.tiles;
     // this CTA's records: 0 for the segment its share begins in, else 1
-    const int xi = wk.s * p.blocks + wk.block, begin = cta_begin(p.units, p.grid, blockIdx.x);
+    const int xi = wk.s * p.blocks + wk.block, begin = cta_begin(p, blockIdx.x);
     float* rec = p.parts + ((size_t)blockIdx.x * 2 + (xi * p.tiles + wk.t0 == begin ? 0 : 1)) * p.rec;
     const int rr = (DUAL ? half * kHalfRows : 0) + cb;  // first row within the block
     // C rows of bf16 leave from shared memory, 16 bytes a thread
@@ -1414,7 +1453,7 @@ __global__ void __launch_bounds__(Split<COLS>::kThreads, 1) tree_kernel(const __
   __syncthreads();
   tc_after();
   pdl_wait();  // the cache, q, k, v and the mask may be written by earlier kernels
-  const Walk wk{cta_begin(p.units, p.grid, blockIdx.x), cta_begin(p.units, p.grid, blockIdx.x + 1), 0, 0, 0, 0};
+  const Walk wk{cta_begin(p, blockIdx.x), cta_begin(p, blockIdx.x + 1), 0, 0, 0, 0};
   if (warp < kWiden0) {
     regs_up<S::kSoftRegs>();
     softmax_role<BITS, COLS, DUAL>(p, sm, sb, base, wk, warp >> 2, threadIdx.x & 127);

@@ -1082,8 +1082,7 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
 }
 
 // Sum or maximum over the warp's lanes of N values a lane: every exchange halves
-// the values a lane carries.  N >= 32: lane L ends with values 0 .. N/32 - 1 of
-// columns L N/32 ...; N = 16: with column L / 2.
+// the values a lane carries.  Lane L ends, in v[0], with column L N / 32 (N <= 32).
 template <int N, bool MAX>
 __device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
   auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
@@ -1138,42 +1137,45 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
     for (int i = 0; i < C / 2; i++) l2[i] = make_float2(0.f, 0.f);
     if (mine > 0) {
       // ---- q' = q lambda sm_scale log2(e) as fp16, K-major, channels of a quad in the order 0, 2, 1, 3 ----
-      const float4 lam = a.c.lam ? __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane)
-                                 : make_float4(1.f, 1.f, 1.f, 1.f);
+      // (Few instructions matter here more than anything: they run once a segment,
+      // from cold instruction memory.)
+      float4 lam = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (a.c.lam) lam = __ldg(reinterpret_cast<const float4*>(a.c.lam + (size_t)j * kHeadDim) + lane);
+      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + (long long)(j * a.group) * a.q_h + 4 * lane;
+      int node = (r0 + w) / a.group, g = r0 + w - node * a.group;
       uint2 raw[C / 4];
 #pragma unroll
-      for (int i = 0; i < C / 4; i++) {
-        const int r = w + 4 * i;
+      for (int i = 0; i < C / 4; i++) {  // rows w, w + 4, ...
         raw[i] = make_uint2(0u, 0u);
-        if (r < nr) {
-          const int row = r0 + r, node = row / a.group, g = row - node * a.group;
-          raw[i] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + node * a.q_t +
-                                                   (long long)(j * a.group + g) * a.q_h + 4 * lane);
+        if (w + 4 * i < nr) raw[i] = *reinterpret_cast<const uint2*>(qp + node * a.q_t + g * a.q_h);
+        g += 4;
+        while (g >= a.group) {
+          g -= a.group;
+          node++;
         }
       }
+      lam.x *= a.qscale; lam.y *= a.qscale; lam.z *= a.qscale; lam.w *= a.qscale;
+      uint8_t* qs = q_smem + (lane >> 4) * (kQBytes / 2) + 8 * (lane & 1);
+      float sum[C / 4];  // of the rounded q', as the products see it
 #pragma unroll
       for (int i = 0; i < C / 4; i++) {
         const int rs = cb + w + 4 * i;  // row of the half's Q
-        const float x0 = __uint_as_float(raw[i].x << 16) * a.qscale * lam.x;
-        const float x1 = __uint_as_float(raw[i].x & 0xffff0000u) * a.qscale * lam.y;
-        const float x2 = __uint_as_float(raw[i].y << 16) * a.qscale * lam.z;
-        const float x3 = __uint_as_float(raw[i].y & 0xffff0000u) * a.qscale * lam.w;
-        const uint32_t h02 = sat_h2(x0, x2), h13 = sat_h2(x1, x3);
+        const uint32_t h02 = sat_h2(__uint_as_float(raw[i].x << 16) * lam.x, __uint_as_float(raw[i].y << 16) * lam.z);
+        const uint32_t h13 = sat_h2(__uint_as_float(raw[i].x & 0xffff0000u) * lam.y, __uint_as_float(raw[i].y & 0xffff0000u) * lam.w);
         const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02));
         const float2 f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
-        float sum = (f02.x + f02.y) + (f13.x + f13.y);  // of the rounded q', as the products see it
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int chunk = (lane & 15) >> 1;
-        *reinterpret_cast<uint2*>(q_smem + (lane >> 4) * (kQBytes / 2) + rs * 128 + ((chunk ^ (rs & 7)) << 4) + 8 * (lane & 1)) =
-            make_uint2(h02, h13);
-        if (lane == 0) {
-          const float sc = fminf(fmaxf(sum * (1.0f / kSumScale), -65504.f), 65504.f);
-          const float hi = __half2float(__float2half_rn(sc));
-          *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs)) = make_uint4(pack_h2(hi, sc - hi), pack_h2(hi, 0.f), 0u, 0u);
-          *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs) + 128) = make_uint4(0u, 0u, 0u, 0u);
-          sm.neg[half][rs] = kUnset;  // no maximum yet
-        }
+        sum[i] = (f02.x + f02.y) + (f13.x + f13.y);
+        *reinterpret_cast<uint2*>(qs + rs * 128 + ((((lane & 15) >> 1) ^ (rs & 7)) << 4)) = make_uint2(h02, h13);
+      }
+      warp_columns<C / 4, false>(sum, lane);
+      constexpr int kSumLanes = 128 / C;  // lanes that end with the same row
+      if (lane % kSumLanes == 0) {
+        const int rs = cb + w + 4 * (lane / kSumLanes);
+        const float sc = fminf(fmaxf(sum[0] * (1.0f / kSumScale), -65504.f), 65504.f);
+        const float hi = __half2float(__float2half_rn(sc));
+        *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs)) = make_uint4(pack_h2(hi, sc - hi), pack_h2(hi, 0.f), 0u, 0u);
+        *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs) + 128) = make_uint4(0u, 0u, 0u, 0u);
+        sm.neg[half][rs] = kUnset;  // no maximum yet
       }
       fence_async_smem();
       __syncwarp();

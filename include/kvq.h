@@ -297,15 +297,21 @@ size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_node
  * sequence), or NULL: a chain, i sees j <= i (n_nodes = 1: one decode step
  * whose token is not yet appended).  A node that sees nothing in an empty
  * block gets zeros.  What a node does not see never reaches its output,
- * whatever it holds; drafted values beyond binary16's range and infinities
- * are read as +-65504, and q lambda sm_scale log2(e) likewise.
+ * whatever it holds (NaN and infinities included), and a node's own query
+ * reaches no other node's.  Drafted Keys (also over lambda) and Values should
+ * be within binary16's range (65,504); larger ones, infinities and NaN that a
+ * node does see count as some finite value of about that size or twice it.
+ * |q lambda sm_scale log2(e)| should be within that range per channel, too.
  * q: bf16 [batch][n_nodes][q_heads][128], k, v: dtype KVQ_DTYPE_*
  * [batch][n_nodes][kv_heads][128], all as kvq_rows with 16-byte aligned rows;
  * out: device bf16 [batch][n_nodes][q_heads][128], contiguous, 16-byte
  * aligned.  Scores and sums are fp32; products take operands rounded to
- * binary16 (the codes are exact at 8 bits and fewer).
+ * binary16 (codes of 8 bits and fewer are exact, and a Key's range and zero
+ * are applied in fp32, except with per-channel Key groups).
  * 1 <= n_nodes <= 1024; q_heads as in kvq_decode_attn.  workspace: as there,
- * kvq_tree_workspace(c, layer, q_heads, n_nodes) bytes, 16-byte aligned.
+ * kvq_tree_workspace(c, layer, q_heads, n_nodes) bytes, 16-byte aligned; it
+ * is all that calls share, so calls with workspaces of their own may overlap
+ * on the GPU.  A captured call replays over the tokens of its capture.
  * Errors: WORKSPACE, INVALID, CUDA. */
 kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads, int n_nodes, const kvq_rows* k,
                          const kvq_rows* v, int dtype, const unsigned char* mask, long long mask_stride_b,

@@ -199,7 +199,9 @@ struct kvq_cache {
   cudaError_t ensure_err(cudaStream_t s) {
     if (err_zeroed) return cudaSuccess;
     cudaError_t e = cudaMemsetAsync(pool, 0, 4, s);
-    if (e == cudaSuccess) err_zeroed = true;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
+    if (e == cudaSuccess && cap == cudaStreamCaptureStatusNone) err_zeroed = true;  // captured: it happens at the replay
     return e;
   }
 

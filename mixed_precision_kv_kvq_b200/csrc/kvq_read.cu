@@ -12,7 +12,11 @@
 // lane then holds channels of tokens g and g + 8 for Keys and Values alike and
 // needs two (R, Z) pairs.  The 16 rows go through the warp's own shared memory
 // (rows padded by 16 bytes: no bank conflicts) and leave as whole rows of
-// 16-byte stores.
+// 16-byte stores.  Measured on a B200 (copy peak 6.46 TB/s): 16 x 32768 tokens of
+// 4 heads from 2 bits to bf16 246 us, 4.98 TB/s (issue: ~1000 instructions a group,
+// half of the time); 8 x 9001 tokens of 8 heads from 4 bits to fp32 122 us, 5.48
+// TB/s.  Codes turned to floats by an OR and a subtraction instead of the
+// integer conversion took 266 us, ten CTAs an SM at fewer registers the same.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
   // row in flight a thread and eight CTAs an SM: two or four rows a thread cost
   // registers and so CTAs (a 1.2 GB bf16 call: 248 and 397 us against 214).
   constexpr int kPer = INTER ? V : 2 * V;  // channels per chunk
-  const int turned = a.rot_dim / kPer, chunks = turned + (kHeadDim - a.rot_dim + kPer - 1) / kPer;
+  const int turned = a.rot_dim / kPer, chunks = kHeadDim / kPer;  // kPer divides rot_dim (launch_t)
   const int heads = a.q.heads + a.k.heads, rows = nt * heads, step = kRopeThreads / chunks;
   const int ch = threadIdx.x % chunks;
   if ((int)threadIdx.x / chunks >= step) return;
@@ -68,7 +68,6 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
   const bool turn = ch < turned;
   const int c0 = turn ? ch * V : a.rot_dim + (ch - turned) * kPer;
   const int c1 = INTER ? c0 : turn ? c0 + half : c0 + V;
-  const bool two = !INTER && c1 < kHeadDim;  // a passing chunk may be one pack short
   for (int r = threadIdx.x / chunks; r < rows; r += step) {
     const int tt = r / heads, hh = r - tt * heads;
     const bool is_k = hh >= a.q.heads;
@@ -78,7 +77,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
     const T* src = static_cast<const T*>(x.in) + b * x.in_b + t * x.in_t + h * x.in_h;
     T* dst = static_cast<T*>(x.out) + b * x.out_b + t * x.out_t + h * x.out_h;
     Pack<V, T> y0 = *reinterpret_cast<const Pack<V, T>*>(src + c0), y1;
-    if (two) y1 = *reinterpret_cast<const Pack<V, T>*>(src + c1);
+    if constexpr (!INTER) y1 = *reinterpret_cast<const Pack<V, T>*>(src + c1);
     if (turn) {
       const float2* w = cs + tt * half;
       if constexpr (INTER) {
@@ -100,7 +99,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_cons
       }
     }
     *reinterpret_cast<Pack<V, T>*>(dst + c0) = y0;
-    if (two) *reinterpret_cast<Pack<V, T>*>(dst + c1) = y1;
+    if constexpr (!INTER) *reinterpret_cast<Pack<V, T>*>(dst + c1) = y1;
   }
 }
 

@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
   pdl_wait();
   pdl_launch_dependents();  // the decode launch waits for this kernel before it touches what it writes
   if (threadIdx.x == 0) t.counters[s] = 1;  // this partial's ticket
+  // Values beyond what the tree kernel's binary16 operands hold end there too.
+  auto limit = [](float x) { return fminf(fmaxf(x, -131008.f), 131008.f); };
   auto load4 = [&](const void* x, long long at, float (&y)[4], bool f32) {
     if (f32) {
       const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
       if (see) {
         float k[4];
         load4(a.k, b * a.k_b + i * a.k_t + j * a.k_h + 4 * lane, k, a.f32);
-        d = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
+        d = q[0] * limit(k[0]) + q[1] * limit(k[1]) + q[2] * limit(k[2]) + q[3] * limit(k[3]);
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
   float o[kN] = {};
   for (int i = 0; i < a.n; i++) {
     const long long at = b * a.v_b + i * a.v_t + j * a.v_h + threadIdx.x;
-    const float v = a.f32 ? static_cast<const float*>(a.v)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[at]);
+    const float v = limit(a.f32 ? static_cast<const float*>(a.v)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[at]));
 #pragma unroll
     for (int r = 0; r < kN; r++)
       if (r < R && sc[r][i] != 0.f) o[r] = fmaf(sc[r][i], v, o[r]);  // what a row does not see may be anything

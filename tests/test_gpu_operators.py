@@ -622,3 +622,79 @@ def test_draft_verify_commit_read(kvq, mode):
         step = (x.amax(-1) - x.amin(-1)) * 1.002 / (2 ** bits - 1)  # the range is rounded up to binary16
         worst = ((rk - k[:, path].float()).abs() / scale.cuda()).amax(-1)
         assert (worst <= 0.5 * step + 2.0 ** -20 * x.abs().amax(-1)).all()
+
+
+def test_first_calls_in_a_capture():
+    """A fresh process whose first calls of the operators are captured, on a cache that nothing has touched yet."""
+    code = r"""
+import torch
+import mixed_precision_kv_kvq_b200 as kvq
+torch.cuda.init()
+cache = kvq.KVQCache(1, 1, 2, 512 * 2 * 2 * (16 * 4 + 4), [4])
+q = torch.randn(1, 9, 8, 128, device="cuda").bfloat16()
+k, v = torch.randn(1, 9, 2, 128, device="cuda").bfloat16(), torch.randn(1, 9, 2, 128, device="cuda").bfloat16()
+pos = torch.arange(9, device="cuda")
+rope = kvq.Rope(128)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    a, b = kvq.kvq_rope(rope, pos, q, k)
+    out = cache.tree_attn(0, a, b, v)
+cache.device_status()
+graph.replay()
+torch.cuda.synchronize()
+cache.device_status()
+a2, b2 = kvq.kvq_rope(rope, pos, q, k)
+assert torch.equal(a, a2) and torch.equal(b, b2) and torch.equal(out, cache.tree_attn(0, a2, b2, v))
+assert torch.equal(out[:, 0], v[:, 0].repeat_interleave(4, 1))
+cache.append(0, b, v)
+graph2 = torch.cuda.CUDAGraph()
+rk = torch.empty_like(k)
+with torch.cuda.graph(graph2):
+    cache.read(0, 0, 9, k_out=rk)
+graph2.replay()
+torch.cuda.synchronize()
+assert torch.equal(rk, cache.read(0)[0])
+print("ok")
+"""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n,G", [(2, 2), (12, 4)])
+def test_tree_extremes_that_are_seen_stay_finite(kvq, n, G):
+    """Drafted values at and beyond binary16's range, and queries of a tiny and a huge row, in nodes that see them."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 1, 2, 200, 4, 512)
+    q, dk, dv = tree_inputs(37, 1, n, 2, G, F32)
+    dk[:, 0, :, :5] = torch.tensor([math.inf, -math.inf, 1e30, -1e30, math.nan], device="cuda")
+    dv[:, 0, :, :5] = torch.tensor([math.inf, -math.inf, 1e30, -1e30, math.nan], device="cuda")
+    q[:, 1] *= 1e-6
+    out = cache.tree_attn(0, q, dk, dv)
+    assert torch.isfinite(out).all()
+    # a node that sees the first one not at all is as if it were ordinary
+    mask = torch.ones(n, n, dtype=torch.bool).tril()
+    mask[1:, 0] = False
+    good_k, good_v = dk.clone(), dv.clone()
+    good_k[:, 0] = good_v[:, 0] = 0.5
+    tree_check(q[:, 1:], good_k[:, 1:], good_v[:, 1:], mask[1:, 1:], ks, vs, cache.tree_attn(0, q, dk, dv, mask.cuda())[:, 1:])
+
+
+@pytest.mark.parametrize("R,Z", [(0.0, 3.0), (1e-3, 8.0), (30.0, -15.0), (2.0, 60000.0)])
+def test_tree_keys_with_offsets(kvq, R, Z):
+    """Groups that are constant, nearly constant beside a large zero, or wide: the range's floor in the score's centre."""
+    B, H, T = 1, 1, 300
+    for fbit in (2, 8):
+        cache = kvq.KVQCache(1, B, H, 512 * B * H * 2 * (16 * fbit + 4), [fbit])
+        g = torch.Generator().manual_seed(1)
+        k = Z + R * torch.rand(B, T, H, 128, generator=g)
+        v = torch.randn(B, T, H, 128, generator=g)
+        cache.append(0, k.cuda(), v.cuda())
+        ks, vs = held(kvq, cache, "plain", B, H, T, None)
+        q, dk, dv = tree_inputs(3, B, 6, H, 3)
+        q *= 0.2 if abs(Z) < 100 else 1e-4
+        tree_check(q, dk, dv, None, ks, vs, cache.tree_attn(0, q, dk, dv))

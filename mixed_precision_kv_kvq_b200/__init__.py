@@ -203,7 +203,8 @@ class _On:
         elif isinstance(stream, torch.cuda.Stream):
             self.stream, self.ptr = stream, stream.cuda_stream
         else:
-            self.ptr = int(stream)  # a raw handle: torch's allocator knows nothing of it
+            self.ptr = int(stream)  # a raw handle; what the call allocates belongs to it, not to the current stream
+            self.stream = (torch.cuda.ExternalStream(self.ptr, device) if self.ptr else torch.cuda.default_stream(device))
 
     def __enter__(self):
         if self.guard is not None:

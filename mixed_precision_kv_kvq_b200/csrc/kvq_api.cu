@@ -1012,6 +1012,10 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
   a.tokens = (long long)batch * n_tokens;
   a.rot_dim = rot_dim;
   a.mag = magnitude;
+  // One token a CTA spreads few tokens over the SMs, four share a CTA's start and
+  // its wait for the angles (72 bf16 heads, 1 and 4 tokens a CTA: 256 tokens 6.2
+  // and 12.0 us, 2048 19.7 and 21.3, 4096 34.7 and 33.8, 32768 214 and 202; 3
+  // heads, 16384 tokens: 28.6 and 16.6; eight tokens a CTA: 206 and 15.5).
   a.tokens_per_cta = a.tokens >= 4096 ? 4 : 1;
   if (cudaError_t e = launch_rope(a, layout == KVQ_ROPE_INTERLEAVED, dtype == KVQ_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)))
     return cuda_fail(e, "rope launch");
@@ -1074,7 +1078,7 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   const int rows = n_nodes * G;
   // Few rows over a cache that holds tokens: the decode kernel reads it (one of
   // its eight query columns a row), with the drafted tokens as one more partial
-  // of each stream.  One node of 7 heads over 32K 4-bit tokens takes 58 us so and
+  // of each stream.  One node of 7 heads over 32K 4-bit tokens takes 59 us so and
   // 120 us through the tree kernel, whose tiles cost the same for 1 to 16 rows.
   if (rows <= kTreeNarrowRows && a.c.n_prog + a.c.n_win > 0) {
     const int n_streams = c->batch * c->kv_heads;

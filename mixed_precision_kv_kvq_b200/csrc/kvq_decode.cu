@@ -973,15 +973,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
 template <int BITS, bool CHAN, bool TREE>
 cudaError_t launch_bits(const DecodeArgs& a, cudaStream_t s) {
   constexpr int kBytes = kSmemBytes + (CHAN ? kChanSmem : 0);
-  static bool attr_set = false;  // per process and kernel; set before the first launch
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               (int)cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static DeviceOnce once;
+  if (cudaError_t e = once([] {
+        cudaError_t e = cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(decode_kernel<BITS, CHAN, TREE>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                       (int)cudaSharedmemCarveoutMaxShared);
+      }))
+    return e;
   const unsigned grid = (unsigned)(a.batch * a.kv_heads) * (unsigned)a.splits;
   return launch_pdl(decode_kernel<BITS, CHAN, TREE>, dim3(grid), dim3(kThreads), kBytes, s, a);
 }

@@ -46,6 +46,7 @@
 // per tile (F = the block's Fbit, the widest a tile ever gets).  A shrink
 // never touches meta.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -295,6 +296,22 @@ inline cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem,
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// Kernel attributes are a kernel's on one device: set them once per kernel and
+// device, before its first launch there.
+struct DeviceOnce {
+  std::atomic<unsigned long long> done{0};  // a bit per device; devices past 63 are set on every call
+  template <typename Set>
+  cudaError_t operator()(Set set) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaError_t e = set();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_block_move(const BlockMoveArgs& a, int n_streams, cudaStream_t s);

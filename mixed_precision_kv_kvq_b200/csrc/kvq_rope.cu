@@ -14,11 +14,15 @@
 // rounding to fp32) plus that function's own.
 //
 // The kernel is bound by HBM (each value read once and written once).  A CTA
-// takes up to kTokens tokens: its threads first form the tokens' cos and sin,
-// one pair each, in shared memory -- every head of a token shares them -- and
-// then walk the (token, head, chunk) items with 16-byte accesses (8 bytes an
-// access in the halves of bf16 heads whose rot_dim / 2 is not a multiple of 8
-// but of 4; single elements for any other rot_dim or alignment).
+// takes four tokens, or one where there are few (RopeArgs::tokens_per_cta): its
+// threads first form the tokens' cos and sin, one pair each, in shared memory --
+// every head of a token shares them -- and then walk the rows (token, head), a
+// thread always at the same chunk of the head, with 16-byte accesses (8 bytes
+// where rot_dim / 2 or the rows' alignment allows no more; single elements, or
+// pairs, for any other).  Measured on a B200 (copy peak 6.46 TB/s): 8 x 4096
+// tokens of 64 + 8 heads, bf16, 202 us, 5.98 TB/s; 3 x 1001 tokens of 40 + 8
+// heads, fp32, half of each head turned, 32 us, 4.60 TB/s; one token of 16
+// sequences, 28 + 4 heads, 2.9 us in a graph (launch latency).
 #include <cuda_bf16.h>
 
 #include "kvq_rope.cuh"

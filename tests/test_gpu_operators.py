@@ -698,3 +698,27 @@ def test_tree_keys_with_offsets(kvq, R, Z):
         q, dk, dv = tree_inputs(3, B, 6, H, 3)
         q *= 0.2 if abs(Z) < 100 else 1e-4
         tree_check(q, dk, dv, None, ks, vs, cache.tree_attn(0, q, dk, dv))
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (16, 4)])
+def test_raw_stream_handles_own_what_the_call_allocates(kvq, n, G):
+    """A stream given as its handle: the workspace and the output are not the current stream's to hand out meanwhile."""
+    cache, *_ = make_cache(kvq, "plain", 2, 2, 500, 4, 1024)
+    q, dk, dv = tree_inputs(21, 2, n, 2, G)
+    rope, pos = kvq.Rope(128), torch.arange(n, device="cuda")
+    want, turned, (rk, rv) = cache.tree_attn(0, q, dk, dv), kvq.kvq_rope(rope, pos, q, dk), cache.read(0)
+    nbytes = kvq.kvq_tree_workspace(cache.handle, 0, 2 * G, n)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    h = side.cuda_stream
+    out, got, back = cache.tree_attn(0, q, dk, dv, stream=h), kvq.kvq_rope(rope, pos, q, dk, stream=h), cache.read(0, stream=h)
+    junk = [torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda") for size in (nbytes, out.numel() * 2) for _ in range(4)]
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(got + back, turned + (rk, rv)))
+    assert all(bool((j == 0x7F).all()) for j in junk)
+    # the default stream's handle
+    assert torch.equal(cache.tree_attn(0, q, dk, dv, stream=torch.cuda.default_stream().cuda_stream), want)

@@ -171,21 +171,20 @@ def _rows(t: Optional[torch.Tensor]):
     return _ROWS(t.data_ptr(), b, n, h)
 
 
-def _is_rows(t: torch.Tensor, dtype, device) -> bool:
-    """A [batch][n][heads][128] CUDA tensor of this type and device whose channels are neighbours."""
-    return (t.dtype is dtype and t.device == device and t.dim() == 4 and t.shape[3] == HEAD_DIM
-            and (t.stride(3) == 1 or not t.numel()) and t.is_cuda)
-
-
-def _check_rows(name: str, t: torch.Tensor, dtype, shape=None, device=None) -> None:
-    if not _is_rows(t, dtype, t.device if device is None else device):
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-        raise ValueError(f"{name} must be a CUDA tensor [batch][n][heads][128] with neighbouring channels")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _take(name: str, t: torch.Tensor, dtype, device, shape=None):
+    """kvq_rows of a [batch][n][heads][128] CUDA tensor of this type and device whose channels are neighbours; these
+    calls last a few microseconds on the GPU, so what is checked is read once."""
+    s, x = t.stride(), t.shape
+    if t.dtype is dtype and t.device == device and len(x) == 4 and x[3] == HEAD_DIM and (s[3] == 1 or not t.numel()):
+        if shape is not None and x != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x)}")
+        if device.type == "cuda":
+            return _ROWS(t.data_ptr(), s[0], s[1], s[2])
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be a CUDA tensor [batch][n][heads][128] with neighbouring channels")
 
 
 class _On:
@@ -221,6 +220,13 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def like(self, t: torch.Tensor) -> torch.Tensor:
+        """The same, contiguous and shaped like t."""
+        if self.stream is None:
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
+        with torch.cuda.stream(self.stream):
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 _SCALINGS = {"none": KVQ_ROPE_NONE, "linear": KVQ_ROPE_LINEAR, "ntk": KVQ_ROPE_NTK, "yarn": KVQ_ROPE_YARN}
@@ -273,36 +279,39 @@ def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: 
     if first is None:
         raise ValueError("q and k are both None")
     dtype, dt, device = _dtype_code(first), first.dtype, first.device
-    _check_rows("q" if q is not None else "k", first, dt)
-    batch, n = first.shape[0], first.shape[1]
-    if q is not None and k is not None:
-        _check_rows("k", k, dt, device=device)
-        if k.shape[0] != batch or k.shape[1] != n:
-            raise ValueError(f"q and k must agree in batch and tokens, got {list(q.shape)} and {list(k.shape)}")
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if y is not None:
-            if x is None:
-                raise ValueError(f"{name}_out without {name}")
-            _check_rows(name + "_out", y, dt, x.shape, device)
-    pt = positions.dtype
+    qr = _take("q", q, dt, device) if q is not None else None
+    kr = _take("k", k, dt, device) if k is not None else None
+    batch, n = first.shape[:2]
+    if q is not None and k is not None and k.shape[:2] != (batch, n):
+        raise ValueError(f"q and k must agree in batch and tokens, got {list(q.shape)} and {list(k.shape)}")
+    if (q_out is not None and q is None) or (k_out is not None and k is None):
+        raise ValueError("an output without its input")
+    pt, shape = positions.dtype, positions.shape
     if (pt is not torch.int64 and pt is not torch.int32) or positions.device != device:
         raise ValueError("positions must be an int32 or int64 tensor on the device of q and k")
-    shape = positions.shape
-    if len(shape) == 2 and shape[0] == batch and shape[1] == n:
+    if shape == (batch, n):
         ps_b, ps_t = positions.stride()
-    elif len(shape) == 1 and shape[0] == n:
+    elif shape == (n,):
         ps_b, ps_t = 0, positions.stride(0)
     else:
         raise ValueError(f"positions must be [{batch}][{n}] or [{n}], got {list(shape)}")
+    qo = ko = None
     with _On(device, stream) as on:
-        if q is not None and q_out is None:
-            q_out = on.empty(q.shape, dt)
-        if k is not None and k_out is None:
-            k_out = on.empty(k.shape, dt)
+        if q is not None:
+            if q_out is None:
+                q_out = on.like(q)
+                qo = _rows(q_out)
+            else:
+                qo = _take("q_out", q_out, dt, device, q.shape)
+        if k is not None:
+            if k_out is None:
+                k_out = on.like(k)
+                ko = _rows(k_out)
+            else:
+                ko = _take("k_out", k_out, dt, device, k.shape)
         check(load().kvq_rope(rope.rot_dim, rope._code, rope._ptr, rope.magnitude, positions.data_ptr(),
                               KVQ_POS_I64 if pt is torch.int64 else KVQ_POS_I32, ps_b, ps_t, batch, n, dtype,
-                              _rows(q), _rows(q_out), q.shape[2] if q is not None else 0,
-                              _rows(k), _rows(k_out), k.shape[2] if k is not None else 0, on.ptr))
+                              qr, qo, q.shape[2] if q is not None else 0, kr, ko, k.shape[2] if k is not None else 0, on.ptr))
     return q_out, k_out
 
 
@@ -316,13 +325,12 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
     shaped like q."""
     dtype, dt, device = _dtype_code(k), k.dtype, q.device
-    _check_rows("q", q, torch.bfloat16)
+    qr, kr = _take("q", q, torch.bfloat16, device), _take("k", k, dt, device)
+    vr = _take("v", v, dt, device, k.shape)
+    _take("out", out, torch.bfloat16, device, q.shape)
     b, n, q_heads, _ = q.shape
-    _check_rows("k", k, dt, device=device)
-    if k.shape[0] != b or k.shape[1] != n:
+    if k.shape[:2] != (b, n):
         raise ValueError(f"k must be [{b}][{n}][kv_heads][128], got {list(k.shape)}")
-    _check_rows("v", v, dt, k.shape, device)
-    _check_rows("out", out, torch.bfloat16, q.shape, device)
     if not out.is_contiguous() or workspace.device != device:
         raise ValueError("out must be contiguous and workspace on its device")
     mask_ptr, mask_b = None, 0
@@ -330,12 +338,12 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
         mt, ms = mask.dtype, mask.shape
         if (mt is not torch.bool and mt is not torch.uint8) or mask.device != device or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous bool or uint8 tensor on the device of q")
-        if len(ms) == 3 and ms[0] == b and ms[1] == n and ms[2] == n:
+        if ms == (b, n, n):
             mask_b = n * n
-        elif len(ms) != 2 or ms[0] != n or ms[1] != n:
+        elif ms != (n, n):
             raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(ms)}")
         mask_ptr = mask.data_ptr()
-    check(load().kvq_tree_attn(cache, layer, _rows(q), q_heads, n, _rows(k), _rows(v), dtype, mask_ptr, mask_b, sm_scale,
+    check(load().kvq_tree_attn(cache, layer, qr, q_heads, n, kr, vr, dtype, mask_ptr, mask_b, sm_scale,
                                out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                stream if type(stream) is int else _stream_ptr(stream)))
 
@@ -347,13 +355,12 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
     first = k_out if k_out is not None else v_out
     if first is None:
         raise ValueError("k_out and v_out are both None")
-    dtype, dt = _dtype_code(first), first.dtype
-    _check_rows("k_out" if first is k_out else "v_out", first, dt)
-    if k_out is not None and v_out is not None:
-        _check_rows("v_out", v_out, dt, k_out.shape, k_out.device)
+    dtype, dt, device = _dtype_code(first), first.dtype, first.device
+    kr = _take("k_out", k_out, dt, device) if k_out is not None else None
+    vr = _take("v_out", v_out, dt, device, first.shape) if v_out is not None else None
     if first.shape[1] != count:
         raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
-    check(load().kvq_read(cache, layer, start, count, dtype, _rows(k_out), _rows(v_out),
+    check(load().kvq_read(cache, layer, start, count, dtype, kr, vr,
                           stream if type(stream) is int else _stream_ptr(stream)))
 
 
@@ -536,7 +543,7 @@ class KVQCache:
                 if nbytes:
                     self._tree_ws[size] = nbytes
             if out is None:
-                out = on.empty(q.shape, torch.bfloat16)
+                out = on.like(q)
             kvq_tree_attn(self.handle, layer, q, k, v, mask, HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out,
                           on.empty((nbytes,), torch.uint8), on.ptr)
         return out
@@ -554,7 +561,8 @@ class KVQCache:
         with _On(device, stream) as on:
             if k_out is None and v_out is None:
                 shape = (self.batch, count, self.kv_heads, HEAD_DIM)
-                k_out, v_out = on.empty(shape, dtype), on.empty(shape, dtype)
+                k_out = on.empty(shape, dtype)
+                v_out = on.like(k_out)
             else:
                 for name, x in (("k_out", k_out), ("v_out", v_out)):
                     if x is not None:

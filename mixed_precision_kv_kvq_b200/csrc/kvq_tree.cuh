@@ -64,13 +64,16 @@
 // tree_merge_kernel joins.
 //
 // Measured on a B200 (graph replay, inputs larger than L2): 16 nodes of 7 heads
-// over 16 x 32768 2-bit tokens of 4 heads 218 us, 552 TFLOP/s; 63 nodes of 8 heads
-// over 8 x 16383 8-bit tokens of 8 heads 458 us, 594 TFLOP/s; 5 nodes of 5 heads
+// over 16 x 32768 2-bit tokens of 4 heads 207 us, 580 TFLOP/s; 63 nodes of 8 heads
+// over 8 x 16383 8-bit tokens of 8 heads 429 us, 633 TFLOP/s; 5 nodes of 5 heads
 // over 4 x 4999 16-bit tokens of 8 heads 52 us, 1.6 TB/s; one tile a CTA 14 us
 // (query set-up, cold instructions, the drafted tile's scattered loads).
-// A 128 x 128 tile takes ~3300 cycles, against ~1330 of MMA issue and 1024 of
-// ex2 at 16 an SM and cycle: what bounds it is the chain widen -> S -> softmax ->
-// P -> O of few, large steps with their waits, and instruction fetch, not a pipe.
+// A 128 x 128 tile takes ~2700 cycles, against ~1300 of MMA and 1024 of ex2 at
+// 16 an SM and cycle.  A half's loop is its score product (~1800 cycles from its
+// issue until it is in, the other half's products between), 220 until it is in
+// registers and S is free, and ~500 until the next is issued; S is single, as
+// tensor memory is full.  (S held until the maxima were agreed on: 220 and 456
+// us.)  Widening hides behind it: without any, 16 nodes took 208 us of 220.
 // At 16 bits a tile is 64 KiB and two ring stages are what fits.  Every wait is bounded: a wait that gives up raises
 // the cache's error flag and the CTA's abort flag, after which all waits return
 // at once and the loops run out.
@@ -125,7 +128,9 @@ constexpr int kMaxStages = 8;
 constexpr int kHalfRows = 64;        // rows of a half's operands in shared memory
 constexpr int kQBytes = kHalfRows * kHeadDim * 2;  // one half's Q: two 64-channel slabs of [64][128 B]
 constexpr int kPBytes = kTile * 128;               // one half's P: [128 tokens][64 rows] fp16
-constexpr float kUnset = 1e30f;      // -m of a row with no token yet
+// -m of a row with no token yet (0 - m is never -0)
+constexpr uint32_t kUnsetBits = 0x80000000u;
+__device__ __forceinline__ bool unset(float neg) { return __float_as_uint(neg) == kUnsetBits; }
 
 // How the warps are divided, the registers of each kind (setmaxnreg from what the
 // launch gives) and tensor memory's columns.  With 64 rows a half (128 rows a
@@ -157,8 +162,9 @@ constexpr float kCentreMax = 4000.0f;
 
 struct Small {
   float rk[4][kTile];                // of the tokens of tile t, ring of 4
-  float neg[2][kHalfRows];           // per half: -m (kUnset: no token yet)
+  float neg[2][kHalfRows];           // per half: -m
   float alpha[2][kHalfRows];         // factor of the last rescaling
+  float shift[2][kHalfRows];         // what it added to -m
   float red[2][4][kHalfRows];        // per warp: column maxima, then row sums
   float2 ml[2][kHalfRows];           // final (m, l)
   uint32_t seen[4][kTile][4];        // drafted tile t: bit i of word w: the row sees token 32 w + i
@@ -317,8 +323,15 @@ __device__ __forceinline__ void tc_st_16x128_x4(uint32_t t, const uint32_t (&r)[
 }
 template <int N>
 __device__ __forceinline__ void tc_ld(uint32_t (&r)[N], uint32_t t) {
-  static_assert(N == 16 || N == 32);
-  if constexpr (N == 32)
+  static_assert(N == 8 || N == 16 || N == 32);
+  if constexpr (N == 8)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : KVQ_W4(r, 0), KVQ_W4(r, 4)
+        : "r"(t)
+        : "memory");
+  else if constexpr (N == 32)
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
@@ -334,20 +347,9 @@ __device__ __forceinline__ void tc_ld(uint32_t (&r)[N], uint32_t t) {
         : "r"(t)
         : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tc_st(uint32_t t, const uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32);
-  if constexpr (N == 32)
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_R16(r, 0),
-        KVQ_R16(r, 16), "r"(t)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16(r, 0),
-        "r"(t)
-        : "memory");
+__device__ __forceinline__ void tc_st(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KVQ_R4(r, 0), KVQ_R4(r, 4), "r"(t)
+               : "memory");
 }
 // Where a group lies: a stage of the ring (shared memory) or the window's
 // tiles (global memory).
@@ -834,7 +836,7 @@ __device__ __forceinline__ void key_terms(uint32_t m, float half_codes, float& r
   const float r = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * half_codes;
   const float z = __half2float(__ushort_as_half((unsigned short)(m >> 16)));
   rk = fmaxf(r, fabsf(z) * (1.0f / (kCentreMax - 1.0f)));
-  const float a = rk > 0.f ? (z + rk) / rk * kSumScale : 0.f;
+  const float a = rk > 0.f ? __fdividef(z + rk, rk) * kSumScale : 0.f;  // 2 ulp, as fine as the pair
   const float hi = __half2float(__float2half_rn(a));
   centre = make_uint2(pack_h2(hi, hi), pack_h2(a - hi, 0.f));
 }
@@ -1185,7 +1187,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
         const float hi = __half2float(__float2half_rn(sc));
         *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs)) = make_uint4(pack_h2(hi, sc - hi), pack_h2(hi, 0.f), 0u, 0u);
         *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs) + 128) = make_uint4(0u, 0u, 0u, 0u);
-        sm.neg[half][rs] = kUnset;  // no maximum yet
+        sm.neg[half][rs] = __uint_as_float(kUnsetBits);
       }
       fence_async_smem();
       __syncwarp();
@@ -1208,74 +1210,84 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
       }
       const float rk = sm.rk[ct & 3][tl];
       float2 x[C / 2];
-      auto scores = [&]() {  // less the running maxima (a row that has none: relative to -kUnset)
+      {  // scores less the running maxima (of a row that has none: as they are)
         uint32_t d[C];
         tc_ld(d, ts);
+        tc_before();  // S is in registers: the next tile's product may start
+        __syncwarp();
+        if (lane == 0) mbar_arrive(KVQ_BAR(s_free, half));
 #pragma unroll
         for (int i = 0; i < C; i += 4) {
           const float4 neg = *reinterpret_cast<const float4*>(&sm.neg[half][cb + i]);
           x[i / 2] = fma2(splat2(rk), make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), make_float2(neg.x, neg.y));
           x[i / 2 + 1] = fma2(splat2(rk), make_float2(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), make_float2(neg.z, neg.w));
         }
-        if (hide) {
+      }
+      if (hide) {
 #pragma unroll
-          for (int i = 0; i < C / 2; i++) {
-            if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
-            if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
-          }
+        for (int i = 0; i < C / 2; i++) {
+          if (hide >> (2 * i) & 1u) x[i].x = -INFINITY;
+          if (hide >> (2 * i + 1) & 1u) x[i].y = -INFINITY;
         }
-      };
-      scores();
+      }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < C / 2; i++) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(x[i].x, x[i].y));
-      if (bar_or(id, 128, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
-        // Column maxima from the scores themselves: a row's first ones were taken
-        // against no maximum.
-        {
-          uint32_t d[C];
-          float v[C];
-          tc_ld(d, ts);
+      // Every row sees some token of a cached tile, so only the first tile and the
+      // drafted ones meet rows without a maximum.
+      const bool some_unset = done == 0 || t >= p.tp + p.tw;
+      if (bar_or(id, 128, some_unset || fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRebase)) {
 #pragma unroll
-          for (int i = 0; i < C; i++) v[i] = (hide >> i & 1u) ? -INFINITY : rk * __uint_as_float(d[i]);
-          warp_columns<C, true>(v, lane);
-          sm.red[half][w][cb + (C == 32 ? lane : lane >> 1)] = v[0];
+        for (int c0 = 0; c0 < C; c0 += 8) {  // column maxima, of the scores themselves; eight columns are what registers hold
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float2 neg = *reinterpret_cast<const float2*>(&sm.neg[half][cb + c0 + i]);
+            v[i] = x[(c0 + i) / 2].x - neg.x;
+            v[i + 1] = x[(c0 + i) / 2].y - neg.y;
+          }
+          warp_columns<8, true>(v, lane);
+          if ((lane & 3) == 0) sm.red[half][w][cb + c0 + (lane >> 2)] = v[0];
         }
         bar_sync(id, 128);
         if (tl < C) {
           const int c = cb + tl;
           const float old = sm.neg[half][c];
           float m = fmaxf(fmaxf(sm.red[half][0][c], sm.red[half][1][c]), fmaxf(sm.red[half][2][c], sm.red[half][3][c]));
-          float f = 0.f;
-          if (old != kUnset) {
+          float f = 0.f, shift = 0.f;
+          if (!unset(old)) {
             m = fmaxf(m, -old);
             f = ex2(-old - m);
           }
+          if (m > -INFINITY) {  // a row that has seen nothing stays unset
+            const float neg = 0.f - m;
+            shift = neg - old;
+            sm.neg[half][c] = neg;
+          }
           sm.alpha[half][c] = f;
-          if (m > -INFINITY) sm.neg[half][c] = -m;  // a row that has seen nothing stays unset
+          sm.shift[half][c] = shift;
         }
         bar_sync(id, 128);
-        if (done > 0) {  // O so far, once the last product is in
+        if (done > 0) {  // O so far, once the last product is in; eight columns at a time (sixteen spilled: 209 -> 207 us)
           const float2* al = reinterpret_cast<const float2*>(sm.alpha[half] + cb);
           wait_pv(n - 1);
           tc_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            uint32_t o[16];
+          for (int c0 = 0; c0 < C; c0 += 8) {
+            uint32_t o[8];
             tc_ld(o, to + c0);
 #pragma unroll
-            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.alpha[half][cb + c0 + i]);
+            for (int i = 0; i < 8; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.alpha[half][cb + c0 + i]);
             tc_st(to + c0, o);
           }
 #pragma unroll
           for (int i = 0; i < C / 2; i++) l2[i] = mul2(l2[i], al[i]);
           tc_wait_st();
         }
-        scores();
+        const float2* sh = reinterpret_cast<const float2*>(sm.shift[half] + cb);
+#pragma unroll
+        for (int i = 0; i < C / 2; i++) x[i] = add2(x[i], sh[i]);
       }
-      tc_before();  // S is in registers: the next tile's product may start
-      __syncwarp();
-      if (lane == 0) mbar_arrive(KVQ_BAR(s_free, half));
       if (done > 0) wait_pv(n - 1);  // P is free again
       uint8_t* p_at = p_smem + tl * 128;
 #pragma unroll
@@ -1309,8 +1321,9 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
     if (tl < C) {
       const float* r = &sm.red[half][0][cb + tl];
       const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
-      const float neg = mine > 0 ? sm.neg[half][cb + tl] : kUnset;
-      sm.ml[half][cb + tl] = make_float2(neg == kUnset ? -INFINITY : -neg, neg == kUnset ? 0.f : l);
+      const float neg = sm.neg[half][cb + tl];
+      const bool any = mine > 0 && !unset(neg);
+      sm.ml[half][cb + tl] = make_float2(any ? -neg : -INFINITY, any ? l : 0.f);
     }
     if (mine > 0) {
       wait_pv(n - 1);

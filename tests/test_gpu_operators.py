@@ -722,3 +722,28 @@ def test_raw_stream_handles_own_what_the_call_allocates(kvq, n, G):
     assert all(bool((j == 0x7F).all()) for j in junk)
     # the default stream's handle
     assert torch.equal(cache.tree_attn(0, q, dk, dv, stream=torch.cuda.default_stream().cuda_stream), want)
+
+
+@pytest.mark.parametrize("T", [0, 130])
+@pytest.mark.parametrize("n,G", [(300, 2), (60, 1), (30, 1), (12, 1)])
+def test_tree_low_scores_seen_late(kvq, T, n, G):
+    """Scores far below zero (2^-60 against no maximum), some rows' first tokens in the last drafted tile, one row's nowhere."""
+    B, H = 1, 2
+    cache = kvq.KVQCache(1, B, H, 512 * B * H * 2 * (16 * 8 + 4), [8])
+    g = torch.Generator().manual_seed(3)
+    k, v = 0.1 * torch.randn(B, max(T, 1), H, 128, generator=g), torch.randn(B, max(T, 1), H, 128, generator=g)
+    k[..., 0] = -22.0
+    if T:
+        cache.append(0, k.cuda(), v.cuda())
+    ks, vs = held(kvq, cache, "plain", B, H, T, None)
+    q, dk, dv = tree_inputs(5, B, n, H, G)
+    q *= 0.1
+    dk *= 0.1
+    q[..., 0] = 22.0
+    dk[..., 0] = -22.0
+    late = 128 if n > 128 else n // 2
+    mask = torch.ones(n, n, dtype=torch.bool)
+    mask[::2, :late] = False
+    mask[1::4, late:] = False
+    mask[5] = False
+    tree_check(q, dk, dv, mask, ks, vs, cache.tree_attn(0, q, dk, dv, mask.cuda()))

@@ -258,11 +258,18 @@ class Rope:
         self.rot_dim, self.layout = int(rot_dim), layout
         if inv_freq is None:
             inv_freq, magnitude = kvq_rope_freqs(self.rot_dim, theta, _SCALINGS[scaling], factor, original_tokens)
-        self.inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
-        if self.inv_freq.shape != (self.rot_dim // 2,):
+        inv_freq = np.array(inv_freq, dtype=np.float64)  # a copy: the schedule does not change under its user
+        if inv_freq.shape != (self.rot_dim // 2,):
             raise ValueError(f"inv_freq must hold rot_dim / 2 = {self.rot_dim // 2} values")
-        self.magnitude = float(magnitude)
-        self._code = _LAYOUTS[layout]
+        self.__setstate__({"rot_dim": self.rot_dim, "layout": layout, "inv_freq": inv_freq, "magnitude": float(magnitude)})
+
+    def __getstate__(self):
+        return {"rot_dim": self.rot_dim, "layout": self.layout, "inv_freq": self.inv_freq, "magnitude": self.magnitude}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.inv_freq.flags.writeable = False
+        self._code = _LAYOUTS[self.layout]
         self._ptr = self.inv_freq.ctypes.data_as(C.c_void_p)
 
 
@@ -274,7 +281,8 @@ def kvq_rope(rope: Rope, positions: torch.Tensor, q: Optional[torch.Tensor], k: 
     neighbouring channels (slices of a fused projection are read in place).
     positions: device int32 or int64, [batch][n], or [n] for every sequence.
     q_out, k_out: outputs shaped like q and k (an input itself: in place);
-    allocated contiguous by default.  -> (q_out, k_out)."""
+    allocated contiguous by default.  -> (q_out, k_out), which carry no
+    gradient (as everything here: the path is inference)."""
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")

@@ -184,3 +184,20 @@ def test_python_refusals_before_any_launch(kvq):
         kvq.kvq_rope(rope, pos, x)          # not on a GPU
     with pytest.raises(TypeError):
         kvq.kvq_rope(rope, pos, x.half())   # a type the cache does not take
+
+
+def test_rope_schedule_is_its_own(kvq):
+    """A schedule keeps what it was made with, and copies and pickles as any other object."""
+    import copy
+    import pickle
+
+    w = np.linspace(1.0, 0.1, 32)
+    rope = kvq.Rope(64, layout="interleaved", inv_freq=w, magnitude=1.25)
+    w[:] = 7.0
+    assert rope.inv_freq[0] == 1.0
+    with pytest.raises(ValueError):
+        rope.inv_freq[0] = 2.0
+    for other in (copy.copy(rope), copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+        assert (other.rot_dim, other.layout, other.magnitude) == (64, "interleaved", 1.25)
+        assert np.array_equal(other.inv_freq, rope.inv_freq)
+        assert other._ptr.value == other.inv_freq.ctypes.data and other._code == rope._code

@@ -10,6 +10,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -52,6 +54,19 @@ struct Range {
   Range(const Range&) = delete;
   Range& operator=(const Range&) = delete;
 };
+
+// A value of the error word that no other cache of the process has: successive
+// numbers from an arbitrary start, spread over the word by multiplicative
+// hashing (an odd factor near 2^32 / golden ratio, so distinct numbers stay
+// distinct): neither an earlier cache's code in the same memory nor other data in
+// a pool that was never cleared reads as an error.  Zero is no code.
+int new_err_code() {
+  static std::atomic<unsigned> next{(unsigned)std::chrono::steady_clock::now().time_since_epoch().count()};
+  unsigned x;
+  do x = next.fetch_add(1, std::memory_order_relaxed) * 2654435761u;
+  while (x == 0);
+  return (int)x;
+}
 
 // Host-side fault injection: with KVQ_FAULT_ALLOC set to anything but "" or
 // "0", the library's own device allocation reports failure without calling
@@ -136,7 +151,7 @@ bool make_plan(int layers, int batch, int kv_heads, int head_dim, size_t budget,
   }
   p.n_f = n_f;
   p.layers.assign(layers, LayerState{});
-  size_t off = kAlign;  // [0, 256): device error flag
+  size_t off = kAlign;  // [0, 256): device error word
   const size_t n_streams = (size_t)batch * kv_heads;
   for (int l = 0; l < layers; l++) {
     LayerState& L = p.layers[l];
@@ -191,19 +206,8 @@ struct kvq_cache {
   size_t pool_bytes;
   bool owns_pool;
   int num_sms;
-  bool err_zeroed;
+  int err_code;  // this cache's value of its error word (ErrWord)
   std::vector<LayerState> L;
-
-  // The error flag lives in the pool; clear it once, stream-ordered, before
-  // the first kernel of this cache can set it.
-  cudaError_t ensure_err(cudaStream_t s) {
-    if (err_zeroed) return cudaSuccess;
-    cudaError_t e = cudaMemsetAsync(pool, 0, 4, s);
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (e == cudaSuccess) e = cudaStreamIsCapturing(s, &cap);
-    if (e == cudaSuccess && cap == cudaStreamCaptureStatusNone) err_zeroed = true;  // captured: it happens at the replay
-    return e;
-  }
 
   int sms() {
     if (num_sms <= 0) {
@@ -227,7 +231,7 @@ struct kvq_cache {
   float* lam(int l) { return reinterpret_cast<float*>(pool + L[l].off_lam); }
   float* lam_inv(int l) { return reinterpret_cast<float*>(pool + L[l].off_lam_inv); }
   int* counters(int l) { return reinterpret_cast<int*>(pool + L[l].off_counters); }
-  int* err() { return reinterpret_cast<int*>(pool); }
+  ErrWord err() { return ErrWord{reinterpret_cast<int*>(pool), err_code}; }
 };
 
 namespace {
@@ -556,7 +560,7 @@ kvq_status kvq_alloc_ex(kvq_cache** out, int layers, int batch, int kv_heads, in
   c->n_f = p.n_f;
   c->L = p.layers;
   c->num_sms = 0;
-  c->err_zeroed = false;
+  c->err_code = new_err_code();
   if (dev_pool) {
     c->pool = static_cast<uint8_t*>(dev_pool);
     c->owns_pool = false;
@@ -620,7 +624,6 @@ kvq_status kvq_append(kvq_cache* c, int layer, const void* k, const void* v, int
       return fail(KVQ_ERR_BUDGET, "layer %d holds %lld tokens (%lld staged); %d more complete blocks that do not fit at "
                   "Fbit %d", layer, L.n_all, L.n_all - L.n, n_tokens, L.fbit);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
     return append_chan(c, layer, k, v, dtype, n_tokens, s);
   }
   if (!L.window && L.n + n_tokens > c->n_f)
@@ -630,7 +633,6 @@ kvq_status kvq_append(kvq_cache* c, int layer, const void* k, const void* v, int
     return fail(KVQ_ERR_BUDGET, "layer %d holds %lld tokens (%lld in the window); %d more do not fit at Fbit %d", layer,
                 L.n_all, std::min(L.n_all, W1), n_tokens, L.fbit);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   int off = 0;
   while (off < n_tokens) {
     const long long cap = capacity(L, c->n_f, L.bits);
@@ -748,7 +750,6 @@ kvq_status kvq_decode_attn(kvq_cache* c, int layer, const void* q, int q_heads, 
   if (!workspace || ws_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace ? ws_bytes : (size_t)0, need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   if (!L.counters_zeroed) {
     cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
     if (e != cudaSuccess) return cuda_fail(e, "counter reset");
@@ -789,7 +790,6 @@ kvq_status kvq_append_decode(kvq_cache* c, int layer, const void* k, const void*
   if (!workspace || ws_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace ? ws_bytes : (size_t)0, need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   if (!L.counters_zeroed) {
     cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
     if (e != cudaSuccess) return cuda_fail(e, "counter reset");
@@ -874,7 +874,6 @@ kvq_status kvq_decode_attn_noalloc(kvq_cache* c, int layer, const void* q, int q
   void* scratch = nullptr;
   if (cudaError_t e = noalloc_scratch(&scratch)) return cuda_fail(e, "scratch address");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   if (!L.counters_zeroed) {  // the ticket counters live in the cache pool and must start at zero
     cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
     if (e != cudaSuccess) return cuda_fail(e, "counter reset");
@@ -1054,7 +1053,6 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   if (!workspace || ws_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed, 16-byte aligned", workspace ? ws_bytes : (size_t)0, need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   TreeArgs a{};
   a.c = view_of(c, layer);
   a.q = q->data;
@@ -1296,14 +1294,13 @@ kvq_status kvq_export_window(const kvq_cache* c, int layer, int b, int j, uint16
 kvq_status kvq_device_status(kvq_cache* c, kvq_stream_t stream) {
   if (!c) return fail(KVQ_ERR_INVALID, "cache is NULL");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   int flag = 0;
-  cudaError_t e = cudaMemcpyAsync(&flag, c->err(), 4, cudaMemcpyDeviceToHost, s);
+  cudaError_t e = cudaMemcpyAsync(&flag, c->err().at, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "device status");
-  if (flag) {
+  if (flag == c->err_code) {
     const int zero = 0;
-    e = cudaMemcpy(c->err(), &zero, 4, cudaMemcpyHostToDevice);
+    e = cudaMemcpy(c->err().at, &zero, 4, cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "device status reset");
     return fail(KVQ_ERR_TIMEOUT, "a kernel gave up waiting on its own bulk copies");
   }
@@ -1313,7 +1310,6 @@ kvq_status kvq_device_status(kvq_cache* c, kvq_stream_t stream) {
 kvq_status kvq_selftest_timeout(kvq_cache* c, kvq_stream_t stream) {
   if (!c) return fail(KVQ_ERR_INVALID, "cache is NULL");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaError_t e = c->ensure_err(s)) return cuda_fail(e, "error flag reset");
   if (cudaError_t e = launch_wait_probe(c->err(), s)) return cuda_fail(e, "wait probe launch");
   return KVQ_OK;
 }

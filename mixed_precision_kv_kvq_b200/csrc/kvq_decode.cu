@@ -1000,7 +1000,7 @@ cudaError_t launch_width(const DecodeArgs& a, cudaStream_t s) {
 // bring.  The decode kernel's own wait gives up after its time limit, raises
 // the device error flag and the kernel returns normally; no copy is in flight,
 // so nothing touches shared memory after the kernel ends.
-__global__ void wait_probe_kernel(int* err) {
+__global__ void wait_probe_kernel(ErrWord err) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ volatile int abort_flag;
   if (threadIdx.x == 0) {
@@ -1014,7 +1014,7 @@ __global__ void wait_probe_kernel(int* err) {
 
 }  // namespace
 
-cudaError_t launch_wait_probe(int* err, cudaStream_t s) {
+cudaError_t launch_wait_probe(ErrWord err, cudaStream_t s) {
   wait_probe_kernel<<<1, 32, 0, s>>>(err);
   return cudaGetLastError();
 }

@@ -46,21 +46,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded wait: true when the phase completed, false after kWaitNs (the
-// error flag is then set and *abort raised so later waits give up at once).
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+// error word is then set and *abort raised so later waits give up at once).
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, ErrWord err, volatile int* abort) {
   const unsigned long long t0 = global_ns();
   for (unsigned it = 0;; it++) {
     if (mbar_try(bar, parity)) return true;
     if ((it & 15) == 15) {
       if (*abort || global_ns() - t0 > kWaitNs) {
         *abort = 1;
-        atomicExch(err, 1);
+        atomicExch(err.at, err.code);
         return false;
       }
     }
   }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, ErrWord err, volatile int* abort) {
   if (mbar_try(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, err, abort);
 }

@@ -225,6 +225,15 @@ inline Epochs make_epochs(int nt, int n_shrinks) {
   return ep;
 }
 
+// The cache's error word, in its pool.  A kernel that gives up on a wait writes
+// the cache's own code there.  The pool is not cleared (whatever it held before
+// is no error of this cache), so no call has to clear the word first and no
+// call, captured or not, can erase what another raised.
+struct ErrWord {
+  int* at;
+  int code;
+};
+
 struct DecodeArgs {
   uint8_t* codes;       // the block's (or window's) codes; written only by a fused append
   uint32_t* meta;
@@ -233,7 +242,7 @@ struct DecodeArgs {
   float* out;           // fp32 [batch][q_heads][128]
   float* parts;         // workspace partials: [batch*kv_heads][splits] records of M[8], L[8], O[128][8]
   int* counters;        // [batch*kv_heads] ticket counters (zero between calls)
-  int* err;             // device error flag
+  ErrWord err;
   Fill fill;
   int batch, kv_heads, q_heads, group;
   float qscale;         // sm_scale * log2(e)
@@ -318,6 +327,6 @@ cudaError_t launch_block_move(const BlockMoveArgs& a, int n_streams, cudaStream_
 cudaError_t launch_shrink(const ShrinkArgs& a, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 
-cudaError_t launch_wait_probe(int* err, cudaStream_t s);
+cudaError_t launch_wait_probe(ErrWord err, cudaStream_t s);
 
 }  // namespace kvq

@@ -222,14 +222,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded wait: gives up after kWaitNs or once another wait of the CTA has.
-__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, int* err, volatile int* abort) {
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, const ErrWord& err, volatile int* abort) {
   if (mbar_try_many(bar, parity)) return;
   const unsigned long long t0 = global_ns();
   while (!mbar_try_many(bar, parity)) {
     if (*abort) return;
     if (global_ns() - t0 > kWaitNs) {
       *abort = 1;
-      atomicExch(err, 1);
+      atomicExch(err.at, err.code);
       return;
     }
   }
@@ -1083,7 +1083,7 @@ __device__ __forceinline__ void mma_role(const TreePlan& p, Small& sm, uint32_t 
       if (t0 == 0) t0 = now;
       if (now - t0 > kWaitNs) {
         sm.abort = 1;
-        atomicExch(p.a.err, 1);
+        atomicExch(p.a.err.at, p.a.err.code);
         break;
       }
     }

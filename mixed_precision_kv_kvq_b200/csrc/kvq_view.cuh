@@ -65,7 +65,7 @@ struct TreeArgs {
   int n, q_heads, group;
   float qscale;  // sm_scale * log2(e)
   void* out;     // bf16 [batch][n][q_heads][128]
-  int* err;
+  ErrWord err;
   void* ws;
   int num_sms;
 };

@@ -1,0 +1,80 @@
+"""A cache over memory that holds anything: the error word."""
+import pytest
+import torch
+
+import kvq_synth as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mixed_precision_kv_kvq_b200 import build
+
+    build.build()
+    import mixed_precision_kv_kvq_b200 as m
+
+    m.load()
+    return m
+
+
+def used_memory(kvq, byte, layers=1, B=1, H=2, fbit=4):
+    """A cache whose pool held other data before (every byte the same)."""
+    cache = kvq.KVQCache(layers, B, H, 512 * layers * B * H * 2 * (16 * fbit + 4), [fbit] * layers)
+    cache.pool.fill_(byte)
+    return cache
+
+
+def tokens(n, H=2, B=1):
+    k, v = S.keys_values(3, 0, B, n, H, 0, 2)
+    return k.cuda(), v.cuda()
+
+
+@pytest.mark.parametrize("byte", [0x00, 0x01, 0x7F, 0xFF])
+def test_what_the_pool_held_is_no_error(kvq, byte):
+    cache = used_memory(kvq, byte)
+    cache.device_status()
+    cache.append(0, *tokens(40))
+    cache.decode_attn(0, S.queries(1, 0, 0, 1, 8, 40, dtype=torch.bfloat16).cuda())
+    cache.device_status()
+
+
+def test_an_error_word_of_an_earlier_cache_is_not_this_ones(kvq):
+    cache = used_memory(kvq, 0)
+    kvq.kvq_selftest_timeout(cache.handle)
+    torch.cuda.synchronize()
+    per = 2 * 2 * (16 * 4 + 4)
+    other = kvq.kvq_alloc(1, 1, 2, 128, 512 * per, [4], cache.pool)
+    try:
+        kvq.kvq_device_status(other)
+    finally:
+        kvq.kvq_free(other)
+    with pytest.raises(kvq.KVQError) as e:
+        cache.device_status()
+    assert e.value.status == 7
+
+
+def test_replays_of_a_first_use_keep_an_error(kvq):
+    """Two blocks appended to and attended over in one graph, captured before anything else touched the cache: a wait that
+    gave up before a replay is still reported after it."""
+    cache = used_memory(kvq, 0x7F, layers=2)
+    k, v = tokens(9)
+    q = torch.randn(1, 9, 8, 128, device="cuda").bfloat16()
+    tree = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for layer in (0, 1):
+            cache.append(layer, k, v)
+            cache.tree_attn(layer, q, k, v, out=tree)
+    kvq.kvq_selftest_timeout(cache.handle)
+    graph.replay()
+    torch.cuda.synchronize()
+    with pytest.raises(kvq.KVQError) as e:
+        cache.device_status()
+    assert e.value.status == 7
+    graph.replay()
+    cache.device_status()
+    assert torch.isfinite(tree).all() and (tree != 0).any()

@@ -107,6 +107,7 @@ struct LayerState {
   int nt;  // tiles per stream
   int pf;  // meta slots per tile
   bool counters_zeroed;
+  unsigned long long counters_capture;  // the capture that cleared them last; 0: none
   size_t off_lam, off_lam_inv, off_counters, off_codes, off_meta;
   // sink + window option: n counts the progressive cache; n_all every token
   bool window;
@@ -164,6 +165,7 @@ bool make_plan(int layers, int batch, int kv_heads, int head_dim, size_t budget,
     L.pf = slots_per_tile(L.fbit);
     L.nt = (int)(n_f / L.pf);
     L.counters_zeroed = false;
+    L.counters_capture = 0;
     L.lambda_set = false;
     L.off_lam = off;
     off += align_up((size_t)kv_heads * kHeadDim * 4);
@@ -208,6 +210,27 @@ struct kvq_cache {
   int num_sms;
   int err_code;  // this cache's value of its error word (ErrWord)
   std::vector<LayerState> L;
+
+  // The ticket counters live in the pool, must start at zero and are left so by
+  // every decode call; calls of one block never overlap.  Cleared in stream order
+  // before the block's first decode.  A captured clearing happens at the replay:
+  // it serves the rest of its capture (captures have numbers of their own), and
+  // calls outside it clear for themselves until one of them did so at once.
+  cudaError_t ensure_counters(int l, cudaStream_t s) {
+    LayerState& x = L[l];
+    if (x.counters_zeroed) return cudaSuccess;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaError_t e = cudaStreamGetCaptureInfo(s, &cap, &id)) return e;
+    const bool captured = cap != cudaStreamCaptureStatusNone;
+    if (captured && x.counters_capture == id) return cudaSuccess;
+    if (cudaError_t e = cudaMemsetAsync(counters(l), 0, (size_t)batch * kv_heads * 4, s)) return e;
+    if (captured)
+      x.counters_capture = id;
+    else
+      x.counters_zeroed = true;
+    return cudaSuccess;
+  }
 
   int sms() {
     if (num_sms <= 0) {
@@ -750,11 +773,7 @@ kvq_status kvq_decode_attn(kvq_cache* c, int layer, const void* q, int q_heads, 
   if (!workspace || ws_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace ? ws_bytes : (size_t)0, need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!L.counters_zeroed) {
-    cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
-    if (e != cudaSuccess) return cuda_fail(e, "counter reset");
-    L.counters_zeroed = true;
-  }
+  if (cudaError_t e = c->ensure_counters(layer, s)) return cuda_fail(e, "counter reset");
   const DecodePlan d = plan_decode(c, L);
   cudaError_t e = enqueue_decode(c, layer, d, q, q_heads, sm_scale, out, static_cast<float*>(workspace), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
@@ -790,11 +809,7 @@ kvq_status kvq_append_decode(kvq_cache* c, int layer, const void* k, const void*
   if (!workspace || ws_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes; %zu needed", workspace ? ws_bytes : (size_t)0, need);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!L.counters_zeroed) {
-    cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
-    if (e != cudaSuccess) return cuda_fail(e, "counter reset");
-    L.counters_zeroed = true;
-  }
+  if (cudaError_t e = c->ensure_counters(layer, s)) return cuda_fail(e, "counter reset");
   if (L.n == capacity(L, c->n_f, L.bits)) {  // full: shrink one level first, as kvq_append would
     const ShrinkArgs sa = shrink_args(c, layer);
     if (cudaError_t e = launch_shrink(sa, s)) return cuda_fail(e, "shrink launch");
@@ -874,11 +889,7 @@ kvq_status kvq_decode_attn_noalloc(kvq_cache* c, int layer, const void* q, int q
   void* scratch = nullptr;
   if (cudaError_t e = noalloc_scratch(&scratch)) return cuda_fail(e, "scratch address");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!L.counters_zeroed) {  // the ticket counters live in the cache pool and must start at zero
-    cudaError_t e = cudaMemsetAsync(c->counters(layer), 0, (size_t)n_streams * 4, s);
-    if (e != cudaSuccess) return cuda_fail(e, "counter reset");
-    L.counters_zeroed = true;
-  }
+  if (cudaError_t e = c->ensure_counters(layer, s)) return cuda_fail(e, "counter reset");
   // the scratch is fully written before it is read: it needs no clearing
   cudaError_t e = enqueue_decode(c, layer, d, q, q_heads, sm_scale, out, static_cast<float*>(scratch), s);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");

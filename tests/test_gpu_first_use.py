@@ -1,4 +1,5 @@
-"""A cache over memory that holds anything: the error word."""
+"""A cache over memory that holds anything: the error word and the ticket
+counters, when the first use is captured, eager, or one and then the other."""
 import pytest
 import torch
 
@@ -78,3 +79,57 @@ def test_replays_of_a_first_use_keep_an_error(kvq):
     graph.replay()
     cache.device_status()
     assert torch.isfinite(tree).all() and (tree != 0).any()
+
+
+@pytest.mark.parametrize("how", ["decode_attn", "noalloc", "append_decode"])
+def test_eager_decode_between_a_capture_and_its_replay(kvq, how):
+    """The first decode is captured and does not run yet; an eager one before the replay, the replay, another graph."""
+    B, H, n = 2, 2, 400
+    k, v = tokens(n, H, B)
+    k1, v1 = tokens(1, H, B)
+    q = S.queries(1, 0, 0, B, 8, n, dtype=torch.bfloat16).cuda()
+
+    def make(byte):
+        cache = used_memory(kvq, byte, B=B, H=H)
+        cache.append(0, k, v)
+        return cache
+
+    def call(cache, out, eager):
+        if how == "noalloc":
+            kvq.kvq_decode_attn_noalloc(cache.handle, 0, q, 128 ** -0.5, out)
+        elif how == "append_decode" and not eager:
+            cache.append_decode(0, k1, v1, q, out=out)
+        else:
+            cache.decode_attn(0, q, out=out)
+
+    ref = make(0)
+    if how == "append_decode":
+        ref.append(0, k1, v1)
+    want = ref.decode_attn(0, q)
+
+    cache = make(0x7F)
+    cache.workspace(0, 8)
+    first, second, eager = (torch.full_like(want, 7.0) for _ in range(3))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(cache, first, False)
+    if how == "append_decode":  # the captured token is not in the cache before the replay: put it there
+        slot = make(0)
+        slot.append(0, k1, v1)
+        lo = 4096
+        cache.pool[lo:].copy_(slot.pool[lo:])
+    call(cache, eager, True)
+    torch.cuda.synchronize()
+    assert ((eager - want).abs() <= 1e-5 * want.abs().amax()).all()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert ((first - want).abs() <= 1e-5 * want.abs().amax()).all()
+    again = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(again):
+        cache.decode_attn(0, q, out=second)
+    for g in (again, graph, again):
+        g.replay()
+    torch.cuda.synchronize()
+    assert ((second - want).abs() <= 1e-5 * want.abs().amax()).all()
+    cache.device_status()

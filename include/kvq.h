@@ -329,6 +329,10 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
 kvq_status kvq_read(kvq_cache* c, int layer, int start, int n_tokens, int dtype, const kvq_rows* k_out,
                     const kvq_rows* v_out, kvq_stream_t stream);
 
+/* What the cache was made with.  Any output pointer may be NULL.
+ * Errors: INVALID. */
+kvq_status kvq_dims(const kvq_cache* c, int* layers, int* batch, int* kv_heads);
+
 /* Host-side state of one block.  Any output pointer may be NULL.
  * capacity: tokens that fit at the current width. */
 kvq_status kvq_query(const kvq_cache* c, int layer, int* tokens, int* bits, int* capacity,

@@ -25,7 +25,7 @@ HEAD_DIM = 128
 __all__ = [
     "KVQCache", "KVQError", "Rope", "load",
     "kvq_pool_bytes", "kvq_pool_bytes_ex", "kvq_alloc", "kvq_alloc_ex", "kvq_export_window", "kvq_set_lambda", "kvq_append", "kvq_shrink", "kvq_set_shift_mode",
-    "kvq_decode_workspace", "kvq_decode_attn", "kvq_decode_attn_noalloc", "kvq_append_decode", "kvq_query", "kvq_max_tokens", "kvq_export",
+    "kvq_decode_workspace", "kvq_decode_attn", "kvq_decode_attn_noalloc", "kvq_append_decode", "kvq_dims", "kvq_query", "kvq_max_tokens", "kvq_export",
     "kvq_rope_freqs", "kvq_rope", "kvq_tree_workspace", "kvq_tree_attn", "kvq_read",
     "kvq_device_status", "kvq_selftest_timeout", "kvq_last_error", "kvq_free", "kvq_allocate_bits",
 ]
@@ -50,6 +50,20 @@ def _dptr(t: torch.Tensor) -> C.c_void_p:
     return C.c_void_p(t.data_ptr())
 
 
+class _Handle(C.c_void_p):
+    """A cache's handle, with what kvq_dims says of it."""
+
+    dims = None
+
+
+def _check_cache(cache, **tensors) -> None:
+    """That [batch][n][heads][128] tensors have the cache's batch and KV heads: the kernels go by the cache's."""
+    _, batch, heads = getattr(cache, "dims", None) or kvq_dims(cache)
+    for name, t in tensors.items():
+        if t is not None and (t.dim() != 4 or t.shape[0] != batch or t.shape[2] != heads):
+            raise ValueError(f"{name} must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(t.shape)}")
+
+
 # ---------------------------------------------------------------- C ABI mirror
 
 def kvq_pool_bytes(layers: int, batch: int, kv_heads: int, head_dim: int, budget_bytes: int,
@@ -69,11 +83,12 @@ def kvq_alloc(layers: int, batch: int, kv_heads: int, head_dim: int, budget_byte
 
 def kvq_alloc_ex(layers: int, batch: int, kv_heads: int, head_dim: int, budget_bytes: int,
                  fbit: Sequence[int], dev_pool: Optional[torch.Tensor] = None, options: int = 0) -> C.c_void_p:
-    h = C.c_void_p()
+    h = _Handle()
     pool_ptr = _dptr(dev_pool) if dev_pool is not None else C.c_void_p(None)
     pool_bytes = dev_pool.numel() * dev_pool.element_size() if dev_pool is not None else 0
     check(load().kvq_alloc_ex(C.byref(h), layers, batch, kv_heads, head_dim, budget_bytes,
                               _fbit_array(fbit), pool_ptr, pool_bytes, options))
+    h.dims = kvq_dims(h)
     return h
 
 
@@ -332,6 +347,7 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     """q: device bf16 [batch][n][q_heads][128]; k, v: device [batch][n][kv_heads][128], bf16 or fp32 (strided views
     allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
     shaped like q."""
+    _check_cache(cache, k=k, v=v)
     dtype, dt, device = _dtype_code(k), k.dtype, q.device
     qr, kr = _take("q", q, torch.bfloat16, device), _take("k", k, dt, device)
     vr = _take("v", v, dt, device, k.shape)
@@ -339,8 +355,8 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     b, n, q_heads, _ = q.shape
     if k.shape[:2] != (b, n):
         raise ValueError(f"k must be [{b}][{n}][kv_heads][128], got {list(k.shape)}")
-    if not out.is_contiguous() or workspace.device != device:
-        raise ValueError("out must be contiguous and workspace on its device")
+    if not out.is_contiguous() or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("out and workspace must be contiguous and on one device")
     mask_ptr, mask_b = None, 0
     if mask is not None:
         mt, ms = mask.dtype, mask.shape
@@ -363,6 +379,7 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
     first = k_out if k_out is not None else v_out
     if first is None:
         raise ValueError("k_out and v_out are both None")
+    _check_cache(cache, k_out=k_out, v_out=v_out)
     dtype, dt, device = _dtype_code(first), first.dtype, first.device
     kr = _take("k_out", k_out, dt, device) if k_out is not None else None
     vr = _take("v_out", v_out, dt, device, first.shape) if v_out is not None else None
@@ -370,6 +387,13 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
         raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
     check(load().kvq_read(cache, layer, start, count, dtype, kr, vr,
                           stream if type(stream) is int else _stream_ptr(stream)))
+
+
+def kvq_dims(cache) -> tuple:
+    """-> (layers, batch, kv_heads) of a cache."""
+    n, b, h = C.c_int(), C.c_int(), C.c_int()
+    check(load().kvq_dims(cache, C.byref(n), C.byref(b), C.byref(h)))
+    return n.value, b.value, h.value
 
 
 def kvq_query(cache, layer: int) -> dict:
@@ -540,8 +564,6 @@ class KVQCache:
         device = self.pool.device
         if q.dim() != 4 or q.shape[0] != self.batch or q.device != device:
             raise ValueError(f"q must be [{self.batch}][n][q_heads][128] on {device}, got {list(q.shape)} on {q.device}")
-        if k.dim() != 4 or k.shape[2] != self.kv_heads:
-            raise ValueError(f"k must be [{self.batch}][n][{self.kv_heads}][128], got {list(k.shape)}")
         with _On(device, stream) as on:
             # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
             size = (q.shape[2], q.shape[1])
@@ -573,16 +595,10 @@ class KVQCache:
                 v_out = on.like(k_out)
             else:
                 for name, x in (("k_out", k_out), ("v_out", v_out)):
-                    if x is not None:
-                        self._check_batch(name, x, self.kv_heads)
+                    if x is not None and x.device != device:
+                        raise ValueError(f"{name} must be on the cache's device {device}, got {x.device}")
             kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr)
         return k_out, v_out
-
-    def _check_batch(self, name: str, t: torch.Tensor, heads: Optional[int]) -> None:
-        if t.device != self.pool.device:
-            raise ValueError(f"{name} must be on the cache's device {self.pool.device}, got {t.device}")
-        if t.dim() != 4 or t.shape[0] != self.batch or (heads is not None and t.shape[2] != heads):
-            raise ValueError(f"{name} must be [{self.batch}][n][{heads or 'heads'}][128], got {list(t.shape)}")
 
     def query(self, layer: int) -> dict:
         return kvq_query(self.handle, layer)

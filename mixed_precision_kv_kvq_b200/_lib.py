@@ -65,6 +65,7 @@ SIGNATURES = {
     "kvq_tree_workspace": (SZ, [P, I, I, I]),
     "kvq_tree_attn": (I, [P, I, P, I, I, P, P, I, P, LL, F, P, P, SZ, P]),
     "kvq_read": (I, [P, I, I, I, I, P, P, P]),
+    "kvq_dims": (I, [P, P, P, P]),
     "kvq_query": (I, [P, I, P, P, P, P]),
     "kvq_max_tokens": (I, [P]),
     "kvq_export": (I, [P, I, I, I, P, P, P, P, P]),

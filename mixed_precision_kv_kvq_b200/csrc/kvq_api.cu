@@ -1147,6 +1147,14 @@ kvq_status kvq_read(kvq_cache* c, int layer, int start, int n_tokens, int dtype,
   return KVQ_OK;
 }
 
+kvq_status kvq_dims(const kvq_cache* c, int* layers, int* batch, int* kv_heads) {
+  if (!c) return fail(KVQ_ERR_INVALID, "cache is NULL");
+  if (layers) *layers = c->layers;
+  if (batch) *batch = c->batch;
+  if (kv_heads) *kv_heads = c->kv_heads;
+  return KVQ_OK;
+}
+
 kvq_status kvq_query(const kvq_cache* c, int layer, int* tokens, int* bits, int* cap, int* n_shrinks) {
   if (kvq_status s = check_layer(c, layer)) return s;
   const LayerState& L = c->L[layer];

@@ -1,0 +1,56 @@
+"""The Python functions go by the cache's own batch and KV heads: tensors of
+others are refused before anything is launched (CPU tensors and a cache over a
+host buffer: nothing here reaches a GPU)."""
+import pytest
+import torch
+
+from test_abi_host import _host_cache
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from mixed_precision_kv_kvq_b200 import build
+
+    build.build()
+    import mixed_precision_kv_kvq_b200 as m
+
+    m.load()
+    return m
+
+
+@pytest.fixture
+def cache(kvq):
+    h, pool = _host_cache(kvq, batch=2, kv_heads=3)
+    yield h
+    kvq.kvq_free(h)
+
+
+def x(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_dims(kvq, cache):
+    assert kvq.kvq_dims(cache) == (1, 2, 3)
+    assert kvq.load().kvq_dims(cache, None, None, None) == 0
+    with pytest.raises(kvq.KVQError):
+        kvq.kvq_dims(None)
+
+
+WRONG = [(1, 4, 3, 128), (3, 4, 3, 128), (2, 4, 2, 128), (2, 4, 4, 128), (2, 4, 128)]
+
+
+@pytest.mark.parametrize("shape", WRONG)
+def test_read_refuses_outputs_of_another_cache(kvq, cache, shape):
+    for args in ((x(*shape), None), (None, x(*shape)), (x(2, 4, 3, 128), x(*shape))):
+        with pytest.raises(ValueError, match=r"must be \[2\]\[n\]\[3\]\[128\]"):
+            kvq.kvq_read(cache, 0, 0, 4, *args)
+
+
+@pytest.mark.parametrize("shape", WRONG)
+def test_tree_refuses_inputs_of_another_cache(kvq, cache, shape):
+    good = x(2, 4, 3, 128)
+    for k, v in ((x(*shape), x(*shape)), (good, x(*shape)), (x(*shape), good)):
+        with pytest.raises(ValueError, match=r"must be \[2\]\[n\]\[3\]\[128\]"):
+            kvq.kvq_tree_attn(cache, 0, x(2, 4, 6, 128), k, v, None, 0.1, x(2, 4, 6, 128), x(1 << 16, dtype=torch.uint8))

@@ -64,6 +64,15 @@ def _check_cache(cache, **tensors) -> None:
             raise ValueError(f"{name} must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(t.shape)}")
 
 
+def _check_queries(cache, q: torch.Tensor, workspace: Optional[torch.Tensor] = None) -> None:
+    """The same of [batch][q_heads][128] queries, and a workspace whose bytes neighbour."""
+    batch = (getattr(cache, "dims", None) or kvq_dims(cache))[1]
+    if q.dim() != 3 or q.shape[0] != batch:
+        raise ValueError(f"q must be [{batch}][q_heads][{HEAD_DIM}], got {list(q.shape)}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 # ---------------------------------------------------------------- C ABI mirror
 
 def kvq_pool_bytes(layers: int, batch: int, kv_heads: int, head_dim: int, budget_bytes: int,
@@ -107,6 +116,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def kvq_append(cache, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """k, v: device [batch][n][kv_heads][128], bf16 or fp32, contiguous."""
+    _check_cache(cache, k=k, v=v)
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[-1] != HEAD_DIM:
         raise ValueError("k and v must both be [batch][n][kv_heads][128] of one dtype")
     if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
@@ -131,6 +141,7 @@ def kvq_decode_workspace(cache, layer: int, q_heads: int) -> int:
 def kvq_decode_attn(cache, layer: int, q: torch.Tensor, sm_scale: float, out: torch.Tensor,
                     workspace: torch.Tensor, stream=None) -> None:
     """q: device bf16 [batch][q_heads][128]; out: device fp32, same shape."""
+    _check_queries(cache, q, workspace)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[-1] != HEAD_DIM or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
     if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():
@@ -146,6 +157,8 @@ def kvq_append_decode(cache, layer: int, k: torch.Tensor, v: torch.Tensor, q: to
                       out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """One decode step in one launch: append k, v (device [batch][1][kv_heads][128])
     then attend with q (device bf16 [batch][q_heads][128]) into out (fp32)."""
+    _check_cache(cache, k=k, v=v)
+    _check_queries(cache, q, workspace)
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[1] != 1 or k.shape[-1] != HEAD_DIM:
         raise ValueError("k and v must both be [batch][1][kv_heads][128] of one dtype")
     if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
@@ -165,6 +178,7 @@ def kvq_decode_attn_noalloc(cache, layer: int, q: torch.Tensor, sm_scale: float,
     device memory where they run decode.  The library's own fixed 24 MiB
     scratch buffer (one per GPU, kept until exit) holds the split partials;
     calls that can overlap on the GPU share it and must be serialised."""
+    _check_queries(cache, q)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[-1] != HEAD_DIM or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
     if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():

@@ -54,3 +54,31 @@ def test_tree_refuses_inputs_of_another_cache(kvq, cache, shape):
     for k, v in ((x(*shape), x(*shape)), (good, x(*shape)), (x(*shape), good)):
         with pytest.raises(ValueError, match=r"must be \[2\]\[n\]\[3\]\[128\]"):
             kvq.kvq_tree_attn(cache, 0, x(2, 4, 6, 128), k, v, None, 0.1, x(2, 4, 6, 128), x(1 << 16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("shape", WRONG)
+def test_append_refuses_tokens_of_another_cache(kvq, cache, shape):
+    with pytest.raises(ValueError, match=r"must be \[2\]\[n\]\[3\]\[128\]"):
+        kvq.kvq_append(cache, 0, x(*shape), x(*shape))
+    one = (shape[0], 1) + shape[2:]
+    with pytest.raises(ValueError, match=r"must be \[2\]\[n\]\[3\]\[128\]"):
+        kvq.kvq_append_decode(cache, 0, x(*one), x(*one), x(2, 6, 128), 0.1, x(2, 6, 128, dtype=torch.float32), x(1 << 16))
+
+
+@pytest.mark.parametrize("batch", [1, 3])
+def test_decode_refuses_queries_of_another_cache(kvq, cache, batch):
+    q, out, ws = x(batch, 6, 128), x(batch, 6, 128, dtype=torch.float32), x(1 << 16, dtype=torch.float32)
+    kv = x(2, 1, 3, 128)
+    for call in (lambda: kvq.kvq_decode_attn(cache, 0, q, 0.1, out, ws), lambda: kvq.kvq_decode_attn_noalloc(cache, 0, q, 0.1, out),
+                 lambda: kvq.kvq_append_decode(cache, 0, kv, kv, q, 0.1, out, ws)):
+        with pytest.raises(ValueError, match=r"q must be \[2\]\[q_heads\]\[128\]"):
+            call()
+
+
+def test_decode_refuses_a_strided_workspace(kvq, cache):
+    q, out, ws = x(2, 6, 128), x(2, 6, 128, dtype=torch.float32), x(1 << 20, dtype=torch.float32)[::2]
+    kv = x(2, 1, 3, 128)
+    for call in (lambda: kvq.kvq_decode_attn(cache, 0, q, 0.1, out, ws),
+                 lambda: kvq.kvq_append_decode(cache, 0, kv, kv, q, 0.1, out, ws)):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            call()

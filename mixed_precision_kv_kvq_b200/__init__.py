@@ -220,19 +220,17 @@ class _On:
     """Device guard, launch stream and allocator of one call on `device`: the
     given stream, or the device's current one."""
 
-    __slots__ = ("device", "guard", "stream", "ptr")
+    __slots__ = ("device", "guard", "given", "ptr")
 
     def __init__(self, device, stream):
-        self.device = device
+        self.device, self.given = device, stream
         self.guard = torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else None
-        self.stream = None
         if stream is None:
             self.ptr = torch._C._cuda_getCurrentRawStream(device.index)
         elif isinstance(stream, torch.cuda.Stream):
-            self.stream, self.ptr = stream, stream.cuda_stream
+            self.ptr = stream.cuda_stream
         else:
-            self.ptr = int(stream)  # a raw handle; what the call allocates belongs to it, not to the current stream
-            self.stream = (torch.cuda.ExternalStream(self.ptr, device) if self.ptr else torch.cuda.default_stream(device))
+            self.ptr = int(stream)
 
     def __enter__(self):
         if self.guard is not None:
@@ -243,18 +241,24 @@ class _On:
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
+    def _stream(self):
+        """The given stream; of a raw handle, what the call allocates belongs to it and not to the current stream."""
+        if isinstance(self.given, torch.cuda.Stream):
+            return self.given
+        return torch.cuda.ExternalStream(self.ptr, self.device) if self.ptr else torch.cuda.default_stream(self.device)
+
     def empty(self, shape, dtype) -> torch.Tensor:
         """A new tensor that belongs to the call's stream."""
-        if self.stream is None:
+        if self.given is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self._stream()):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def like(self, t: torch.Tensor) -> torch.Tensor:
         """The same, contiguous and shaped like t."""
-        if self.stream is None:
+        if self.given is None:
             return torch.empty_like(t, memory_format=torch.contiguous_format)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self._stream()):
             return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
@@ -362,6 +366,14 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
     shaped like q."""
     _check_cache(cache, k=k, v=v)
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    with _On(q.device, stream) as on:
+        _tree_attn(cache, layer, q, k, v, mask, sm_scale, out, workspace, on.ptr)
+
+
+def _tree_attn(cache, layer, q, k, v, mask, sm_scale, out, workspace, ptr) -> None:
+    """kvq_tree_attn with k and v of the cache's shape and q's device current, on the stream handle ptr."""
     dtype, dt, device = _dtype_code(k), k.dtype, q.device
     qr, kr = _take("q", q, torch.bfloat16, device), _take("k", k, dt, device)
     vr = _take("v", v, dt, device, k.shape)
@@ -382,8 +394,7 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
             raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(ms)}")
         mask_ptr = mask.data_ptr()
     check(load().kvq_tree_attn(cache, layer, qr, q_heads, n, kr, vr, dtype, mask_ptr, mask_b, sm_scale,
-                               out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               stream if type(stream) is int else _stream_ptr(stream)))
+                               out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), ptr))
 
 
 def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor],
@@ -394,13 +405,21 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
     if first is None:
         raise ValueError("k_out and v_out are both None")
     _check_cache(cache, k_out=k_out, v_out=v_out)
+    if not first.is_cuda:
+        raise ValueError("k_out and v_out must be CUDA tensors")
+    with _On(first.device, stream) as on:
+        _read(cache, layer, start, count, k_out, v_out, on.ptr)
+
+
+def _read(cache, layer, start, count, k_out, v_out, ptr) -> None:
+    """kvq_read with outputs of the cache's shape and their device current, on the stream handle ptr."""
+    first = k_out if k_out is not None else v_out
     dtype, dt, device = _dtype_code(first), first.dtype, first.device
     kr = _take("k_out", k_out, dt, device) if k_out is not None else None
     vr = _take("v_out", v_out, dt, device, first.shape) if v_out is not None else None
     if first.shape[1] != count:
         raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
-    check(load().kvq_read(cache, layer, start, count, dtype, kr, vr,
-                          stream if type(stream) is int else _stream_ptr(stream)))
+    check(load().kvq_read(cache, layer, start, count, dtype, kr, vr, ptr))
 
 
 def kvq_dims(cache) -> tuple:
@@ -578,6 +597,7 @@ class KVQCache:
         device = self.pool.device
         if q.dim() != 4 or q.shape[0] != self.batch or q.device != device:
             raise ValueError(f"q must be [{self.batch}][n][q_heads][128] on {device}, got {list(q.shape)} on {q.device}")
+        _check_cache(self.handle, k=k, v=v)
         with _On(device, stream) as on:
             # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
             size = (q.shape[2], q.shape[1])
@@ -588,8 +608,8 @@ class KVQCache:
                     self._tree_ws[size] = nbytes
             if out is None:
                 out = on.like(q)
-            kvq_tree_attn(self.handle, layer, q, k, v, mask, HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out,
-                          on.empty((nbytes,), torch.uint8), on.ptr)
+            _tree_attn(self.handle, layer, q, k, v, mask, HEAD_DIM ** -0.5 if sm_scale is None else sm_scale, out,
+                       on.empty((nbytes,), torch.uint8), on.ptr)
         return out
 
     def read(self, layer: int, start: int = 0, count: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
@@ -608,10 +628,11 @@ class KVQCache:
                 k_out = on.empty(shape, dtype)
                 v_out = on.like(k_out)
             else:
+                _check_cache(self.handle, k_out=k_out, v_out=v_out)
                 for name, x in (("k_out", k_out), ("v_out", v_out)):
                     if x is not None and x.device != device:
                         raise ValueError(f"{name} must be on the cache's device {device}, got {x.device}")
-            kvq_read(self.handle, layer, start, count, k_out, v_out, on.ptr)
+            _read(self.handle, layer, start, count, k_out, v_out, on.ptr)
         return k_out, v_out
 
     def query(self, layer: int) -> dict:

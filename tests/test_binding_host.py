@@ -82,3 +82,55 @@ def test_decode_refuses_a_strided_workspace(kvq, cache):
                  lambda: kvq.kvq_append_decode(cache, 0, kv, kv, q, 0.1, out, ws)):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             call()
+
+
+class OnDevice1:
+    """What the binding reads of a tensor, of one on the second GPU."""
+
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def __init__(self, *shape, dtype=BF):
+        self.like = torch.zeros(*shape, dtype=dtype)
+
+    def __getattr__(self, name):
+        return getattr(self.like, name)
+
+
+@pytest.mark.parametrize("stream", [None, 77])
+def test_functions_launch_on_the_tensors_device(kvq, cache, monkeypatch, stream):
+    """Device 0 is current, the tensors lie on device 1: its current stream (or the given one), with it made current."""
+    calls = []
+
+    class Guard:
+        def __init__(self, device):
+            calls.append(("device", device.index))
+
+        def __enter__(self):
+            calls.append("in")
+
+        def __exit__(self, *exc):
+            calls.append("out")
+
+    class Lib:
+        def kvq_read(self, *args):
+            calls.append(("read", args[-1]))
+            return 0
+
+        def kvq_tree_attn(self, *args):
+            calls.append(("tree", args[-1]))
+            return 0
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    kvq.kvq_dims(cache)
+    monkeypatch.setattr(kvq, "load", lambda: Lib())
+    monkeypatch.setattr(kvq, "kvq_dims", lambda c: (1, 2, 3))
+    want = 1001 if stream is None else stream
+    kvq.kvq_read(cache, 0, 0, 4, OnDevice1(2, 4, 3, 128), None, stream)
+    assert calls == [("device", 1), "in", ("read", want), "out"]
+    calls.clear()
+    k = OnDevice1(2, 4, 3, 128)
+    kvq.kvq_tree_attn(cache, 0, OnDevice1(2, 4, 6, 128), k, k, None, 0.1, OnDevice1(2, 4, 6, 128),
+                      OnDevice1(1 << 16, dtype=torch.uint8), stream)
+    assert calls == [("device", 1), "in", ("tree", want), "out"]

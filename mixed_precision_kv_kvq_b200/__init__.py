@@ -167,6 +167,8 @@ def kvq_append_decode(cache, layer: int, k: torch.Tensor, v: torch.Tensor, q: to
         raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
     if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous fp32 tensor shaped like q")
+    if not (q.is_cuda and out.is_cuda and workspace.is_cuda):
+        raise ValueError("q, out and workspace must be CUDA tensors")
     ws_bytes = workspace.numel() * workspace.element_size()
     check(load().kvq_append_decode(cache, layer, _dptr(k), _dptr(v), _dtype_code(k), _dptr(q), q.shape[1],
                                    float(sm_scale), _dptr(out), _dptr(workspace), ws_bytes, _stream_ptr(stream)))

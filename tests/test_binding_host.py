@@ -134,3 +134,14 @@ def test_functions_launch_on_the_tensors_device(kvq, cache, monkeypatch, stream)
     kvq.kvq_tree_attn(cache, 0, OnDevice1(2, 4, 6, 128), k, k, None, 0.1, OnDevice1(2, 4, 6, 128),
                       OnDevice1(1 << 16, dtype=torch.uint8), stream)
     assert calls == [("device", 1), "in", ("tree", want), "out"]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_append_decode_refuses_host_tensors(kvq, cache, monkeypatch, which):
+    monkeypatch.setattr(kvq, "load", lambda: None)  # nothing is called
+    monkeypatch.setattr(kvq, "kvq_dims", lambda c: (1, 2, 3))
+    kv = OnDevice1(2, 1, 3, 128)
+    args = [OnDevice1(2, 6, 128), OnDevice1(2, 6, 128, dtype=torch.float32), OnDevice1(1 << 16, dtype=torch.uint8)]
+    args[which] = args[which].like
+    with pytest.raises(ValueError, match="must be CUDA tensors"):
+        kvq.kvq_append_decode(cache, 0, kv, kv, args[0], 0.1, args[1], args[2])

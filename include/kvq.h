@@ -223,9 +223,9 @@ kvq_status kvq_decode_attn_noalloc(kvq_cache* c, int layer, const void* q, int q
                                    float* out, kvq_stream_t stream);
 
 /* A tensor [batch][n][heads][128] in device memory: element (b, t, h, c) at
- * data + b stride_b + t stride_t + h stride_h + c, strides in elements, so a
- * slice of a fused projection or a [batch][heads][n][128] layout is passed
- * as it is. */
+ * data + b stride_b + t stride_t + h stride_h + c, strides in elements (that
+ * of a dimension of one element may be anything), so a slice of a fused
+ * projection or a [batch][heads][n][128] layout is passed as it is. */
 typedef struct {
   void* data;
   long long stride_b, stride_t, stride_h;

@@ -927,12 +927,14 @@ CacheView view_of(kvq_cache* c, int layer) {
   return v;
 }
 
-// Whether every row of x starts on a multiple of `bytes`.
-bool rows_aligned(const kvq_rows& x, size_t esize, size_t bytes) {
-  return (reinterpret_cast<uintptr_t>(x.data) | (uintptr_t)(x.stride_b * (long long)esize) |
-          (uintptr_t)(x.stride_t * (long long)esize) | (uintptr_t)(x.stride_h * (long long)esize)) %
-             bytes ==
-         0;
+// Whether every row of x [batch][n][heads] starts on a multiple of `bytes`.  A
+// dimension of one element has a stride that nothing uses.
+bool rows_aligned(const kvq_rows& x, int batch, int n, int heads, size_t esize, size_t bytes) {
+  uintptr_t at = reinterpret_cast<uintptr_t>(x.data);
+  if (batch != 1) at |= (uintptr_t)(x.stride_b * (long long)esize);
+  if (n != 1) at |= (uintptr_t)(x.stride_t * (long long)esize);
+  if (heads != 1) at |= (uintptr_t)(x.stride_h * (long long)esize);
+  return at % bytes == 0;
 }
 
 }  // namespace
@@ -1007,7 +1009,9 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
     if (heads == 0) return true;
     if (!in || !out || !in->data || !out->data) return false;
     r = RopeRows{in->data, out->data, heads, in->stride_b, in->stride_t, in->stride_h, out->stride_b, out->stride_t, out->stride_h};
-    while (a.align > 1 && !(rows_aligned(*in, esize, a.align) && rows_aligned(*out, esize, a.align))) a.align /= 2;
+    while (a.align > 1 && !(rows_aligned(*in, batch, n_tokens, heads, esize, a.align) &&
+                            rows_aligned(*out, batch, n_tokens, heads, esize, a.align)))
+      a.align /= 2;
     return true;
   };
   if (!take(q, q_out, q_heads, a.q) || !take(k, k_out, kv_heads, a.k)) return fail(KVQ_ERR_INVALID, "q, k or an output is NULL");
@@ -1057,8 +1061,8 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   if (!std::isfinite(sm_scale)) return fail(KVQ_ERR_INVALID, "sm_scale is not finite");
   if (mask_stride_b < 0) return fail(KVQ_ERR_INVALID, "mask_stride_b < 0");
   const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
-  if (!rows_aligned(*q, 2, 16) || !rows_aligned(*k, esize, 16) || !rows_aligned(*v, esize, 16) ||
-      reinterpret_cast<uintptr_t>(out) % 16)
+  if (!rows_aligned(*q, c->batch, n_nodes, q_heads, 2, 16) || !rows_aligned(*k, c->batch, n_nodes, c->kv_heads, esize, 16) ||
+      !rows_aligned(*v, c->batch, n_nodes, c->kv_heads, esize, 16) || reinterpret_cast<uintptr_t>(out) % 16)
     return fail(KVQ_ERR_INVALID, "the rows of q, k and v, and out, must be 16-byte aligned");
   const size_t need = kvq_tree_workspace(c, layer, q_heads, n_nodes);
   if (!workspace || ws_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)
@@ -1127,7 +1131,8 @@ kvq_status kvq_read(kvq_cache* c, int layer, int start, int n_tokens, int dtype,
   if (n_tokens > 0 && ((k_out && !k_out->data) || (v_out && !v_out->data)))
     return fail(KVQ_ERR_INVALID, "an output has no data");
   const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
-  if ((k_out && !rows_aligned(*k_out, esize, 16)) || (v_out && !rows_aligned(*v_out, esize, 16)))
+  if ((k_out && !rows_aligned(*k_out, c->batch, n_tokens, c->kv_heads, esize, 16)) ||
+      (v_out && !rows_aligned(*v_out, c->batch, n_tokens, c->kv_heads, esize, 16)))
     return fail(KVQ_ERR_INVALID, "the rows of k_out and v_out must be 16-byte aligned");
   if (n_tokens == 0 || (!k_out && !v_out)) return KVQ_OK;
   ReadArgs a{};

@@ -58,3 +58,37 @@ def test_functions_refuse_other_batches_and_heads(kvq):
     assert (out == 0).all()
     kvq.kvq_tree_attn(cache.handle, 0, q, k, k, None, 0.1, out, ws)
     assert torch.equal(out, cache.tree_attn(0, q, k, k, sm_scale=0.1))
+
+
+def odd(t, *dims):
+    """The same elements with strides of 1 in the given dimensions, each of one element."""
+    strides = list(t.stride())
+    for d in dims:
+        assert t.shape[d] == 1
+        strides[d] = 1
+    return torch.as_strided(t, t.shape, strides, t.storage_offset())
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("B,n,H,dims", [(1, 5, 2, (0,)), (2, 1, 2, (1,)), (2, 5, 1, (2,)), (1, 1, 1, (0, 1, 2))])
+def test_strides_of_single_elements_are_free(kvq, dtype, B, n, H, dims):
+    """A dimension of one element may have any stride: [b][n][1][128] made of a transposed [b][n][128][1], a slice of one
+    sequence or token."""
+    cache = filled(kvq, B, H)
+    k, v = rand(2, B, n, H, 128, dtype=dtype), rand(3, B, n, H, 128, dtype=dtype)
+    room = torch.zeros(B, n, H, 128, device="cuda", dtype=dtype)
+    want = cache.read(0, 3, n, dtype=dtype)
+    got = cache.read(0, 3, n, k_out=odd(room, *dims), v_out=odd(torch.zeros_like(room), *dims))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(room, want[0])
+    for G in (1, 8):
+        q = rand(1, B, n, H * G, 128)
+        want = cache.tree_attn(0, q, k, v)
+        qd = [d for d in dims if q.shape[d] == 1]
+        assert torch.equal(cache.tree_attn(0, odd(q, *qd), odd(k, *dims), odd(v, *dims)), want)
+    pos = torch.arange(n, device="cuda")
+    for layout in ("half", "interleaved"):
+        rope = kvq.Rope(128, layout=layout)
+        want = kvq.kvq_rope(rope, pos, k, v)
+        out = torch.zeros_like(k)
+        assert torch.equal(kvq.kvq_rope(rope, pos, odd(k, *dims), odd(v, *dims), q_out=odd(out, *dims))[0], want[0])
+        assert torch.equal(out, want[0])

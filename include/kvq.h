@@ -257,8 +257,9 @@ kvq_status kvq_rope_freqs(int rot_dim, double theta, int scaling, double factor,
  * angle positions[b][t] * inv_freq[p] and multiply it by magnitude:
  *   y0 = (x0 cos - x1 sin) magnitude,  y1 = (x1 cos + x0 sin) magnitude;
  * the other channels pass unchanged.  Pair p is channels (p, p + rot_dim / 2)
- * (KVQ_ROPE_HALF) or (2p, 2p + 1) (KVQ_ROPE_INTERLEAVED).  The angle is
- * reduced exactly, so positions may be any integers; arithmetic is fp32,
+ * (KVQ_ROPE_HALF) or (2p, 2p + 1) (KVQ_ROPE_INTERLEAVED).  The phase is
+ * a 64-bit fraction of a turn, off by at most |position| 2^-65 of a turn (4e-10
+ * rad at 2^31, 2e-7 at 2^40) at any frequency; angle and arithmetic are fp32,
  * rounded once to dtype (KVQ_DTYPE_*).  Keys are turned before kvq_append,
  * queries before the attention calls, both here in one launch.
  *

@@ -927,6 +927,25 @@ CacheView view_of(kvq_cache* c, int layer) {
   return v;
 }
 
+// 2^64 w / (2 pi) modulo 2^64, rounded, for |w| <= 2^20.  w is m 2^e with an
+// integer m < 2^53, so e <= -32, and 1 / (2 pi) is taken to 128 binary places: the
+// product m (1 / (2 pi)) 2^128, 181 bits, is off by less than m, i.e. by less than
+// 2^-43 of the result's unit, and its whole turns drop out as integers.
+unsigned long long turn_of(double w) {
+  constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;
+  int e;
+  const double f = std::frexp(std::fabs(w), &e);  // [1/2, 1) 2^e, or 0
+  const unsigned long long m = (unsigned long long)std::ldexp(f, 53);
+  e -= 53;
+  const unsigned __int128 lo = (unsigned __int128)m * kLo, hi = (unsigned __int128)m * kHi + (unsigned long long)(lo >> 64);
+  // the product is hi 2^64 + the low half of lo; the result is that / 2^(64 - e), a
+  // shift of hi by -e >= 32 places, rounded by the last bit shifted out
+  const int shift = -e;
+  unsigned long long t = 0;
+  if (shift < 128) t = (unsigned long long)(hi >> shift) + (unsigned long long)((hi >> (shift - 1)) & 1);
+  return w < 0.0 ? 0ull - t : t;
+}
+
 // Whether every row of x [batch][n][heads] starts on a multiple of `bytes`.  A
 // dimension of one element has a stride that nothing uses.
 bool rows_aligned(const kvq_rows& x, int batch, int n, int heads, size_t esize, size_t bytes) {
@@ -990,12 +1009,7 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
   for (int p = 0; p < rot_dim / 2; p++) {
     const double w = inv_freq[p];
     if (!(std::fabs(w) <= 1048576.0)) return fail(KVQ_ERR_INVALID, "inv_freq[%d] = %g is not within 2^20", p, w);
-    // 2^64 w / (2 pi) modulo 2^64, in 64-bit significands (the whole turns of
-    // a frequency above 2 pi drop out)
-    long double turns = (long double)w * 0.159154943091895335768883763372514362L;
-    if (!(turns >= 0.0L && turns < 1.0L)) turns -= floorl(turns);  // [0, 1]
-    const long double scaled = turns * 18446744073709551616.0L + 0.5L;
-    a.turn[p] = scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
+    a.turn[p] = turn_of(w);
   }
   const size_t esize = dtype == KVQ_DTYPE_F32 ? 4 : 2;
   const size_t unit = layout == KVQ_ROPE_INTERLEAVED ? 2 * esize : esize;

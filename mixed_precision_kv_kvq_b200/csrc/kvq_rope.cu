@@ -8,10 +8,10 @@
 //
 // Angles.  At position 10^6 an fp32 product m w_p is off by ~0.06 rad, so the
 // phase is kept as an integer: the host turns w_p into 2^64 w_p / (2 pi)
-// modulo 2^64, and m times that, modulo 2^64, is the fraction of a turn
-// exactly up to m 2^-65 of a turn.  Its top 32 bits become the angle in half turns, in
-// [-1, 1), for sincospif: the total error is below 2 pi 2^-26 rad (one
-// rounding to fp32) plus that function's own.
+// modulo 2^64, rounded once, and m times that, modulo 2^64, is the fraction of a
+// turn up to |m| 2^-65 of a turn, whatever the frequency.  Its top 32 bits become
+// the angle in half turns, in [-1, 1), for sincospif: 2 pi 2^-26 rad more (one
+// rounding to fp32) and that function's own error.
 //
 // The kernel is bound by HBM (each value read once and written once).  A CTA
 // takes four tokens, or one where there are few (RopeArgs::tokens_per_cta): its

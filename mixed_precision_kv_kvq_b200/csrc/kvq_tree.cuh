@@ -465,9 +465,10 @@ __device__ __forceinline__ void window_factors(uint32_t m0, uint32_t m1, uint32_
 
 // Keys of one group into 16 tensor-memory rows, 64 channels at a time.  part:
 // the group's Key part.  CHAN: per-channel groups, their (R, Z) words at kmc (the
-// cache's width): values times g; otherwise val.
-template <int BITS, bool CHAN, typename From>
-__device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t taddr, int lane) {
+// cache's width): values times g; otherwise val, or (SHARE) val times share[x], the
+// fp16 pairs of the lane's tokens g and g + 8 (key_terms).
+template <int BITS, bool CHAN, bool SHARE, typename From>
+__device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t taddr, int lane, const uint32_t* share = nullptr) {
   constexpr int kHalfWords = BITS / 2;  // words of 4 quad positions of one token
   const From unit = part + lane * unit_bytes(BITS);
 #pragma unroll
@@ -505,6 +506,10 @@ __device__ __forceinline__ void widen_keys(From part, FromRing kmc, uint32_t tad
         if constexpr (CHAN) {
           k0 = hfma2_u(k0, ra[0], za[0]);
           k1 = hfma2_u(k1, ra[1], za[1]);
+        }
+        if constexpr (SHARE) {
+          k0 = hmul2_u(k0, share[x]);
+          k1 = hmul2_u(k1, share[x]);
         }
       }
     }
@@ -830,15 +835,36 @@ __device__ __forceinline__ void draft_seen(const TreePlan& p, uint32_t (*seen)[4
 }
 
 // What a token's score needs beside val: rk for the softmax, a for the extra
-// k-step.  A range below |Z + rk| / 4000 (binary16 gives Z itself to 1 / 2048) is
-// taken as that, in a too, so that equal codes still give Z.
-__device__ __forceinline__ void key_terms(uint32_t m, float half_codes, float& rk, uint2& centre) {
+// k-step.  A range so small beside its zero that a would leave binary16
+// (|Z + rk| > 3999 rk) is taken as |Z + rk| / 3999 by both, and the Key's val counts
+// with the share of it that the true range is: rounded once more, by 2^-11 of the
+// Key's distance from its group's centre (and by 2^-25 / 3999 of |Z + rk|, below
+// what fp32 holds of that).  -> whether the range is such a one.
+__device__ __forceinline__ bool key_terms(uint32_t m, float half_codes, float& rk, uint2& centre) {
   const float r = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * half_codes;
-  const float z = __half2float(__ushort_as_half((unsigned short)(m >> 16)));
-  rk = fmaxf(r, fabsf(z) * (1.0f / (kCentreMax - 1.0f)));
-  const float a = rk > 0.f ? __fdividef(z + rk, rk) * kSumScale : 0.f;  // 2 ulp, as fine as the pair
+  const float mid = __half2float(__ushort_as_half((unsigned short)(m >> 16))) + r;
+  rk = fmaxf(r, fabsf(mid) * (1.0f / (kCentreMax - 1.0f)));
+  const float a = rk > 0.f ? __fdividef(mid, rk) * kSumScale : 0.f;  // 2 ulp, as fine as the pair
   const float hi = __half2float(__float2half_rn(a));
   centre = make_uint2(pack_h2(hi, hi), pack_h2(a - hi, 0.f));
+  return r < rk;
+}
+// A group's Keys once more, with its tokens' shares.  Few caches have such groups at
+// all, so the ordinary way writes every Key first and stays as it is (a choice before
+// it took 3-7% of a tree of 14 or 28 rows).  meta: the group's (R, Z) words.
+template <int BITS, typename From>
+__device__ __forceinline__ void share_keys(From part, From meta, float half_codes, uint32_t taddr, int lane) {
+  uint32_t sh[2];
+#pragma unroll
+  for (int x = 0; x < 2; x++) {
+    const uint32_t m = (meta + 8 * (8 * x + (lane >> 2))).u64().x;
+    const float r = __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) * half_codes;
+    float rk;
+    uint2 centre;
+    const float y = key_terms(m, half_codes, rk, centre) ? __fdividef(r, rk) : 1.0f;
+    sh[x] = pack_h2(y, y);
+  }
+  widen_keys<BITS, false, true>(part, FromRing{0}, taddr, lane, sh);
 }
 
 // Widening: Keys, then Values of buffer buf's tiles (every second one), and for
@@ -846,7 +872,9 @@ __device__ __forceinline__ void key_terms(uint32_t m, float half_codes, float& r
 // 32 w .. + 31: Keys of tokens 32 w .. + 31, Values of the channels of lane units
 // 2 w and 2 w + 1; of two groups that share a tile each takes one of the two Key
 // groups and half of the Value groups (part).
-template <int BITS, int COLS>
+// KEYS: the cache's Key groups, known here or (kAnyKeys) at run time.
+enum { kTokenKeys, kChannelKeys, kAnyKeys };
+template <int BITS, int COLS, int KEYS>
 __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_t sb, uint32_t ring, Walk wk, int buf, int part,
                                            int w, int lane) {
   using S = Split<COLS>;
@@ -855,6 +883,7 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
   const int i0 = part * kKeys, v0 = part * kValues;
   const CacheView& c = p.a.c;
   constexpr int gb = group_bytes(BITS);
+  constexpr float kHalfCodes = (float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u), kHalfCodes16 = 32768.0f / 65535.0f;
   const int t4 = lane & 3;
   const uint32_t centre_at = sb - Lay::kSmall + Lay::kCentre + buf * kCentreBytes;
   const uint32_t tk = sm.tmem + ((uint32_t)(32 * w) << 16) + S::kColK + 64 * buf;
@@ -874,28 +903,29 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
         const int tl = 32 * w + 16 * i0 + (kKeys == 2 ? lane : lane & 15);  // this lane's token (one group: twice)
         float rk = 0.f;
         uint2 centre = make_uint2(0u, 0u);
+        bool small = false;
         if (packed) {
           // groups that do not exist are read as whatever the stage holds: those rows of S are not used
           const uint32_t m = (st + (kTileGroups * gb + 8 * tl)).u32();
-          if (c.kmc) {
+          if (KEYS == kChannelKeys || (KEYS == kAnyKeys && c.kmc)) {
 #pragma unroll 1
             for (int i = i0; i < i0 + kKeys; i++)
-              widen_keys<BITS, true>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), tk + ((uint32_t)(16 * i) << 16), lane);
+              widen_keys<BITS, true, false>(st + (2 * w + i) * gb, st + kTileGroups * (gb + 128), tk + ((uint32_t)(16 * i) << 16), lane);
             rk = 1.0f / value_scale<BITS>();
           } else {
 #pragma unroll 1
             for (int i = i0; i < i0 + kKeys; i++)
-              widen_keys<BITS, false>(st + (2 * w + i) * gb, st, tk + ((uint32_t)(16 * i) << 16), lane);
-            key_terms(m, (float)(1u << (BITS - 1)) / (float)((1u << BITS) - 1u), rk, centre);
+              widen_keys<BITS, false, false>(st + (2 * w + i) * gb, st, tk + ((uint32_t)(16 * i) << 16), lane);
+            small = key_terms(m, kHalfCodes, rk, centre);
           }
         } else if (t < p.tp + p.tw) {
 #pragma unroll 1
           for (int i = i0; i < i0 + kKeys; i++) {
             const WindowGroup wg = window_group(p, wk.s, t, 2 * w + i);
-            if (wg.code) widen_keys<16, false>(FromGlobal{wg.code}, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
+            if (wg.code) widen_keys<16, false, false>(FromGlobal{wg.code}, FromRing{0}, tk + ((uint32_t)(16 * i) << 16), lane);
           }
           const WindowGroup wg = window_group(p, wk.s, t, tl >> 4);
-          if (wg.meta) key_terms(wg.meta[2 * (tl & 15)], 32768.0f / 65535.0f, rk, centre);
+          if (wg.meta) small = key_terms(wg.meta[2 * (tl & 15)], kHalfCodes16, rk, centre);
         } else {
           const int j0 = (t - p.tp - p.tw) * kTile + 32 * w, sb_ = wk.s / c.kv_heads, sh = wk.s - sb_ * c.kv_heads;
           if (c.lam_inv && lane < 4) asm volatile("prefetch.global.L1 [%0];" ::"l"(c.lam_inv + (size_t)sh * kHeadDim + 32 * lane));
@@ -923,6 +953,19 @@ __device__ __forceinline__ void widen_role(const TreePlan& p, Small& sm, uint32_
         }
         sm.rk[ct & 3][tl] = rk;
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(centre_at + narrow_at(tl)), "r"(centre.x), "r"(centre.y) : "memory");
+        if (__builtin_expect(__any_sync(0xffffffffu, small), 0)) {
+          tc_wait_st();  // the first writing of these rows
+#pragma unroll 1
+          for (int i = i0; i < i0 + kKeys; i++) {
+            const uint32_t ti = tk + ((uint32_t)(16 * i) << 16);
+            if (packed) {
+              share_keys<BITS>(st + (2 * w + i) * gb, st + (kTileGroups * gb + 128 * (2 * w + i)), kHalfCodes, ti, lane);
+            } else {
+              const WindowGroup wg = window_group(p, wk.s, t, 2 * w + i);
+              if (wg.code) share_keys<16>(FromGlobal{wg.code}, FromGlobal{reinterpret_cast<const uint8_t*>(wg.meta)}, kHalfCodes16, ti, lane);
+            }
+          }
+        }
         fence_async_smem();
         tc_wait_st();
         tc_before();
@@ -1486,7 +1529,14 @@ __global__ void __launch_bounds__(Split<COLS>::kThreads, 1) tree_kernel(const __
     if constexpr (S::kWidenRegs > S::kRegs) regs_up<S::kWidenRegs>();
     if constexpr (S::kWidenRegs < S::kRegs) regs_down<S::kWidenRegs>();
     const int group = (warp - kWiden0) >> 2, buf = group & 1, part = group >> 1, w = warp & 3;
-    widen_role<BITS, COLS>(p, sm, sb, ring_at, wk, buf, part, w, lane);
+    // One loop for both kinds of Key groups, or one each: 28 rows over 4 bits and
+    // per-channel groups 237 us and 213, 63 x 8 rows over 8 bits 491 and 503.
+    if constexpr (COLS == 64)
+      widen_role<BITS, COLS, kAnyKeys>(p, sm, sb, ring_at, wk, buf, part, w, lane);
+    else if (p.a.c.kmc)
+      widen_role<BITS, COLS, kChannelKeys>(p, sm, sb, ring_at, wk, buf, part, w, lane);
+    else
+      widen_role<BITS, COLS, kTokenKeys>(p, sm, sb, ring_at, wk, buf, part, w, lane);
   } else {
     regs_down<S::kCtlRegs>();
     if (warp == kCtl0)

@@ -44,8 +44,10 @@ def sees(mask, B, n):
 class Stream:
     """One (sequence, KV head) stream's tokens, cached ones before drafted ones, in fp64, and how each is rounded."""
 
-    def __init__(self, ks, vs, dk, dv, mode, bits, lam, narrow):
-        """ks, vs [T][128] with .centre, .range; dk, dv [n][128]; lam [128] or None."""
+    def __init__(self, ks, vs, dk, dv, mode, bits, lam, narrow, cancel=False):
+        """ks, vs [T][128] with .centre, .range; dk, dv [n][128]; lam [128] or None.  cancel: every query's channels cancel
+        exactly (sums of equal powers of two, rounded nowhere), so that a cached Key's centre adds no error to a score, and the
+        groups' ranges are small beside their zeros, so that a Key's distance from its centre is rounded, u (k - c)."""
         dev = dk.device
         T, n = ks.shape[0], dk.shape[0]
         d = lambda x: x.to(dev).double()  # noqa: E731
@@ -69,11 +71,14 @@ class Stream:
         chan = (cached[:, None] & ~(at >= T - T % 128)[:, None]) if mode == "channel" else torch.zeros_like(code16)
         drafted = ~cached[:, None]
         away = (self.k - self.kc).abs()
+        self.size = torch.where(cached[:, None], away, self.k.abs()) if cancel else self.k.abs()
         self.kerr = U16 * torch.where(chan | drafted, self.k.abs(), torch.where(code16, away, 0.0))
         self.kblock = U16 * torch.where(chan, self.kc.abs(), 0.0)
         self.blocks = (T - T % 128) // 128 if mode == "channel" else 0
         v2, c2 = self.v ** 2, vc ** 2
         self.verr2 = U16 ** 2 * (2 * v2 + c2 + torch.where(code16, 2 * (self.v - vc) ** 2, 0.0))  # p's rounding and the Value's own
+        if cancel:
+            self.kerr = torch.where(cached[:, None], U16 * away * (1 + code16), self.kerr)
         if narrow:
             self.kerr.zero_()
             self.kblock.zero_()
@@ -99,7 +104,7 @@ class Stream:
             a = w2 * e2
             return a @ self.v ** 2 - 2 * o * (a @ self.v) + o ** 2 * a.sum(1, keepdim=True)
 
-        size = abs(sm_scale) * (q.abs() @ self.k.abs().T)
+        size = abs(sm_scale) * (q.abs() @ self.size.T)
         fp32 = 2.0 ** -20 * size + 2.0 ** -21 * abs(sm_scale) * (q @ self.kc.T).abs()
         fp32 = fp32 + 2.0 ** -22 * (torch.where(vis, s, 0.0).abs() + 1.0)
         var = var + by_score(fp32 ** 2 + sm_scale ** 2 * (q ** 2 @ (self.kerr ** 2).T))
@@ -137,7 +142,7 @@ def over(err, var):
     return max(whole, float(rows.max()))
 
 
-def judge(q, dk, dv, mask, ks, vs, got, mode, bits, lam=None, sm_scale=128 ** -0.5, plant=(), streams=None):
+def judge(q, dk, dv, mask, ks, vs, got, mode, bits, lam=None, sm_scale=128 ** -0.5, plant=(), streams=None, cancel=False):
     """Check an output [B][n][Hq][128]; -> the relative root mean square error of the streams looked at.
 
     plant: pairs (tokens, times): an output that lost those tokens of each stream (cached ones first; times 0) or counted them
@@ -149,7 +154,8 @@ def judge(q, dk, dv, mask, ks, vs, got, mode, bits, lam=None, sm_scale=128 ** -0
     errs, outs = [], []
     for b, j in streams or [(b, j) for b in range(B) for j in range(H)]:
         part = lambda x: _rows(x, b, j)  # noqa: E731
-        st = Stream(part(ks), part(vs), dk[b, :, j], dv[b, :, j], mode, bits, None if lam is None else lam[j], n * G <= 8 and ks.shape[2] > 0)
+        st = Stream(part(ks), part(vs), dk[b, :, j], dv[b, :, j], mode, bits, None if lam is None else lam[j], n * G <= 8 and ks.shape[2] > 0,
+                    cancel)
         qs = [q[b, :, j * G + g].double() for g in range(G)]
         o, var = (torch.stack(x, 1) for x in zip(*(st.expect(x, seen[b], sm_scale) for x in qs)))
         err = got[b, :, j * G:(j + 1) * G].double() - o

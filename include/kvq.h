@@ -302,7 +302,9 @@ size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_node
  * reaches no other node's.  Drafted Keys (also over lambda) and Values should
  * be within binary16's range (65,504); larger ones, infinities and NaN that a
  * node does see count as some finite value of about that size or twice it.
- * |q lambda sm_scale log2(e)| should be within that range per channel, too.
+ * |q lambda sm_scale log2(e)| should be within that range per channel, too; a
+ * query that holds NaN or an infinity gives NaN in all its channels (zeros if it
+ * sees nothing).
  * q: bf16 [batch][n_nodes][q_heads][128], k, v: dtype KVQ_DTYPE_*
  * [batch][n_nodes][kv_heads][128], all as kvq_rows with 16-byte aligned rows;
  * out: device bf16 [batch][n_nodes][q_heads][128], contiguous, 16-byte

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
   constexpr int kN = kTreeNarrowRows;  // rows, and nodes
   __shared__ float sc[kN][kN];         // score, then weight, of row r and node i
   __shared__ float ml[2][kN];
+  __shared__ float nan_of[kN];         // NaN for a row whose query holds one or an infinity, else 0
   const int s = blockIdx.x, b = s / a.c.kv_heads, j = s - b * a.c.kv_heads;
   const int R = a.n * a.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -112,6 +113,9 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
         *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at);
     float q[4];
     load4(a.q, at, q, false);
+    const float z = ((q[0] + q[1]) + (q[2] + q[3])) * 0.f;
+    const bool nan = __any_sync(0xffffffffu, isnan(z));
+    if (lane == 0) nan_of[r] = nan ? __int_as_float(0x7fffffff) : 0.f;
     for (int i = 0; i < a.n; i++) {
       const bool see = a.mask ? a.mask[b * a.mask_b + (long long)node * a.n + i] != 0 : i <= node;
       float d = 0.f;
@@ -136,6 +140,7 @@ __global__ void __launch_bounds__(kHeadDim) tree_draft_kernel(const __grid_const
         sc[r][i] = w;
         l += w;
       }
+      l += nan_of[r];  // reaches the joined sum whatever this partial's weight
     }
     ml[0][r] = m;
     ml[1][r] = l;

@@ -1215,18 +1215,20 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
 #pragma unroll
       for (int i = 0; i < C / 4; i++) {
         const int rs = cb + w + 4 * i;  // row of the half's Q
-        const uint32_t h02 = sat_h2(__uint_as_float(raw[i].x << 16) * lam.x, __uint_as_float(raw[i].y << 16) * lam.z);
-        const uint32_t h13 = sat_h2(__uint_as_float(raw[i].x & 0xffff0000u) * lam.y, __uint_as_float(raw[i].y & 0xffff0000u) * lam.w);
+        const float q0 = __uint_as_float(raw[i].x << 16) * lam.x, q2 = __uint_as_float(raw[i].y << 16) * lam.z;
+        const float q1 = __uint_as_float(raw[i].x & 0xffff0000u) * lam.y, q3 = __uint_as_float(raw[i].y & 0xffff0000u) * lam.w;
+        const uint32_t h02 = sat_h2(q0, q2), h13 = sat_h2(q1, q3);
         const float2 f02 = __half22float2(*reinterpret_cast<const __half2*>(&h02));
         const float2 f13 = __half22float2(*reinterpret_cast<const __half2*>(&h13));
-        sum[i] = (f02.x + f02.y) + (f13.x + f13.y);
+        // sat_h2 makes numbers of NaN and infinities; the row's sum, and so its scores, become NaN instead
+        sum[i] = fmaf(0.f, (q0 + q2) + (q1 + q3), (f02.x + f02.y) + (f13.x + f13.y));
         *reinterpret_cast<uint2*>(qs + rs * 128 + ((((lane & 15) >> 1) ^ (rs & 7)) << 4)) = make_uint2(h02, h13);
       }
       warp_columns<C / 4, false>(sum, lane);
       constexpr int kSumLanes = 128 / C;  // lanes that end with the same row
       if (lane % kSumLanes == 0) {
         const int rs = cb + w + 4 * (lane / kSumLanes);
-        const float sc = fminf(fmaxf(sum[0] * (1.0f / kSumScale), -65504.f), 65504.f);
+        const float sc = isnan(sum[0]) ? sum[0] : fminf(fmaxf(sum[0] * (1.0f / kSumScale), -65504.f), 65504.f);
         const float hi = __half2float(__float2half_rn(sc));
         *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs)) = make_uint4(pack_h2(hi, sc - hi), pack_h2(hi, 0.f), 0u, 0u);
         *reinterpret_cast<uint4*>(sum_smem + narrow_at(rs) + 128) = make_uint4(0u, 0u, 0u, 0u);
@@ -1365,7 +1367,7 @@ __device__ __forceinline__ void softmax_role(const TreePlan& p, Small& sm, uint3
       const float* r = &sm.red[half][0][cb + tl];
       const float l = (r[0] + r[kHalfRows]) + (r[2 * kHalfRows] + r[3 * kHalfRows]);
       const float neg = sm.neg[half][cb + tl];
-      const bool any = mine > 0 && !unset(neg);
+      const bool any = mine > 0 && (!unset(neg) || isnan(l));  // a row of NaN has no maximum
       sm.ml[half][cb + tl] = make_float2(any ? -neg : -INFINITY, any ? l : 0.f);
     }
     if (mine > 0) {

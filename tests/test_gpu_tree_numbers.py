@@ -1,11 +1,11 @@
-"""Tree attention on Key groups whose zero is thousands of times their range."""
+"""Tree attention on Key groups whose zero is thousands of times their range, and on queries that are no numbers."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_operators import BF, half, kvq, tree_inputs  # noqa: F401
+from test_gpu_operators import BF, half, kvq, make_cache, tree_inputs  # noqa: F401
 from tree_accuracy import judge
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +65,30 @@ def test_small_ranges_beside_large_zeros(kvq, mode, fbit, n, G, Z, R):
         dk = dk * 2.0 ** round(math.log2(R))
     got = cache.tree_attn(0, q.to(BF), dk, dv)
     judge(q.to(BF), dk, dv, None, ks, vs, got, mode, fbit, cancel=True)
+
+
+@pytest.mark.parametrize("T", [0, 300])
+@pytest.mark.parametrize("n,G", [(4, 2), (2, 3), (4, 7), (20, 3), (40, 4)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_that_is_no_number_gives_none(kvq, T, n, G, bad):
+    """NaN or an infinity in one channel of a query: its row is NaN in every channel, whatever the path, and no other row notices;
+    a row that sees nothing is zeros as ever."""
+    cache, _, ks, vs = make_cache(kvq, "plain", 2, 2, T, 4, 512)
+    q, dk, dv = tree_inputs(9, 2, n, 2, G)
+    mask = torch.ones(n, n, dtype=torch.bool).tril()
+    mask[1] = False
+    want = cache.tree_attn(0, q, dk, dv, mask.cuda())
+    hit = torch.zeros(2, n, 2 * G, dtype=torch.bool, device="cuda")
+    hit[0, 0, 1] = hit[1, n - 1, G] = hit[1, n // 2, 0] = hit[0, 1, 0] = True
+    at = torch.arange(int(hit.sum()), device="cuda") * 37 % 128
+    worse = q.clone()
+    rows = worse[hit]
+    rows[torch.arange(len(at), device="cuda"), at] = bad
+    worse[hit] = rows
+    got = cache.tree_attn(0, worse, dk, dv, mask.cuda())
+    assert torch.equal(got[~hit], want[~hit])
+    nothing = torch.zeros_like(hit)
+    nothing[:, 1] = T == 0
+    assert got[hit & ~nothing].isnan().all()
+    assert (got[hit & nothing] == 0).all()
+    cache.device_status()

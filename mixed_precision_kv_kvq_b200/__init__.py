@@ -271,7 +271,10 @@ _LAYOUTS = {"half": KVQ_ROPE_HALF, "interleaved": KVQ_ROPE_INTERLEAVED}
 def kvq_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = KVQ_ROPE_NONE, factor: float = 1.0,
                    original_tokens: int = 0):
     """-> (inv_freq [rot_dim / 2] float64 numpy, magnitude)."""
-    inv = np.zeros(max(rot_dim, 2) // 2, np.float64)
+    for name, x in (("rot_dim", rot_dim), ("scaling", scaling), ("original_tokens", original_tokens)):
+        if not -2 ** 31 <= x < 2 ** 31:  # a C int would keep its low 32 bits
+            raise KVQError(1, f"{name} {x} is out of range")
+    inv = np.zeros(min(max(rot_dim, 2), HEAD_DIM) // 2, np.float64)
     mag = C.c_float()
     check(load().kvq_rope_freqs(rot_dim, theta, scaling, factor, original_tokens, inv.ctypes.data_as(C.c_void_p), C.byref(mag)))
     return inv, mag.value
@@ -419,6 +422,8 @@ def _read(cache, layer, start, count, k_out, v_out, ptr) -> None:
     dtype, dt, device = _dtype_code(first), first.dtype, first.device
     kr = _take("k_out", k_out, dt, device) if k_out is not None else None
     vr = _take("v_out", v_out, dt, device, first.shape) if v_out is not None else None
+    if not -2 ** 31 <= start < 2 ** 31:  # a C int would keep its low 32 bits
+        raise KVQError(1, f"tokens [{start}, {start} + {count}) are not within what layer {layer} holds")
     if first.shape[1] != count:
         raise ValueError(f"the outputs must hold {count} tokens, got {first.shape[1]}")
     check(load().kvq_read(cache, layer, start, count, dtype, kr, vr, ptr))

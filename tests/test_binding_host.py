@@ -145,3 +145,21 @@ def test_append_decode_refuses_host_tensors(kvq, cache, monkeypatch, which):
     args[which] = args[which].like
     with pytest.raises(ValueError, match="must be CUDA tensors"):
         kvq.kvq_append_decode(cache, 0, kv, kv, args[0], 0.1, args[1], args[2])
+
+
+def test_numbers_beyond_32_bits_are_refused(kvq, cache, monkeypatch):
+    """ctypes keeps the low 32 bits of what it passes as a C int: token 2^32 would be token 0."""
+    for args in ((2 ** 32 + 64,), (64, 1e4, 2 ** 32 + 1, 2.0), (64, 1e4, kvq.KVQ_ROPE_YARN, 2.0, 2 ** 32 + 4096)):
+        with pytest.raises(kvq.KVQError):
+            kvq.kvq_rope_freqs(*args)
+
+    class Lib:
+        def kvq_read(self, *args):
+            raise AssertionError("called")
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(kvq, "load", lambda: Lib())
+    monkeypatch.setattr(kvq, "kvq_dims", lambda c: (1, 2, 3))
+    for start in (2 ** 32, -2 ** 32, 2 ** 31):
+        with pytest.raises(kvq.KVQError):
+            kvq.kvq_read(cache, 0, start, 4, OnDevice1(2, 4, 3, 128), None, 77)

@@ -1,5 +1,7 @@
 """A cache over memory that holds anything: the error word and the ticket
 counters, when the first use is captured, eager, or one and then the other."""
+import gc
+
 import pytest
 import torch
 
@@ -28,6 +30,26 @@ def used_memory(kvq, byte, layers=1, B=1, H=2, fbit=4):
     return cache
 
 
+@pytest.fixture(autouse=True)
+def collected():
+    """Graphs left over in reference cycles are destroyed outside captures (a destruction inside one ends it), this module's
+    too before others capture."""
+    gc.collect()
+    yield
+    gc.collect()
+
+
+def status(call):
+    """A call's status; no exception, and so no frame with a graph in it, is kept."""
+    from mixed_precision_kv_kvq_b200 import KVQError
+
+    try:
+        call()
+    except KVQError as e:
+        return e.status
+    return 0
+
+
 def tokens(n, H=2, B=1):
     k, v = S.keys_values(3, 0, B, n, H, 0, 2)
     return k.cuda(), v.cuda()
@@ -52,9 +74,7 @@ def test_an_error_word_of_an_earlier_cache_is_not_this_ones(kvq):
         kvq.kvq_device_status(other)
     finally:
         kvq.kvq_free(other)
-    with pytest.raises(kvq.KVQError) as e:
-        cache.device_status()
-    assert e.value.status == 7
+    assert status(cache.device_status) == 7
 
 
 def test_replays_of_a_first_use_keep_an_error(kvq):
@@ -73,9 +93,7 @@ def test_replays_of_a_first_use_keep_an_error(kvq):
     kvq.kvq_selftest_timeout(cache.handle)
     graph.replay()
     torch.cuda.synchronize()
-    with pytest.raises(kvq.KVQError) as e:
-        cache.device_status()
-    assert e.value.status == 7
+    assert status(cache.device_status) == 7
     graph.replay()
     cache.device_status()
     assert torch.isfinite(tree).all() and (tree != 0).any()

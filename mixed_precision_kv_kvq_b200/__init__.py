@@ -56,19 +56,22 @@ class _Handle(C.c_void_p):
     dims = None
 
 
-def _check_cache(cache, **tensors) -> None:
-    """That [batch][n][heads][128] tensors have the cache's batch and KV heads: the kernels go by the cache's."""
+def _check_cache(cache, k, v, names=("k", "v")) -> None:
+    """That [batch][n][heads][128] tensors (or None) have the cache's batch and KV heads: the kernels go by the cache's."""
     _, batch, heads = getattr(cache, "dims", None) or kvq_dims(cache)
-    for name, t in tensors.items():
-        if t is not None and (t.dim() != 4 or t.shape[0] != batch or t.shape[2] != heads):
-            raise ValueError(f"{name} must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(t.shape)}")
+    for t in (k, v):
+        if t is not None:
+            s = t.shape
+            if len(s) != 4 or s[0] != batch or s[2] != heads:
+                raise ValueError(f"{names[t is not k]} must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(s)}")
 
 
 def _check_queries(cache, q: torch.Tensor, workspace: Optional[torch.Tensor] = None) -> None:
     """The same of [batch][q_heads][128] queries, and a workspace whose bytes neighbour."""
     batch = (getattr(cache, "dims", None) or kvq_dims(cache))[1]
-    if q.dim() != 3 or q.shape[0] != batch:
-        raise ValueError(f"q must be [{batch}][q_heads][{HEAD_DIM}], got {list(q.shape)}")
+    s = q.shape
+    if len(s) != 3 or s[0] != batch:
+        raise ValueError(f"q must be [{batch}][q_heads][{HEAD_DIM}], got {list(s)}")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
 
@@ -116,7 +119,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def kvq_append(cache, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """k, v: device [batch][n][kv_heads][128], bf16 or fp32, contiguous."""
-    _check_cache(cache, k=k, v=v)
+    _check_cache(cache, k, v)
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[-1] != HEAD_DIM:
         raise ValueError("k and v must both be [batch][n][kv_heads][128] of one dtype")
     if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
@@ -157,7 +160,7 @@ def kvq_append_decode(cache, layer: int, k: torch.Tensor, v: torch.Tensor, q: to
                       out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """One decode step in one launch: append k, v (device [batch][1][kv_heads][128])
     then attend with q (device bf16 [batch][q_heads][128]) into out (fp32)."""
-    _check_cache(cache, k=k, v=v)
+    _check_cache(cache, k, v)
     _check_queries(cache, q, workspace)
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[1] != 1 or k.shape[-1] != HEAD_DIM:
         raise ValueError("k and v must both be [batch][1][kv_heads][128] of one dtype")
@@ -370,7 +373,7 @@ def kvq_tree_attn(cache, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.
     """q: device bf16 [batch][n][q_heads][128]; k, v: device [batch][n][kv_heads][128], bf16 or fp32 (strided views
     allowed); mask: device bool or uint8 [batch][n][n] or [n][n] (contiguous), None: a chain; out: contiguous bf16,
     shaped like q."""
-    _check_cache(cache, k=k, v=v)
+    _check_cache(cache, k, v)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     with _On(q.device, stream) as on:
@@ -409,7 +412,7 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
     first = k_out if k_out is not None else v_out
     if first is None:
         raise ValueError("k_out and v_out are both None")
-    _check_cache(cache, k_out=k_out, v_out=v_out)
+    _check_cache(cache, k_out, v_out, ("k_out", "v_out"))
     if not first.is_cuda:
         raise ValueError("k_out and v_out must be CUDA tensors")
     with _On(first.device, stream) as on:
@@ -604,7 +607,7 @@ class KVQCache:
         device = self.pool.device
         if q.dim() != 4 or q.shape[0] != self.batch or q.device != device:
             raise ValueError(f"q must be [{self.batch}][n][q_heads][128] on {device}, got {list(q.shape)} on {q.device}")
-        _check_cache(self.handle, k=k, v=v)
+        _check_cache(self.handle, k, v)
         with _On(device, stream) as on:
             # the workspace belongs to this call alone: calls on other streams and captured graphs have their own
             size = (q.shape[2], q.shape[1])
@@ -635,7 +638,7 @@ class KVQCache:
                 k_out = on.empty(shape, dtype)
                 v_out = on.like(k_out)
             else:
-                _check_cache(self.handle, k_out=k_out, v_out=v_out)
+                _check_cache(self.handle, k_out, v_out, ("k_out", "v_out"))
                 for name, x in (("k_out", k_out), ("v_out", v_out)):
                     if x is not None and x.device != device:
                         raise ValueError(f"{name} must be on the cache's device {device}, got {x.device}")

@@ -66,14 +66,32 @@ def _check_cache(cache, k, v, names=("k", "v")) -> None:
                 raise ValueError(f"{names[t is not k]} must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(s)}")
 
 
-def _check_queries(cache, q: torch.Tensor, workspace: Optional[torch.Tensor] = None) -> None:
-    """The same of [batch][q_heads][128] queries, and a workspace whose bytes neighbour."""
+def _check_queries(cache, q: torch.Tensor, out: torch.Tensor, workspace: Optional[torch.Tensor] = None) -> int:
+    """The same of [batch][q_heads][128] queries, with an output like them and a workspace whose bytes neighbour.  -> q_heads"""
     batch = (getattr(cache, "dims", None) or kvq_dims(cache))[1]
     s = q.shape
     if len(s) != 3 or s[0] != batch:
         raise ValueError(f"q must be [{batch}][q_heads][{HEAD_DIM}], got {list(s)}")
+    if q.dtype is not torch.bfloat16 or s[2] != HEAD_DIM or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
+    if out.dtype is not torch.float32 or out.shape != s or not out.is_contiguous():
+        raise ValueError("out must be a contiguous fp32 tensor shaped like q")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    return s[1]
+
+
+def _check_tokens(cache, k: torch.Tensor, v: torch.Tensor, one: bool) -> int:
+    """The same of contiguous Keys and Values alike, of one token a sequence if `one`.  -> tokens a sequence"""
+    _, batch, heads = getattr(cache, "dims", None) or kvq_dims(cache)
+    s = k.shape
+    if len(s) != 4 or s[0] != batch or s[2] != heads:
+        raise ValueError(f"k must be [{batch}][n][{heads}][{HEAD_DIM}], got {list(s)}")
+    if v.shape != s or k.dtype is not v.dtype or s[3] != HEAD_DIM or (one and s[1] != 1):
+        raise ValueError(f"k and v must both be [batch][{1 if one else 'n'}][kv_heads][128] of one dtype")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k and v must be contiguous")
+    return s[1]
 
 
 # ---------------------------------------------------------------- C ABI mirror
@@ -119,13 +137,10 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def kvq_append(cache, layer: int, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """k, v: device [batch][n][kv_heads][128], bf16 or fp32, contiguous."""
-    _check_cache(cache, k, v)
-    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[-1] != HEAD_DIM:
-        raise ValueError("k and v must both be [batch][n][kv_heads][128] of one dtype")
-    if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
-        raise ValueError("k and v must be contiguous CUDA tensors")
-    check(load().kvq_append(cache, layer, _dptr(k), _dptr(v), _dtype_code(k), k.shape[1],
-                            _stream_ptr(stream)))
+    n = _check_tokens(cache, k, v, False)
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("k and v must be CUDA tensors")
+    check(load().kvq_append(cache, layer, _dptr(k), _dptr(v), _dtype_code(k), n, _stream_ptr(stream)))
 
 
 def kvq_shrink(cache, layer: int, stream=None) -> None:
@@ -144,15 +159,11 @@ def kvq_decode_workspace(cache, layer: int, q_heads: int) -> int:
 def kvq_decode_attn(cache, layer: int, q: torch.Tensor, sm_scale: float, out: torch.Tensor,
                     workspace: torch.Tensor, stream=None) -> None:
     """q: device bf16 [batch][q_heads][128]; out: device fp32, same shape."""
-    _check_queries(cache, q, workspace)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[-1] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
-    if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous fp32 tensor shaped like q")
+    heads = _check_queries(cache, q, out, workspace)
     if not (q.is_cuda and out.is_cuda and workspace.is_cuda):
         raise ValueError("q, out and workspace must be CUDA tensors")
     ws_bytes = workspace.numel() * workspace.element_size()
-    check(load().kvq_decode_attn(cache, layer, _dptr(q), q.shape[1], float(sm_scale), _dptr(out),
+    check(load().kvq_decode_attn(cache, layer, _dptr(q), heads, float(sm_scale), _dptr(out),
                                  _dptr(workspace), ws_bytes, _stream_ptr(stream)))
 
 
@@ -160,20 +171,12 @@ def kvq_append_decode(cache, layer: int, k: torch.Tensor, v: torch.Tensor, q: to
                       out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """One decode step in one launch: append k, v (device [batch][1][kv_heads][128])
     then attend with q (device bf16 [batch][q_heads][128]) into out (fp32)."""
-    _check_cache(cache, k, v)
-    _check_queries(cache, q, workspace)
-    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 4 or k.shape[1] != 1 or k.shape[-1] != HEAD_DIM:
-        raise ValueError("k and v must both be [batch][1][kv_heads][128] of one dtype")
-    if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
-        raise ValueError("k and v must be contiguous CUDA tensors")
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[-1] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
-    if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous fp32 tensor shaped like q")
-    if not (q.is_cuda and out.is_cuda and workspace.is_cuda):
-        raise ValueError("q, out and workspace must be CUDA tensors")
+    _check_tokens(cache, k, v, True)
+    heads = _check_queries(cache, q, out, workspace)
+    if not (k.is_cuda and v.is_cuda and q.is_cuda and out.is_cuda and workspace.is_cuda):
+        raise ValueError("k, v, q, out and workspace must be CUDA tensors")
     ws_bytes = workspace.numel() * workspace.element_size()
-    check(load().kvq_append_decode(cache, layer, _dptr(k), _dptr(v), _dtype_code(k), _dptr(q), q.shape[1],
+    check(load().kvq_append_decode(cache, layer, _dptr(k), _dptr(v), _dtype_code(k), _dptr(q), heads,
                                    float(sm_scale), _dptr(out), _dptr(workspace), ws_bytes, _stream_ptr(stream)))
 
 
@@ -183,14 +186,10 @@ def kvq_decode_attn_noalloc(cache, layer: int, q: torch.Tensor, sm_scale: float,
     device memory where they run decode.  The library's own fixed 24 MiB
     scratch buffer (one per GPU, kept until exit) holds the split partials;
     calls that can overlap on the GPU share it and must be serialised."""
-    _check_queries(cache, q)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[-1] != HEAD_DIM or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 [batch][q_heads][128] tensor")
-    if out.dtype != torch.float32 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous fp32 tensor shaped like q")
+    heads = _check_queries(cache, q, out)
     if not (q.is_cuda and out.is_cuda):
         raise ValueError("q and out must be CUDA tensors")
-    check(load().kvq_decode_attn_noalloc(cache, layer, _dptr(q), q.shape[1], float(sm_scale), _dptr(out),
+    check(load().kvq_decode_attn_noalloc(cache, layer, _dptr(q), heads, float(sm_scale), _dptr(out),
                                          _stream_ptr(stream)))
 
 

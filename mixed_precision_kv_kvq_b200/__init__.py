@@ -278,7 +278,7 @@ def kvq_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = KVQ_ROPE
             raise KVQError(1, f"{name} {x} is out of range")
     inv = np.zeros(min(max(rot_dim, 2), HEAD_DIM) // 2, np.float64)
     mag = C.c_float()
-    check(load().kvq_rope_freqs(rot_dim, theta, scaling, factor, original_tokens, inv.ctypes.data_as(C.c_void_p), C.byref(mag)))
+    check(load().kvq_rope_freqs(int(rot_dim), float(theta), int(scaling), float(factor), int(original_tokens), inv.ctypes.data_as(C.c_void_p), C.byref(mag)))
     return inv, mag.value
 
 
@@ -400,7 +400,7 @@ def _tree_attn(cache, layer, q, k, v, mask, sm_scale, out, workspace, ptr) -> No
         elif ms != (n, n):
             raise ValueError(f"mask must be [{b}][{n}][{n}] or [{n}][{n}], got {list(ms)}")
         mask_ptr = mask.data_ptr()
-    check(load().kvq_tree_attn(cache, layer, qr, q_heads, n, kr, vr, dtype, mask_ptr, mask_b, sm_scale,
+    check(load().kvq_tree_attn(cache, layer, qr, q_heads, n, kr, vr, dtype, mask_ptr, mask_b, float(sm_scale),
                                out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), ptr))
 
 
@@ -421,6 +421,7 @@ def kvq_read(cache, layer: int, start: int, count: int, k_out: Optional[torch.Te
 def _read(cache, layer, start, count, k_out, v_out, ptr) -> None:
     """kvq_read with outputs of the cache's shape and their device current, on the stream handle ptr."""
     first = k_out if k_out is not None else v_out
+    start, count = int(start), int(count)
     dtype, dt, device = _dtype_code(first), first.dtype, first.device
     kr = _take("k_out", k_out, dt, device) if k_out is not None else None
     vr = _take("v_out", v_out, dt, device, first.shape) if v_out is not None else None

@@ -163,3 +163,33 @@ def test_numbers_beyond_32_bits_are_refused(kvq, cache, monkeypatch):
     for start in (2 ** 32, -2 ** 32, 2 ** 31):
         with pytest.raises(kvq.KVQError):
             kvq.kvq_read(cache, 0, start, 4, OnDevice1(2, 4, 3, 128), None, 77)
+
+
+def test_numbers_of_other_types(kvq, cache, monkeypatch):
+    """numpy's and torch's scalars are numbers, as for append and decode."""
+    import numpy as np
+
+    inv, mag = kvq.kvq_rope_freqs(np.int64(64), np.float32(10000.0), kvq.KVQ_ROPE_YARN, torch.tensor(4.0), np.int32(4096))
+    want = kvq.kvq_rope_freqs(64, 10000.0, kvq.KVQ_ROPE_YARN, 4.0, 4096)
+    assert np.array_equal(inv, want[0]) and mag == want[1]
+    calls = []
+
+    class Lib:
+        def kvq_read(self, *args):
+            calls.append(args[2:4])
+            return 0
+
+        def kvq_tree_attn(self, *args):
+            calls.append(args[10])
+            return 0
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(kvq, "load", lambda: Lib())
+    monkeypatch.setattr(kvq, "kvq_dims", lambda c: (1, 2, 3))
+    k = OnDevice1(2, 4, 3, 128)
+    kvq.kvq_read(cache, 0, np.int64(7), torch.tensor(4), k, None, 77)
+    for scale in (np.float32(0.5), torch.tensor(0.5), 0.5):
+        kvq.kvq_tree_attn(cache, 0, OnDevice1(2, 4, 6, 128), k, k, None, scale, OnDevice1(2, 4, 6, 128),
+                          OnDevice1(1 << 16, dtype=torch.uint8), 77)
+    assert calls == [(7, 4), 0.5, 0.5, 0.5] and all(type(x) in (tuple, float) for x in calls)
+    assert all(type(x) is int for x in calls[0])

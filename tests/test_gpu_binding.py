@@ -92,3 +92,64 @@ def test_strides_of_single_elements_are_free(kvq, dtype, B, n, H, dims):
         out = torch.zeros_like(k)
         assert torch.equal(kvq.kvq_rope(rope, pos, odd(k, *dims), odd(v, *dims), q_out=odd(out, *dims))[0], want[0])
         assert torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("T", [0, 300, 2900])
+@pytest.mark.parametrize("n,G", [(1, 7), (4, 2), (4, 7), (16, 7), (40, 7)])
+def test_tree_into_its_own_queries(kvq, T, n, G):
+    """out may be q itself: rows cut over several CTAs, rows of one, and the path of up to 8 rows; eager and replayed."""
+    B, H = 2, 2
+    cache = kvq.KVQCache(1, B, H, 4096 * B * H * 2 * (16 * 4 + 4), [4])
+    if T:
+        k, v = S.keys_values(5, 0, B, T, H, 0, 2)
+        cache.append(0, k.cuda(), v.cuda())
+    q, k, v = rand(1, B, n, H * G, 128), rand(2, B, n, H, 128), rand(3, B, n, H, 128)
+    want = cache.tree_attn(0, q, k, v)
+    for _ in range(5):
+        own = q.clone()
+        assert cache.tree_attn(0, own, k, v, out=own) is own
+        assert torch.equal(own, want)
+    own = q.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.tree_attn(0, own, k, v, out=own)
+    for _ in range(3):
+        own.copy_(q)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(own, want)
+
+
+@pytest.mark.parametrize("n,G", [(1, 7), (4, 7), (16, 7)])
+def test_tree_of_broadcast_queries_and_drafts(kvq, n, G):
+    """Every sequence drafts the same tokens: q, k and v expanded over the batch, as copies of them."""
+    B, H = 3, 2
+    cache = filled(kvq, B, H)
+    q, k, v = (rand(i, 1, n, h, 128).expand(B, n, h, 128) for i, h in ((1, H * G), (2, H), (3, H)))
+    assert torch.equal(cache.tree_attn(0, q, k, v), cache.tree_attn(0, q.contiguous(), k.contiguous(), v.contiguous()))
+    rope, pos = kvq.Rope(128), torch.arange(n, device="cuda")
+    a, b = kvq.kvq_rope(rope, pos, q, k), kvq.kvq_rope(rope, pos[None].expand(B, n), q.contiguous(), k.contiguous())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("mode", [{}, {"sink_window": True}, {"key_channel": True}])
+def test_calls_at_once_on_several_streams(kvq, mode):
+    """Reading, both tree paths and a rotation run at once on streams of their own, over a cache that none of them changes."""
+    B, H = 2, 2
+    cache = kvq.KVQCache(1, B, H, 4096 * B * H * 2 * (16 * 2 + 4), [2], **mode)
+    k, v = S.keys_values(5, 0, B, 3000, H, 0, 2)
+    cache.append(0, k.cuda(), v.cuda())
+    rope, pos = kvq.Rope(128), torch.arange(12, device="cuda")
+    q, dk, dv = rand(1, B, 12, 2 * 7, 128), rand(2, B, 12, H, 128), rand(3, B, 12, H, 128)
+    calls = [lambda s: cache.read(0, 100, 2500, stream=s), lambda s: (cache.tree_attn(0, q, dk, dv, stream=s),),
+             lambda s: (cache.tree_attn(0, q[:, :1], dk[:, :1], dv[:, :1], stream=s),), lambda s: kvq.kvq_rope(rope, pos, q, dk, stream=s)]
+    want = [c(None) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[c(s) for c, s in zip(calls, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for row in got:
+        for a, b in zip(row, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    cache.device_status()

@@ -286,7 +286,8 @@ kvq_status kvq_rope(int rot_dim, int layout, const double* inv_freq, float magni
 size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_nodes);
 
 /* Attention of n_nodes drafted tokens per sequence over the block's cache and
- * over one another, in one pass over the packed cache:
+ * over one another, reading the packed cache once for every 128 query rows of a
+ * KV head (n_nodes times its query heads):
  *   out[b][i][h] = sum_x w_x v_x,  w = softmax over
  *     every cached token t:              sm_scale (q[b][i][h] * lambda) . k^_t
  *     every drafted token j seen by i:   sm_scale q[b][i][h] . k[b][j][h']
@@ -308,7 +309,7 @@ size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_node
  * q: bf16 [batch][n_nodes][q_heads][128], k, v: dtype KVQ_DTYPE_*
  * [batch][n_nodes][kv_heads][128], all as kvq_rows with 16-byte aligned rows;
  * out: device bf16 [batch][n_nodes][q_heads][128], contiguous, 16-byte
- * aligned.  Scores and sums are fp32; products take operands rounded to
+ * aligned; it may be q itself, other overlaps give unspecified values.  Scores and sums are fp32; products take operands rounded to
  * binary16 (codes of 8 bits and fewer are exact, and a Key's range and zero
  * are applied in fp32; with per-channel Key groups the Key is rounded, and in
  * groups whose zero is 4000 times their range its distance from the centre).

@@ -1105,8 +1105,14 @@ kvq_status kvq_tree_attn(kvq_cache* c, int layer, const kvq_rows* q, int q_heads
   const int rows = n_nodes * G;
   // Few rows over a cache that holds tokens: the decode kernel reads it (one of
   // its eight query columns a row), with the drafted tokens as one more partial
-  // of each stream.  One node of 7 heads over 32K 4-bit tokens takes 59 us so and
-  // 120 us through the tree kernel, whose tiles cost the same for 1 to 16 rows.
+  // of each stream; the tree kernel's tiles cost the same for 1 to 16 rows.
+  // Measured both ways (16 x 4 streams, us so / through the tree kernel): one node
+  // of 7 heads over 32K tokens at 2, 4, 8 bits 52 / 123, 59 / 121, 100 / 140 and over
+  // 16K at 16 bits 159 / 175; over 1K 18 / 26, 18 / 26, 19 / 26 and 26 / 29; with the
+  // window at 4 bits 67 / 128 and 24 / 29, with per-channel Keys 88 / 190 and 27 / 28.
+  // Eight nodes of one head, whose drafted partial takes longest, 66 / 121 over 32K
+  // and 26 / 26 over 1K 4-bit tokens, but 34 / 29 over 1K 16-bit ones: that and 1K
+  // 16-bit tokens with per-channel Keys (35 / 31) are where the other way is faster.
   if (rows <= kTreeNarrowRows && a.c.n_prog + a.c.n_win > 0) {
     const int n_streams = c->batch * c->kv_heads;
     DecodePlan d = plan_decode(c, L);

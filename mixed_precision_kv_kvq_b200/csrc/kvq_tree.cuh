@@ -63,17 +63,20 @@
 // partial (max, sum, O) of at most two others in the workspace, which
 // tree_merge_kernel joins.
 //
-// Measured on a B200 (graph replay, inputs larger than L2): 16 nodes of 7 heads
-// over 16 x 32768 2-bit tokens of 4 heads 207 us, 580 TFLOP/s; 63 nodes of 8 heads
-// over 8 x 16383 8-bit tokens of 8 heads 429 us, 633 TFLOP/s; 5 nodes of 5 heads
-// over 4 x 4999 16-bit tokens of 8 heads 52 us, 1.6 TB/s; one tile a CTA 14 us
-// (query set-up, cold instructions, the drafted tile's scattered loads).
+// Every block of up to 128 rows streams and widens the stream's cache again.
+// Measured on a B200 (graph replay): 16 nodes of 7 heads over 16 x 32768 2-bit
+// tokens of 4 heads 206 us, 585 TFLOP/s; 63 nodes of 8 heads over 8 x 16383 8-bit
+// tokens of 8 heads 439 us, 620 TFLOP/s (four blocks of rows; 495 us in a run of
+// many, under the power cap); 4 nodes of 7 heads over 16 x 32701 4-bit tokens of 4
+// heads 158 us; 5 nodes of 5 heads over 4 x 4999 16-bit tokens of 8 heads 50 us, 1.7
+// TB/s (84 MB, of which L2 may hold a part from one replay to the next); one tile
+// a CTA 14 us (query set-up, cold instructions, the drafted tile's scattered loads).
 // A 128 x 128 tile takes ~2700 cycles, against ~1300 of MMA and 1024 of ex2 at
 // 16 an SM and cycle.  A half's loop is its score product (~1800 cycles from its
 // issue until it is in, the other half's products between), 220 until it is in
 // registers and S is free, and ~500 until the next is issued; S is single, as
-// tensor memory is full.  (S held until the maxima were agreed on: 220 and 456
-// us.)  Widening hides behind it: without any, 16 nodes took 208 us of 220.
+// tensor memory is full.  (S held until the maxima were agreed on: 220 us where it
+// is 206; of those 220, 208 were left without any widening at all.)
 // At 16 bits a tile is 64 KiB and two ring stages are what fits.  Every wait is bounded: a wait that gives up raises
 // the cache's error flag and the CTA's abort flag, after which all waits return
 // at once and the loops run out.

@@ -313,6 +313,9 @@ size_t kvq_tree_workspace(const kvq_cache* c, int layer, int q_heads, int n_node
  * binary16 (codes of 8 bits and fewer are exact, and a Key's range and zero
  * are applied in fp32; with per-channel Key groups the Key is rounded, and in
  * groups whose zero is 4000 times their range its distance from the centre).
+ * Up to 8 query rows a KV head over a block that holds tokens go through the
+ * decode kernel, whose roundings differ: the same node's output in a larger
+ * tree may differ by about a bf16 rounding.
  * 1 <= n_nodes <= 1024; q_heads as in kvq_decode_attn.  workspace: as there,
  * kvq_tree_workspace(c, layer, q_heads, n_nodes) bytes, 16-byte aligned; it
  * is all that calls share, so calls with workspaces of their own may overlap

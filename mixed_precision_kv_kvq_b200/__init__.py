@@ -524,8 +524,9 @@ class KVQCache:
 
     The device pool is a torch uint8 tensor sized by kvq_pool_bytes; the
     decode workspace is a torch tensor sized by kvq_decode_workspace.
-    Host (CPU) inputs are copied to the device on the current stream before
-    the call (pinned memory makes the copy asynchronous)."""
+    Host (CPU) inputs of append, decode_attn and append_decode are copied to
+    the device on the current stream before the call (pinned memory makes the
+    copy asynchronous); tree_attn and read take device tensors."""
 
     def __init__(self, layers: int, batch: int, kv_heads: int, budget_bytes: int,
                  fbit: Sequence[int], head_dim: int = HEAD_DIM, device=None, sink_window: bool = False,

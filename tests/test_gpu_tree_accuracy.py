@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from test_gpu_operators import BF, F32, held, kvq, make_cache, randn, tree_inputs, tree_mask  # noqa: F401
-from tree_accuracy import judge
+from tree_accuracy import check_rms
 
 pytestmark = pytest.mark.gpu
 
@@ -32,7 +32,7 @@ def test_near_equal_weights(kvq, mode, fbit, n, G):
     got = cache.tree_attn(0, q, dk, dv, None if mask is None else mask.cuda())
     assert torch.equal(got, cache.tree_attn(0, q, dk, dv, None if mask is None else mask.cuda()))
     plant = spans(T + n, (0, 16), (16 * 61, 16), (T - 20, 16), (T - 4, 4), (1024, 128), (T, n))
-    print("relative rms error", mode, fbit, n * G, judge(q, dk, dv, mask, ks, vs, got, mode, fbit, lam, plant=plant))
+    print("relative rms error", mode, fbit, n * G, check_rms(q, dk, dv, mask, ks, vs, got, mode, fbit, lam, plant=plant))
 
 
 @pytest.mark.parametrize("mode", MODES)
@@ -45,7 +45,7 @@ def test_near_equal_weights_of_wide_trees(kvq, mode):
     mask = torch.rand(B, n, n, generator=torch.Generator().manual_seed(1)) < 0.7
     got = cache.tree_attn(0, q, dk, dv, mask.cuda())
     plant = spans(T + n, (0, 16), (336, 16), (512, 128), (T, 16), (T + 112, 16), (T + 128, 16), (T + n - 6, 6))
-    judge(q, dk, dv, mask, ks, vs, got, mode, 2, lam, plant=plant)
+    check_rms(q, dk, dv, mask, ks, vs, got, mode, 2, lam, plant=plant)
 
 
 @pytest.mark.parametrize("fbit", WIDTHS)
@@ -62,7 +62,7 @@ def test_every_share_of_many_tiles(kvq, fbit, n, G):
     got = cache.tree_attn(0, q, dk, dv)
     plant = spans(T + n, (0, 16), (2048, 16), (T - 20, 16), (1024, 128), (T, n))
     streams = [(0, 0), (0, 1), (3, 2), (7, 3), (11, 1), (15, 3)]
-    judge(q, dk, dv, None, ks, vs, got, "plain", fbit, plant=plant, streams=streams)
+    check_rms(q, dk, dv, None, ks, vs, got, "plain", fbit, plant=plant, streams=streams)
 
 
 @pytest.mark.parametrize("mode", MODES)
@@ -75,7 +75,7 @@ def test_loud_channels(kvq, mode, fbit, n, G, lam):
     cache, scale, ks, vs = make_cache(kvq, mode, B, H, T, fbit, 2048, lam=lam)
     q, dk, dv = tree_inputs(7 * n, B, n, H, G, F32 if n == 2 else BF)
     got = cache.tree_attn(0, q, dk, dv)
-    print("relative rms error", mode, fbit, n * G, lam, judge(q, dk, dv, None, ks, vs, got, mode, fbit, scale))
+    print("relative rms error", mode, fbit, n * G, lam, check_rms(q, dk, dv, None, ks, vs, got, mode, fbit, scale))
 
 
 def hadamard():
@@ -120,13 +120,13 @@ def test_chosen_tokens(kvq, mode, fbit, n, G):
     got = cache.tree_attn(0, q, dk, dv, mask.cuda())
     used = at[:min(len(at), 3 * n * G)]
     plant = spans(T + n, *((t, 1) for t in used), (T, 1)) + spans(T + n, *((T + j, 1) for j in range(1, min(n, 4))))
-    rel = judge(q, dk, dv, mask, ks, vs, got, mode, fbit, plant=plant)
+    rel = check_rms(q, dk, dv, mask, ks, vs, got, mode, fbit, plant=plant)
     print("relative rms error", mode, fbit, n * G, rel)
     shared = mask[0].cuda()
     one = cache.tree_attn(0, q, dk, dv, shared)
-    judge(q, dk, dv, mask[0], ks, vs, one, mode, fbit)
+    check_rms(q, dk, dv, mask[0], ks, vs, one, mode, fbit)
     if n > 2:  # the check tells masks of other sequences and the other way round apart
         for other in (mask.flip(0), mask.transpose(1, 2)):
             if not torch.equal(other, mask):
                 with pytest.raises(AssertionError):
-                    judge(q, dk, dv, other, ks, vs, got, mode, fbit)
+                    check_rms(q, dk, dv, other, ks, vs, got, mode, fbit)

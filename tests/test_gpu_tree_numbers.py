@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from test_gpu_operators import BF, half, kvq, make_cache, tree_inputs  # noqa: F401
-from tree_accuracy import judge
+from tree_accuracy import check_rms
 
 pytestmark = pytest.mark.gpu
 
@@ -64,7 +64,7 @@ def test_small_ranges_beside_large_zeros(kvq, mode, fbit, n, G, Z, R):
         q = q * 2.0 ** round(math.log2(3.0 / (R * 0.29)))
         dk = dk * 2.0 ** round(math.log2(R))
     got = cache.tree_attn(0, q.to(BF), dk, dv)
-    judge(q.to(BF), dk, dv, None, ks, vs, got, mode, fbit, cancel=True)
+    check_rms(q.to(BF), dk, dv, None, ks, vs, got, mode, fbit, cancel=True)
 
 
 @pytest.mark.parametrize("T", [0, 300])

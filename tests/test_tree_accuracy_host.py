@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from tree_accuracy import judge, over
+from tree_accuracy import check_rms, over
 
 MODES = ["plain", "window", "channel"]
 
@@ -88,7 +88,7 @@ def test_roundings_pass(mode, bits, n, G, what, scale):
     ks, vs = cache(mode, bits, 700)
     q, dk, dv = inputs(1, n, G, scale)
     got = rounded(q, dk, dv, ks, vs, torch.ones(n, n, dtype=torch.bool).tril())
-    judge(q, dk, dv, None, ks, vs, got, mode, bits)
+    check_rms(q, dk, dv, None, ks, vs, got, mode, bits)
 
 
 @pytest.mark.parametrize("mode", MODES)
@@ -103,7 +103,7 @@ def test_lost_and_doubled_tokens_fail(mode, bits):
     plants = [((every >= a) & (every < a + size), times) for a, size in ((0, 16), (T // 2, 16), (T - 16, 16), (2048, 128), (T, n))
               for times in (0.0, 2.0)]
     got = rounded(q, dk, dv, ks, vs, seen)
-    judge(q, dk, dv, None, ks, vs, got, mode, bits, plant=plants)
+    check_rms(q, dk, dv, None, ks, vs, got, mode, bits, plant=plants)
     for tokens, times in plants:
 
         def spoil(p, v):
@@ -112,10 +112,10 @@ def test_lost_and_doubled_tokens_fail(mode, bits):
             return p, v
 
         with pytest.raises(AssertionError):
-            judge(q, dk, dv, None, ks, vs, rounded(q, dk, dv, ks, vs, seen, spoil), mode, bits)
+            check_rms(q, dk, dv, None, ks, vs, rounded(q, dk, dv, ks, vs, seen, spoil), mode, bits)
     for factor in (0.0, 0.99, 1.01, 1.1):
         with pytest.raises(AssertionError):
-            judge(q, dk, dv, None, ks, vs, (got.double() * factor).bfloat16(), mode, bits)
+            check_rms(q, dk, dv, None, ks, vs, (got.double() * factor).bfloat16(), mode, bits)
 
 
 def test_wrong_masks_scores_and_heads_fail():
@@ -123,17 +123,17 @@ def test_wrong_masks_scores_and_heads_fail():
     q, dk, dv = inputs(1, 5, 2, 1.0)
     seen = torch.ones(5, 5, dtype=torch.bool).tril()
     got = rounded(q, dk, dv, ks, vs, seen)
-    judge(q, dk, dv, None, ks, vs, got, "plain", 4)
+    check_rms(q, dk, dv, None, ks, vs, got, "plain", 4)
     with pytest.raises(AssertionError):
-        judge(q, dk, dv, None, ks, vs, rounded((q.float() * 0.98).bfloat16(), dk, dv, ks, vs, seen), "plain", 4)
+        check_rms(q, dk, dv, None, ks, vs, rounded((q.float() * 0.98).bfloat16(), dk, dv, ks, vs, seen), "plain", 4)
     with pytest.raises(AssertionError):
-        judge(q, dk, dv, None, ks, vs, got.flip(2), "plain", 4)
+        check_rms(q, dk, dv, None, ks, vs, got.flip(2), "plain", 4)
     # drafted Keys as loud as the cached ones, so that what a row sees of them matters
     dk = (dk.float() * 20.0).bfloat16()
     got = rounded(q, dk, dv, ks, vs, seen)
-    judge(q, dk, dv, None, ks, vs, got, "plain", 4)
+    check_rms(q, dk, dv, None, ks, vs, got, "plain", 4)
     with pytest.raises(AssertionError):
-        judge(q, dk, dv, seen.T, ks, vs, got, "plain", 4)
+        check_rms(q, dk, dv, seen.T, ks, vs, got, "plain", 4)
 
 
 def test_limits():

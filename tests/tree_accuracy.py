@@ -142,7 +142,7 @@ def over(err, var):
     return max(whole, float(rows.max()))
 
 
-def judge(q, dk, dv, mask, ks, vs, got, mode, bits, lam=None, sm_scale=128 ** -0.5, plant=(), streams=None, cancel=False):
+def check_rms(q, dk, dv, mask, ks, vs, got, mode, bits, lam=None, sm_scale=128 ** -0.5, plant=(), streams=None, cancel=False):
     """Check an output [B][n][Hq][128]; -> the relative root mean square error of the streams looked at.
 
     plant: pairs (tokens, times): an output that lost those tokens of each stream (cached ones first; times 0) or counted them
